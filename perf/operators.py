@@ -269,7 +269,7 @@ def prepare(case, seed):
     if own:
         from speculative_decoding_verification_86_b200 import binding
         st["cache"] = binding.BlockCache(dev, heads_q=case.get("hq", hkv), heads_kv=hkv, head_dim=d,
-                                         page_size=page, max_batch=B, max_block=max(1, T))
+                                         page_size=page, max_batch=B)
     return st
 
 
