@@ -69,7 +69,9 @@ typedef enum {
     SPEC_ERR_TIMEOUT = 6        /* reserved: a bounded device wait gave up */
 } spec_status;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+/* Logits are SPEC_F32 or SPEC_BF16; SPEC_F16 is taken by the spec_cache_* entry
+ * points only (SPEC_ERR_INVALID_ARG elsewhere). */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype;
 
 /* Order in which the statistics pass reads a request's rows.  All give the
  * same outputs, bit for bit:
@@ -92,7 +94,9 @@ typedef enum { SPEC_MODE_DENSE = 0, SPEC_MODE_PREFIX = 1, SPEC_MODE_AUTO = 2 } s
 #define SPEC_DEV_NONFINITE 2u       /* NaN/+inf in a row the chain read, or a row of all -inf */
 #define SPEC_DEV_BAD_TEMPERATURE 4u /* temperature negative, NaN, inf, in (0, 2^-100), or
                                        T > 0 with L_i > 0 but no draft logits */
+#define SPEC_DEV_BAD_PAGE 8u        /* (spec_cache_*) a page the call needs is outside [0, num_pages) */
 #define SPEC_DEV_INTERNAL 16u       /* internal consistency check failed (should not occur) */
+#define SPEC_DEV_BAD_LENGTH 32u     /* (spec_cache_*) the request's positions do not fit its table */
 
 typedef struct spec_verify_ctx spec_verify_ctx;
 
@@ -424,6 +428,148 @@ spec_status spec_lmhead_set_cta_pairs(spec_lmhead_ctx* ctx, int pairs);
  * (synchronises the device): bit 0 set = a wait inside a GEMM timed out and
  * that launch's outputs are not to be used. */
 spec_status spec_lmhead_errors(spec_lmhead_ctx* ctx, uint32_t* out);
+
+/* ---------------------------------------------------------------------------
+ * 4-bit block cache: keys and values of the scored positions, and the attention
+ * of a request's block over them.
+ *
+ * Between the verified lengths (spec_verify_lengths) and the LM head
+ * (spec_lmhead_verify) the target model scores each request's block: k drafted
+ * tokens and the one before them, T = k + 1 query tokens that see the request's
+ * whole context and, causally, one another.  These entry points keep that
+ * context in 4 bits: spec_cache_write quantises a block's (or a prompt's) keys
+ * and values as it stores them, spec_cache_attend reads them once for all query
+ * rows that share them, spec_cache_read gives them back as numbers.  A rejected
+ * draft needs no clean-up: the caller's cache_len goes up by the accepted tokens
+ * + 1, and the next block is written over what was rejected.
+ *
+ * The values.  An element is an e2m1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives); 16 neighbouring channels of a token share one e4m3 scale s, and a
+ * key/value head has one fp32 calibration scale g (k_scale, v_scale; 1 where
+ * NULL; it must be positive and finite).  Storing x:
+ *   y = x * (1/g) in fp32, 1/g rounded to fp32;
+ *   s = max(e4m3(min(max|y| / 6, 448)), 2^-9), over the 16 channels, the
+ *       quotient in fp32, to nearest, ties to even;
+ *   c = the e2m1 value nearest to y / s, ties to the even code, at most 6 in
+ *       magnitude, with y's sign.
+ * A group that holds a NaN or an infinity stores s = NaN, and reads as NaN.
+ * The stored value is c * s * g; c * s is exact in fp16, and that is what the
+ * attention multiplies with.
+ *
+ * The layout.  Positions live in pages of page_size tokens, named by a table of
+ * page numbers per request; position t of request i is token t % page_size of
+ * page table[i][t / page_size].  pages is [num_pages, heads_kv,
+ * page_size / 16, 18 * head_dim] bytes: per page and head, runs of 16 tokens.
+ * A run is
+ *   [head_dim / 32][16 tokens][16 B]  key codes, two channels a byte, the lower
+ *                                     channel in the low four bits;
+ *   [16 tokens][head_dim / 16]        key scales;
+ *   [head_dim][8 B]                   value codes, two tokens a byte, the
+ *                                     earlier one in the low four bits;
+ *   [head_dim / 16][16 tokens]        value scales.
+ * Fresh pages may hold anything: bytes behind a request's last position are
+ * never judged.
+ *
+ * Calls on pages that are not the caller's alone: two requests of one
+ * spec_cache_write must not write into the same run of 16 tokens (a page that
+ * is shared is copied before it is written to).  Any number of requests may
+ * read a page.
+ *
+ * Requests that cannot be served.  A request with cache_len < 0, or whose
+ * positions pass table_width * page_size, is skipped: nothing is written for
+ * it and its output rows stay as they were (SPEC_DEV_BAD_LENGTH).  A page
+ * number outside [0, num_pages) is never followed (SPEC_DEV_BAD_PAGE): tokens
+ * on it are not written, read rows of it stay as they were, and the attention
+ * treats them as masked.  Numbers of pages that a call does not need (behind
+ * the last position, or before a window's first) are not looked at.
+ * out_status [B] uint32, or NULL: these bits are OR-ed into it, so the caller
+ * sets it to 0 and may pass it to several calls.
+ * --------------------------------------------------------------------------- */
+typedef struct spec_cache_ctx spec_cache_ctx;
+
+typedef struct {
+    void* pages;           /* device, see above, 16-byte aligned */
+    int64_t num_pages;
+    const int32_t* table;  /* device, [B, table_stride], the first table_width of a row used */
+    int64_t table_stride;
+    int table_width;
+    const float* k_scale;  /* device, [heads_kv] or NULL */
+    const float* v_scale;  /* device, [heads_kv] or NULL */
+} spec_cache_pages;
+
+/* Rows of a [B, T, heads, head_dim] array: element (i, j, h, c) is at
+ * i * stride_b + j * stride_t + h * stride_h + c (elements).  data is 16-byte
+ * aligned and the strides are multiples of 16 bytes, else SPEC_ERR_UNSUPPORTED. */
+typedef struct {
+    void* data;
+    int64_t stride_b, stride_t, stride_h;
+} spec_cache_rows;
+
+/* Bytes of one page (all heads).  heads_kv 1..1024, head_dim 64, 128 or 256,
+ * page_size 16, 32, 64, 128 or 256; SPEC_ERR_UNSUPPORTED otherwise. */
+spec_status spec_cache_page_bytes(int heads_kv, int head_dim, int page_size, size_t* bytes);
+
+/* Create the context of one cache geometry on `device`: heads_q query heads
+ * (a multiple of heads_kv; query head h reads key/value head
+ * h / (heads_q / heads_kv)), batches up to max_batch (<= 65535).  It
+ * owns the workspace in which attention over one long context is joined, about
+ * 0.3 MB per SM at most.  One context per concurrently used stream, as above:
+ * captured graphs that use one context must not be replayed at the same time.
+ * The context holds no cache contents: any number of layers can use it. */
+spec_status spec_cache_init(spec_cache_ctx** ctx, int device, int max_batch, int heads_q,
+                            int heads_kv, int head_dim, int page_size);
+spec_status spec_cache_destroy(spec_cache_ctx* ctx);
+
+/* Quantise and store: token j < L_i of request i goes to position
+ * cache_len_i + j, L_i = block_len_i clamped to [0, T] (block_len NULL => T).
+ * k, v: [B, T, heads_kv, head_dim] rows of `dtype` (SPEC_F32, SPEC_BF16,
+ * SPEC_F16).  cache_len [B] int32.  Every other position keeps its bits. */
+spec_status spec_cache_write(spec_cache_ctx* ctx, const spec_cache_pages* cache,
+                             const spec_cache_rows* k, const spec_cache_rows* v, spec_dtype dtype,
+                             const int32_t* cache_len, const int32_t* block_len, int B, int T,
+                             uint32_t* out_status, cudaStream_t stream);
+
+/* Read back: row j < C_i of request i is position start_i + j, C_i = count_i
+ * clamped to [0, T] (start NULL => 0, count NULL => T).  out_k, out_v:
+ * [B, T, heads_kv, head_dim] rows of `dtype` (any of the three), c * s * g in
+ * fp32 rounded to nearest; rows from C_i on stay as they were. */
+spec_status spec_cache_read(spec_cache_ctx* ctx, const spec_cache_pages* cache,
+                            const int32_t* start, const int32_t* count, int B, int T,
+                            spec_dtype dtype, const spec_cache_rows* out_k,
+                            const spec_cache_rows* out_v, uint32_t* out_status,
+                            cudaStream_t stream);
+
+/* Attention of a block over the cache (which holds the block itself: write it
+ * first).  Query token j < L_i of request i stands at position
+ * p = cache_len_i + j and sees the positions t with
+ *   causal != 0: t <= p;   causal == 0: t < cache_len_i + L_i (a block whose
+ *   tokens see one another, as a parallel drafter's do);
+ *   and, for window > 0, t > p - window.
+ * For each query head, with k~, v~ the stored values:
+ *   out = sum_t softmax_t(scale * q . k~_t) v~_t,   lse = ln sum_t exp(scale * q . k~_t).
+ * q and out: [B, T, heads_q, head_dim] rows of `dtype` (SPEC_BF16 or SPEC_F16);
+ * out_lse [B, T, heads_q] fp32 or NULL.  Rows from L_i on stay as they were.  A
+ * row that sees nothing (its pages are missing) gives 0 and lse = -inf.  NaN
+ * and infinities: a row of q that holds one gives NaN; a NaN key gives NaN to
+ * the rows that see it, a NaN value group to those rows' channels of the group;
+ * rows that do not see the token are unaffected.
+ * Arithmetic: products of q with the stored key values are exact (q as fp16
+ * after scaling each row by a power of two, off by at most 2^-39 of the row's
+ * largest element), sums, maxima and the normalisation are
+ * fp32; probabilities are rounded to fp16 for the second product.  A row's
+ * reduction order depends on B, the lengths and the number of SMs, and not on
+ * timing: equal calls give equal bits.
+ * 1 <= B <= max_batch (0: no-op), 0 <= T <= 65535; scale finite. */
+spec_status spec_cache_attend(spec_cache_ctx* ctx, const spec_cache_pages* cache,
+                              const spec_cache_rows* q, spec_dtype dtype,
+                              const int32_t* cache_len, const int32_t* block_len, int B, int T,
+                              float scale, int causal, int window, const spec_cache_rows* out,
+                              float* out_lse, uint32_t* out_status, cudaStream_t stream);
+
+/* Error word of the attention kernel since the context was created
+ * (synchronises the device): non-zero = a wait inside the kernel timed out and
+ * that launch's outputs are not to be used. */
+spec_status spec_cache_errors(spec_cache_ctx* ctx, uint32_t* out);
 
 const char* spec_status_string(spec_status s);
 

@@ -27,6 +27,7 @@ SPEC_ERR_TIMEOUT = 6
 
 SPEC_F32 = 0
 SPEC_BF16 = 1
+SPEC_F16 = 2  # spec_cache_* only
 
 SPEC_MODE_DENSE = 0
 SPEC_MODE_PREFIX = 1
@@ -36,7 +37,9 @@ MODES = {"dense": SPEC_MODE_DENSE, "prefix": SPEC_MODE_PREFIX, "auto": SPEC_MODE
 DEV_BAD_TOKEN = 1
 DEV_NONFINITE = 2
 DEV_BAD_TEMPERATURE = 4
+DEV_BAD_PAGE = 8
 DEV_INTERNAL = 16
+DEV_BAD_LENGTH = 32
 
 TIMING_ENGINE, TIMING_LM_STATS, TIMING_LM_ROWS, TIMING_CONF = 0, 1, 2, 3
 TIMING_STATS = TIMING_ENGINE
@@ -52,6 +55,17 @@ class ConfArgs(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_void_p), ("w", ctypes.c_void_p), ("bias", ctypes.c_float),
                 ("kb", ctypes.c_int), ("H", ctypes.c_int), ("threshold", ctypes.c_float),
                 ("total_budget", ctypes.c_int64)]
+
+
+class CachePages(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
+
+
+class CacheRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
 
 
 _lib = None
@@ -113,6 +127,15 @@ def lib():
                                             ctypes.POINTER(ctypes.c_double)]
     L.spec_verify_ex2_error_bound.argtypes = []
     L.spec_verify_ex2_error_bound.restype = ctypes.c_double
+    pages_t, rows_t = ctypes.POINTER(CachePages), ctypes.POINTER(CacheRows)
+    L.spec_cache_page_bytes.argtypes = [_i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
+    L.spec_cache_init.argtypes = [ctypes.POINTER(_vp), _i32, _i32, _i32, _i32, _i32, _i32]
+    L.spec_cache_destroy.argtypes = [_vp]
+    L.spec_cache_errors.argtypes = [_vp, ctypes.POINTER(_u32)]
+    L.spec_cache_write.argtypes = [_vp, pages_t, rows_t, rows_t, _i32, _vp, _vp, _i32, _i32, _vp, _vp]
+    L.spec_cache_read.argtypes = [_vp, pages_t, _vp, _vp, _i32, _i32, _i32, rows_t, rows_t, _vp, _vp]
+    L.spec_cache_attend.argtypes = [_vp, pages_t, rows_t, _i32, _vp, _vp, _i32, _i32, ctypes.c_float,
+                                    _i32, _i32, rows_t, _vp, _vp, _vp]
     for name in ("spec_verify_init", "spec_verify_destroy", "spec_verify_run",
                  "spec_verify_run_with_uniforms", "spec_verify_run_host", "spec_verify_greedy",
                  "spec_conf_budget", "spec_verify_lengths", "spec_verify_greedy_noalloc",
@@ -123,7 +146,9 @@ def lib():
                  "spec_lmhead_logits", "spec_lmhead_verify", "spec_lmhead_set_cta_pairs",
                  "spec_verify_set_mode", "spec_verify_set_prefix_tail", "spec_verify_draws",
                  "spec_verify_timing_enable", "spec_verify_timing_read",
-                 "spec_verify_last_counters", "spec_verify_selfcheck_ex2"):
+                 "spec_verify_last_counters", "spec_verify_selfcheck_ex2",
+                 "spec_cache_page_bytes", "spec_cache_init", "spec_cache_destroy", "spec_cache_write",
+                 "spec_cache_read", "spec_cache_attend", "spec_cache_errors"):
         getattr(L, name).restype = _i32
     _lib = L
     return L
@@ -789,3 +814,211 @@ class LmHeadVerifier:
             _redo_requests(self.ver, redo, rows_of, tokens, verify_len, temperature, conf, seed,
                            step, request_offset, keys)
         return o
+
+
+# ------------------------------------------------------- 4-bit block cache --
+
+_CACHE_DTYPES = {torch.float32: SPEC_F32, torch.bfloat16: SPEC_BF16, torch.float16: SPEC_F16}
+
+
+class BlockCache:
+    """The 4-bit block cache (spec_cache_*): quantise keys and values into
+    pages, read them back, and the attention of a request's block over them.
+
+    One object holds one geometry and the workspace of the stream it is used
+    on, not the cache contents: every layer has its own ``pages`` tensor
+    (:meth:`alloc`), and any number of them can be used with one object.  A
+    request's positions are named by its row of ``table`` [B, width] int32 (page
+    numbers; a slice of a wider table is fine) and counted by ``cache_len`` [B]
+    int32, the positions in the cache before the block.  After a verification
+    ``cache_len += accepted + 1`` keeps the accepted tokens and forgets the
+    rest (a failed request's -1 leaves it as it was).
+
+    ``status`` [B] int32, where given, gets DEV_BAD_LENGTH and DEV_BAD_PAGE
+    OR-ed in; the caller zeroes it."""
+
+    def __init__(self, device=None, heads_q=32, heads_kv=8, head_dim=128, page_size=64, max_batch=1024):
+        dev = torch.device("cuda") if device is None else torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("BlockCache needs a CUDA device, got %s" % dev)
+        self._h = None
+        self.page_bytes = self.bytes_per_page(heads_kv, head_dim, page_size)
+        if dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        self.heads_q, self.heads_kv, self.head_dim = int(heads_q), int(heads_kv), int(head_dim)
+        self.page_size, self.max_batch = int(page_size), int(max_batch)
+        h = _vp()
+        _check(lib().spec_cache_init(ctypes.byref(h), dev.index, self.max_batch, self.heads_q,
+                                     self.heads_kv, self.head_dim, self.page_size), "spec_cache_init")
+        self._h = h
+
+    @staticmethod
+    def bytes_per_page(heads_kv, head_dim, page_size):
+        """spec_cache_page_bytes: bytes of one page, all heads."""
+        n = ctypes.c_size_t()
+        _check(lib().spec_cache_page_bytes(int(heads_kv), int(head_dim), int(page_size), ctypes.byref(n)),
+               "spec_cache_page_bytes")
+        return n.value
+
+    def alloc(self, num_pages):
+        """A pool of pages for one layer: [num_pages, heads_kv, page_size / 16, 18 head_dim] uint8."""
+        return torch.empty((int(num_pages), self.heads_kv, self.page_size // 16, 18 * self.head_dim),
+                           dtype=torch.uint8, device=self.device)
+
+    # -- lifecycle ------------------------------------------------------------
+    def close(self):
+        if getattr(self, "_h", None):
+            lib().spec_cache_destroy(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def errors(self):
+        out = _u32(0)
+        _check(lib().spec_cache_errors(self._h, ctypes.byref(out)), "spec_cache_errors")
+        return int(out.value)
+
+    # -- helpers --------------------------------------------------------------
+    def _pages(self, pages, table, B, k_scale, v_scale):
+        shape = (self.heads_kv, self.page_size // 16, 18 * self.head_dim)
+        if pages.dim() != 4 or tuple(pages.shape[1:]) != shape:
+            raise ValueError("pages must be [num_pages, %d, %d, %d]" % shape)
+        if table.dim() != 2 or table.shape[0] != B:
+            raise ValueError("table must be [B, width] with B = %d" % B)
+        if not table.is_cuda or table.device != self.device:
+            raise ValueError("table must be on %s" % self.device)
+        if table.dtype != torch.int32:
+            raise TypeError("table must be torch.int32, got %s" % table.dtype)
+        if table.shape[1] > 1 and table.stride(1) != 1:
+            raise ValueError("a row of the table must be contiguous")
+        for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if s is not None and tuple(s.shape) != (self.heads_kv,):
+                raise ValueError("%s must be [%d]" % (name, self.heads_kv))
+        stride = table.stride(0) if B > 1 else table.shape[1]
+        return CachePages(_dev_ptr(pages, torch.uint8, self.device, "pages"), pages.shape[0],
+                          table.data_ptr(), stride, table.shape[1],
+                          _dev_ptr(k_scale, torch.float32, self.device, "k_scale"),
+                          _dev_ptr(v_scale, torch.float32, self.device, "v_scale"))
+
+    def _rows(self, t, heads, name, shape=None, dtype=None):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if not t.is_cuda or t.device != self.device:
+            raise ValueError("%s must be on %s" % (name, self.device))
+        if t.dtype not in _CACHE_DTYPES or (dtype is not None and t.dtype != dtype):
+            raise TypeError("%s has dtype %s" % (name, t.dtype))
+        if t.dim() != 4 or tuple(t.shape[2:]) != (heads, self.head_dim) or \
+                (shape is not None and tuple(t.shape[:2]) != tuple(shape)):
+            raise ValueError("%s must be [B, T, %d, %d], got %s" % (name, heads, self.head_dim, tuple(t.shape)))
+        if t.stride(3) != 1:
+            raise ValueError("the channels of %s must be contiguous" % name)
+        # the stride of a dimension of one element says nothing
+        st = [t.stride(d) if t.shape[d] > 1 else 0 for d in range(3)]
+        return CacheRows(t.data_ptr(), *st)
+
+    def _ints(self, t, B, name):
+        if t is not None and tuple(t.shape) != (B,):
+            raise ValueError("%s must be [B] = [%d]" % (name, B))
+        return _dev_ptr(t, torch.int32, self.device, name)
+
+    @staticmethod
+    def _one_place(t, name):
+        """Rows that are written must not share memory (an expanded dimension)."""
+        for d in range(t.dim()):
+            if t.shape[d] > 1 and t.stride(d) == 0:
+                raise ValueError("%s must not be an expanded tensor" % name)
+
+    # -- entry points ---------------------------------------------------------
+    def write(self, k, v, pages, table, cache_len, block_len=None, k_scale=None, v_scale=None,
+              status=None, stream=None):
+        """spec_cache_write: k, v [B, T, heads_kv, head_dim] (fp32, bf16 or fp16, any strides with
+        contiguous channels) go to the positions from cache_len on, quantised; block_len [B] limits the
+        tokens of each request."""
+        if not isinstance(k, torch.Tensor) or k.dim() != 4:
+            raise ValueError("k must be [B, T, %d, %d]" % (self.heads_kv, self.head_dim))
+        B, T = k.shape[:2]
+        kr = self._rows(k, self.heads_kv, "k")
+        vr = self._rows(v, self.heads_kv, "v", (B, T), k.dtype)
+        if cache_len is None:
+            raise ValueError("cache_len is needed")
+        pg = self._pages(pages, table, B, k_scale, v_scale)
+        st = lib().spec_cache_write(
+            self._h, ctypes.byref(pg), ctypes.byref(kr), ctypes.byref(vr), _CACHE_DTYPES[k.dtype],
+            self._ints(cache_len, B, "cache_len"), self._ints(block_len, B, "block_len"), B, T,
+            self._ints(status, B, "status"), _stream_handle(stream, self.device))
+        _check(st, "spec_cache_write")
+
+    def read(self, pages, table, start=None, count=None, rows=None, dtype=torch.bfloat16, k_scale=None,
+             v_scale=None, out=None, status=None, stream=None):
+        """spec_cache_read: (k, v) [B, rows, heads_kv, head_dim] of the positions from start (default 0)
+        on; count [B] limits each request's rows, the others stay as they were (0 where ``out`` is not
+        given).  ``rows`` and ``dtype`` are those of ``out`` = (k, v) where it is given."""
+        B = table.shape[0]
+        if out is None:
+            if rows is None:
+                raise ValueError("rows is needed where out is not given")
+            shape = (B, int(rows), self.heads_kv, self.head_dim)
+            out = (torch.zeros(shape, dtype=dtype, device=self.device),
+                   torch.zeros(shape, dtype=dtype, device=self.device))
+        k, v = out
+        if k.dim() != 4 or (rows is not None and k.shape[1] != rows):
+            raise ValueError("out must be two [B, rows, %d, %d] tensors" % (self.heads_kv, self.head_dim))
+        T = k.shape[1]
+        kr = self._rows(k, self.heads_kv, "out[0]", (B, T))
+        vr = self._rows(v, self.heads_kv, "out[1]", (B, T), k.dtype)
+        self._one_place(k, "out[0]")
+        self._one_place(v, "out[1]")
+        pg = self._pages(pages, table, B, k_scale, v_scale)
+        st = lib().spec_cache_read(
+            self._h, ctypes.byref(pg), self._ints(start, B, "start"), self._ints(count, B, "count"), B, T,
+            _CACHE_DTYPES[k.dtype], ctypes.byref(kr), ctypes.byref(vr), self._ints(status, B, "status"),
+            _stream_handle(stream, self.device))
+        _check(st, "spec_cache_read")
+        return out
+
+    def attend(self, q, pages, table, cache_len, block_len=None, scale=None, causal=True, window=0,
+               k_scale=None, v_scale=None, out=None, lse=None, status=None, stream=None):
+        """spec_cache_attend: attention of the block's queries q [B, T, heads_q, head_dim] (bf16 or
+        fp16, any strides with contiguous channels) over the cache, which holds the block itself (call
+        :meth:`write` first).  ``scale`` defaults to head_dim ** -0.5; ``window`` > 0 limits each query
+        to the last ``window`` positions.  Returns (out, lse): out like q, lse [B, T, heads_q] fp32, the
+        natural logarithm of each row's sum.  Rows from block_len on stay as they were (out 0 and lse
+        -inf where they are not given); ``lse=False`` leaves the sums out (None is returned)."""
+        if not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("q must be [B, T, %d, %d]" % (self.heads_q, self.head_dim))
+        if q.dtype == torch.float32:
+            raise TypeError("q must be bfloat16 or float16")
+        B, T = q.shape[:2]
+        qr = self._rows(q, self.heads_q, "q")
+        if cache_len is None:
+            raise ValueError("cache_len is needed")
+        if out is None:
+            out = torch.zeros((B, T, self.heads_q, self.head_dim), dtype=q.dtype, device=self.device)
+        outr = self._rows(out, self.heads_q, "out", (B, T), q.dtype)
+        self._one_place(out, "out")
+        if lse is None or lse is True:
+            lse = torch.full((B, T, self.heads_q), float("-inf"), device=self.device)
+        elif lse is False:
+            lse = None
+        elif tuple(lse.shape) != (B, T, self.heads_q):
+            raise ValueError("lse must be [B, T, %d]" % self.heads_q)
+        pg = self._pages(pages, table, B, k_scale, v_scale)
+        st = lib().spec_cache_attend(
+            self._h, ctypes.byref(pg), ctypes.byref(qr), _CACHE_DTYPES[q.dtype],
+            self._ints(cache_len, B, "cache_len"), self._ints(block_len, B, "block_len"), B, T,
+            float(self.head_dim ** -0.5 if scale is None else scale), int(bool(causal)), int(window),
+            ctypes.byref(outr), _dev_ptr(lse, torch.float32, self.device, "lse"),
+            self._ints(status, B, "status"), _stream_handle(stream, self.device))
+        _check(st, "spec_cache_attend")
+        return out, lse

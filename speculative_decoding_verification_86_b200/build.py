@@ -1,7 +1,7 @@
 """Build step: compile the CUDA library ``libspecverify.so`` for sm_100a in-tree.
 
 ``python -m speculative_decoding_verification_86_b200.build`` (or
-``__graft_entry__.build()``) runs nvcc on ``csrc/spec_verify.cu``.
+``__graft_entry__.build()``) runs nvcc on the units ``csrc/*.cu``.
 """
 from __future__ import annotations
 
@@ -18,7 +18,7 @@ LIB = os.path.join(PKG, "libspecverify.so")
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17", "-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo",
-    "-Xcompiler", "-fPIC", "-shared", "--expt-relaxed-constexpr",
+    "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
 ]
 
 
@@ -38,11 +38,25 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest and not extra_flags:
         return LIB
     tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [_nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC,
-           os.path.join(CSRC, "spec_verify.cu"), "-o", tmp, "-cudart", "static"]
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    objects = ["%s.%s.o" % (tmp, os.path.basename(u)) for u in units]
+    cmds = [[_nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-c", u, "-o", o]
+            for u, o in zip(units, objects)]
+    link = [_nvcc(), *NVCC_FLAGS, "-shared", *objects, "-o", tmp, "-cudart", "static"]
     if verbose:
-        print(" ".join(cmd), file=sys.stderr)
-    subprocess.check_call(cmd)
+        for cmd in cmds + [link]:
+            print(" ".join(cmd), file=sys.stderr)
+    try:
+        jobs = [subprocess.Popen(cmd) for cmd in cmds]  # the units compile side by side
+        codes = [job.wait() for job in jobs]
+        for code, cmd in zip(codes, cmds):
+            if code:
+                raise subprocess.CalledProcessError(code, cmd)
+        subprocess.check_call(link)
+    finally:
+        for o in objects:
+            if os.path.exists(o):
+                os.remove(o)
     os.replace(tmp, LIB)
     return LIB
 

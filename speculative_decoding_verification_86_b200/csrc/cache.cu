@@ -1,0 +1,249 @@
+// Host side of the 4-bit block cache (spec_cache_* in include/spec_verify.h):
+// argument checks, the context's workspace and the launches.
+#include "spec_verify.h"
+
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include "attend.cuh"
+#include "cache.cuh"
+#include "host.cuh"
+
+struct spec_cache_ctx {
+  int device = 0;
+  int num_sms = 0;
+  int max_batch = 0;
+  int heads_q = 0, heads_kv = 0, head_dim = 0, page_size = 0;
+  void* ws = nullptr;
+  unsigned* error = nullptr;
+};
+
+namespace {
+
+bool geometry_ok(int heads_kv, int head_dim, int page_size) {
+  return heads_kv >= 1 && heads_kv <= 1024 && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+         page_size >= 16 && page_size <= 256 && (page_size & (page_size - 1)) == 0;
+}
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+size_t dtype_bytes(spec_dtype t) { return t == SPEC_F32 ? 4 : 2; }
+
+// The pages of a call.  `requests` is false for a batch of no requests, whose
+// table is not looked at.
+spec_status check_pages(const spec_cache_ctx* c, const spec_cache_pages* p, sv::CacheView* out) {
+  if (!p || !p->pages || !p->table || p->num_pages < 0 || p->table_width < 0 ||
+      p->table_stride < p->table_width)
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(p->pages, 16) || !aligned(p->table, 4) || (p->k_scale && !aligned(p->k_scale, 4)) ||
+      (p->v_scale && !aligned(p->v_scale, 4)))
+    return SPEC_ERR_UNSUPPORTED;
+  out->pages = static_cast<uint8_t*>(p->pages);
+  out->num_pages = p->num_pages;
+  out->table = p->table;
+  out->table_stride = p->table_stride;
+  out->capacity = static_cast<int64_t>(p->table_width) * c->page_size;
+  out->heads = c->heads_kv;
+  out->page_shift = log2_of(c->page_size);
+  out->k_scale = p->k_scale;
+  out->v_scale = p->v_scale;
+  return SPEC_OK;
+}
+
+spec_status check_rows(const spec_cache_rows* r, spec_dtype dtype, sv::CacheRows* out) {
+  if (!r || !r->data) return SPEC_ERR_INVALID_ARG;
+  const int64_t unit = static_cast<int64_t>(16 / dtype_bytes(dtype));
+  if (!aligned(r->data, 16) || r->stride_b % unit || r->stride_t % unit || r->stride_h % unit)
+    return SPEC_ERR_UNSUPPORTED;
+  *out = sv::CacheRows{r->data, r->stride_b, r->stride_t, r->stride_h};
+  return SPEC_OK;
+}
+
+// Launch the write or the read with one warp per 64 channels of a run.
+template <bool WRITE, int D>
+spec_status launch_move(const sv::CacheMove& p, spec_dtype dtype, cudaStream_t stream) {
+  const int64_t warps = static_cast<int64_t>(p.B) * p.runs * p.c.heads * 2 * (D / 64);
+  const int64_t blocks = (warps * 32 + sv::kMoveThreads - 1) / sv::kMoveThreads;
+  if (blocks > 0x7fffffff) return SPEC_ERR_INVALID_ARG;
+  const dim3 g(static_cast<unsigned>(blocks)), b(sv::kMoveThreads);
+  if constexpr (WRITE) {
+    if (dtype == SPEC_F32) sv::k_cache_write<D, float><<<g, b, 0, stream>>>(p);
+    else if (dtype == SPEC_BF16) sv::k_cache_write<D, __nv_bfloat16><<<g, b, 0, stream>>>(p);
+    else sv::k_cache_write<D, __half><<<g, b, 0, stream>>>(p);
+  } else {
+    if (dtype == SPEC_F32) sv::k_cache_read<D, float><<<g, b, 0, stream>>>(p);
+    else if (dtype == SPEC_BF16) sv::k_cache_read<D, __nv_bfloat16><<<g, b, 0, stream>>>(p);
+    else sv::k_cache_read<D, __half><<<g, b, 0, stream>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+template <bool WRITE>
+spec_status move(spec_cache_ctx* c, const spec_cache_pages* cache, const spec_cache_rows* k,
+                 const spec_cache_rows* v, spec_dtype dtype, const int32_t* start,
+                 const int32_t* count, int B, int T, uint32_t* out_status, cudaStream_t stream) {
+  if (!c || B < 0 || B > c->max_batch || T < 0) return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return SPEC_OK;
+  if (WRITE && !start) return SPEC_ERR_INVALID_ARG;
+  sv::CacheMove p{};
+  if (spec_status st = check_pages(c, cache, &p.c); st != SPEC_OK) return st;
+  if (spec_status st = check_rows(k, dtype, &p.k); st != SPEC_OK) return st;
+  if (spec_status st = check_rows(v, dtype, &p.v); st != SPEC_OK) return st;
+  if ((start && !aligned(start, 4)) || (count && !aligned(count, 4)) ||
+      (out_status && !aligned(out_status, 4)))
+    return SPEC_ERR_UNSUPPORTED;
+  p.start = start;
+  p.count = count;
+  p.B = B;
+  p.T = T;
+  p.runs = (static_cast<int64_t>(T) + 2 * (sv::kRun - 1)) / sv::kRun;  // a span may start anywhere in a run
+  p.status = out_status;
+  DeviceGuard g(c->device);
+  if (!g.ok) return SPEC_ERR_CUDA;
+  cudaGetLastError();
+  if (c->head_dim == 64) return launch_move<WRITE, 64>(p, dtype, stream);
+  if (c->head_dim == 128) return launch_move<WRITE, 128>(p, dtype, stream);
+  return launch_move<WRITE, 256>(p, dtype, stream);
+}
+
+template <int D>
+void launch_attend(const sv::AttendParams& p, spec_dtype dtype, cudaStream_t stream) {
+  const dim3 g(p.heads_q, p.T, p.B);
+  if (dtype == SPEC_BF16) sv::k_attend<D, __nv_bfloat16><<<g, 128, 0, stream>>>(p);
+  else sv::k_attend<D, __half><<<g, 128, 0, stream>>>(p);
+}
+
+}  // namespace
+
+extern "C" {
+
+spec_status spec_cache_page_bytes(int heads_kv, int head_dim, int page_size, size_t* bytes) {
+  if (!bytes) return SPEC_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (!geometry_ok(heads_kv, head_dim, page_size)) return SPEC_ERR_UNSUPPORTED;
+  *bytes = static_cast<size_t>(heads_kv) * (page_size / sv::kRun) * sv::run_bytes(head_dim);
+  return SPEC_OK;
+}
+
+spec_status spec_cache_init(spec_cache_ctx** out, int device, int max_batch, int heads_q,
+                            int heads_kv, int head_dim, int page_size) {
+  if (!out) return SPEC_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (max_batch < 1 || max_batch > 65535 || heads_kv < 1 || heads_q < heads_kv || heads_q > 65535 ||
+      heads_q % heads_kv != 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (!geometry_ok(heads_kv, head_dim, page_size)) return SPEC_ERR_UNSUPPORTED;
+  int ndev = 0;
+  if (cudaGetDeviceCount(&ndev) != cudaSuccess) {
+    cudaGetLastError();
+    return SPEC_ERR_CUDA;
+  }
+  if (device < 0 || device >= ndev) return SPEC_ERR_INVALID_ARG;
+  DeviceGuard g(device);
+  if (!g.ok) return SPEC_ERR_CUDA;
+  spec_cache_ctx* c = new (std::nothrow) spec_cache_ctx();
+  if (!c) return SPEC_ERR_NOMEM;
+  c->device = device;
+  c->max_batch = max_batch;
+  c->heads_q = heads_q;
+  c->heads_kv = heads_kv;
+  c->head_dim = head_dim;
+  c->page_size = page_size;
+  if (cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess) {
+    delete c;
+    return SPEC_ERR_CUDA;
+  }
+  if (cudaMalloc(&c->ws, 256) != cudaSuccess) {
+    cudaGetLastError();
+    delete c;
+    return SPEC_ERR_NOMEM;
+  }
+  c->error = static_cast<unsigned*>(c->ws);
+  if (cudaMemset(c->ws, 0, 256) != cudaSuccess) {
+    cudaFree(c->ws);
+    delete c;
+    return SPEC_ERR_CUDA;
+  }
+  *out = c;
+  return SPEC_OK;
+}
+
+spec_status spec_cache_destroy(spec_cache_ctx* c) {
+  if (!c) return SPEC_OK;
+  DeviceGuard g(c->device);
+  cudaDeviceSynchronize();
+  cudaFree(c->ws);
+  delete c;
+  return SPEC_OK;
+}
+
+spec_status spec_cache_write(spec_cache_ctx* c, const spec_cache_pages* cache,
+                             const spec_cache_rows* k, const spec_cache_rows* v, spec_dtype dtype,
+                             const int32_t* cache_len, const int32_t* block_len, int B, int T,
+                             uint32_t* out_status, cudaStream_t stream) {
+  return move<true>(c, cache, k, v, dtype, cache_len, block_len, B, T, out_status, stream);
+}
+
+spec_status spec_cache_read(spec_cache_ctx* c, const spec_cache_pages* cache,
+                            const int32_t* start, const int32_t* count, int B, int T,
+                            spec_dtype dtype, const spec_cache_rows* out_k,
+                            const spec_cache_rows* out_v, uint32_t* out_status,
+                            cudaStream_t stream) {
+  return move<false>(c, cache, out_k, out_v, dtype, start, count, B, T, out_status, stream);
+}
+
+spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
+                              const spec_cache_rows* q, spec_dtype dtype,
+                              const int32_t* cache_len, const int32_t* block_len, int B, int T,
+                              float scale, int causal, int window, const spec_cache_rows* out,
+                              float* out_lse, uint32_t* out_status, cudaStream_t stream) {
+  if (!c || B < 0 || B > c->max_batch || T < 0 || T > 65535 || window < 0 || !std::isfinite(scale))
+    return SPEC_ERR_INVALID_ARG;
+  if (dtype != SPEC_BF16 && dtype != SPEC_F16)
+    return dtype == SPEC_F32 ? SPEC_ERR_UNSUPPORTED : SPEC_ERR_INVALID_ARG;
+  if (B == 0 || T == 0) return SPEC_OK;
+  if (!cache_len) return SPEC_ERR_INVALID_ARG;
+  sv::AttendParams p{};
+  if (spec_status st = check_pages(c, cache, &p.c); st != SPEC_OK) return st;
+  if (spec_status st = check_rows(q, dtype, &p.q); st != SPEC_OK) return st;
+  if (spec_status st = check_rows(out, dtype, &p.out); st != SPEC_OK) return st;
+  if (!aligned(cache_len, 4) || (block_len && !aligned(block_len, 4)) ||
+      (out_lse && !aligned(out_lse, 4)) || (out_status && !aligned(out_status, 4)))
+    return SPEC_ERR_UNSUPPORTED;
+  p.cache_len = cache_len;
+  p.block_len = block_len;
+  p.B = B;
+  p.T = T;
+  p.heads_q = c->heads_q;
+  p.group = c->heads_q / c->heads_kv;
+  p.scale = scale;
+  p.causal = causal != 0;
+  p.window = window;
+  p.lse = out_lse;
+  p.status = out_status;
+  DeviceGuard g(c->device);
+  if (!g.ok) return SPEC_ERR_CUDA;
+  cudaGetLastError();
+  if (c->head_dim == 64) launch_attend<64>(p, dtype, stream);
+  else if (c->head_dim == 128) launch_attend<128>(p, dtype, stream);
+  else launch_attend<256>(p, dtype, stream);
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+spec_status spec_cache_errors(spec_cache_ctx* c, uint32_t* out) {
+  if (!c || !out) return SPEC_ERR_INVALID_ARG;
+  DeviceGuard g(c->device);
+  if (cudaDeviceSynchronize() != cudaSuccess) return SPEC_ERR_CUDA;
+  unsigned h = 0;
+  if (cudaMemcpy(&h, c->error, sizeof h, cudaMemcpyDeviceToHost) != cudaSuccess) return SPEC_ERR_CUDA;
+  *out = h;
+  return SPEC_OK;
+}
+
+}  // extern "C"

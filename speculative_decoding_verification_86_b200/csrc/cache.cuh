@@ -1,0 +1,435 @@
+// The 4-bit block cache: its layout, and the kernels that quantise keys and
+// values into it and read them back.
+//
+// A page holds, per key/value head, runs of 16 tokens.  A run is 18 D bytes
+// (D = head_dim): key codes [D/32][16][16 B], key scales [16][D/16], value codes
+// [D][8 B], value scales [D/16][16].  The attention gives one thread a token of
+// the keys and a channel of the values; in this order its threads read their
+// 16 and 8 bytes next to one another, and one copy of 18 D contiguous bytes
+// brings a run into shared memory whatever the page size.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+namespace sv {
+
+constexpr uint32_t kDevBadPage = 8u;
+constexpr uint32_t kDevBadLength = 32u;
+constexpr int kRun = 16;    // tokens of a run
+constexpr int kGroup = 16;  // channels that share a scale
+constexpr uint32_t kScaleNaN = 0x7fu;  // e4m3
+
+__host__ __device__ constexpr int run_bytes(int D) { return 18 * D; }
+__host__ __device__ constexpr int run_k_scales(int D) { return 8 * D; }
+__host__ __device__ constexpr int run_v_codes(int D) { return 9 * D; }
+__host__ __device__ constexpr int run_v_scales(int D) { return 17 * D; }
+
+struct CacheView {
+  uint8_t* pages;
+  int64_t num_pages;
+  const int32_t* table;
+  int64_t table_stride;
+  int64_t capacity;  // positions the table reaches: table_width * page_size
+  int heads;         // key/value heads
+  int page_shift;    // log2(page_size)
+  const float* k_scale;
+  const float* v_scale;
+};
+
+struct CacheRows {
+  void* data;
+  int64_t sb, st, sh;  // elements
+};
+
+// The run `run` (position / 16) of request i, head h; nullptr where the table
+// names no page of the pool.
+template <int D>
+__device__ __forceinline__ uint8_t* cache_run(const CacheView& c, int i, int h, int64_t run) {
+  const int per_page = c.page_shift - 4;  // log2(runs of a page)
+  const int64_t page = __ldg(c.table + i * c.table_stride + (run >> per_page));
+  if (page < 0 || page >= c.num_pages) return nullptr;
+  const int64_t r = ((page * c.heads + h) << per_page) + (run & ((1 << per_page) - 1));
+  return c.pages + r * run_bytes(D);
+}
+
+// Two e4m3 scales (low byte first) -> two fp16; exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(two)));
+  return r;
+}
+// Eight e2m1 codes (low four bits first) -> four fp16 pairs; exact.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// Two values -> two e2m1 codes in a byte (lo in the low four bits), to nearest,
+// ties to even, saturating.
+__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}\n"
+      : "=r"(r)
+      : "f"(lo), "f"(hi));
+  return r;
+}
+// e4m3 of a value in [0, 448], to nearest, ties to even.
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(x));
+  return r & 0xffu;
+}
+__device__ __forceinline__ uint32_t h2_mul(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float2 h2_to_f2(uint32_t a) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&a));
+}
+
+// 16 neighbouring channels of a row, as fp32 (32 or 64 aligned bytes).
+template <typename T>
+__device__ __forceinline__ void load_group(const T* p, float (&x)[16]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + u);
+      x[4 * u] = f.x, x[4 * u + 1] = f.y, x[4 * u + 2] = f.z, x[4 * u + 3] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + u);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float2 f;
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          f = make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
+        } else {
+          f = h2_to_f2(v[e]);
+        }
+        x[8 * u + 2 * e] = f.x;
+        x[8 * u + 2 * e + 1] = f.y;
+      }
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store_group(T* p, const float (&x)[16]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      reinterpret_cast<float4*>(p)[u] = make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      uint32_t v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float a = x[8 * u + 2 * e], b = x[8 * u + 2 * e + 1];
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+          v[e] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __half2 h = __floats2half2_rn(a, b);
+          v[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      reinterpret_cast<uint4*>(p)[u] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+// Quantise one group.  `code` gets the sixteen codes, channel c in bits 4c;
+// returns the scale's byte.  rg = RN(1/g).
+// The quotient y / s is formed as q0 = y r, q = fma(fma(-q0, s, y), r, q0) with
+// r = RN(1/s): the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34,
+// 1990).  A correctly rounded quotient lies on a midpoint of two codes only if
+// the exact one does (the midpoints have three significant bits), so the
+// conversion's ties-to-even decides exactly the ties of y / s.
+__device__ __forceinline__ uint32_t quantise_group(const float (&x)[16], float rg, uint64_t& code) {
+  float y[16];
+  float top = 0.0f;
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    y[e] = __fmul_rn(x[e], rg);
+    top = fmaxf(top, fabsf(y[e]));
+    bad |= !(fabsf(y[e]) < INFINITY);
+  }
+  uint32_t sb = f32_to_e4m3(fminf(__fdiv_rn(top, 6.0f), 448.0f));
+  sb = sb ? sb : 1u;  // 2^-9, the smallest scale
+  const float s = h2_to_f2(e4m3x2_to_f16x2(sb)).x;
+  const float r = __frcp_rn(s);
+  uint32_t lo = 0, hi = 0;
+#pragma unroll
+  for (int e = 0; e < 16; e += 2) {
+    float q[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float q0 = __fmul_rn(y[e + u], r);
+      q[u] = copysignf(__fmaf_rn(__fmaf_rn(-q0, s, y[e + u]), r, q0), y[e + u]);  // -0 stays -0
+    }
+    const uint32_t b = f32x2_to_e2m1x2(q[0], q[1]);
+    if (e < 8) lo |= b << (4 * e);
+    else hi |= b << (4 * (e - 8));
+  }
+  code = bad ? 0ull : (static_cast<uint64_t>(hi) << 32) | lo;
+  return bad ? kScaleNaN : sb;
+}
+
+// Exchange between the eight lanes that share a scale group (lane bits 0-2 = b):
+// halfword c of lane b becomes halfword b of lane c.  Its own inverse.
+__device__ __forceinline__ void transpose_lanes8(uint32_t (&w)[4], int b) {
+  // 4 x 4 words between lanes that differ in bits 1 and 2, then the halfwords
+  // between neighbours
+#pragma unroll
+  for (int bit = 4; bit >= 2; bit >>= 1) {
+    const bool up = b & bit;
+    const int step = bit >> 1;  // words apart: 2, then 1
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      if (a & step) continue;
+      const uint32_t send = up ? w[a] : w[a + step];
+      const uint32_t got = __shfl_xor_sync(0xffffffffu, send, bit);
+      if (up) w[a] = got;
+      else w[a + step] = got;
+    }
+  }
+  const bool odd = b & 1;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, w[a], 1);
+    w[a] = odd ? __byte_perm(got, w[a], 0x7632) : __byte_perm(w[a], got, 0x5410);
+  }
+}
+
+struct CacheMove {
+  CacheView c;
+  CacheRows k, v;
+  const int32_t* start;  // first position per request (nullptr: 0)
+  const int32_t* count;  // tokens per request, clamped to [0, T] (nullptr: T)
+  int B, T;
+  int64_t runs;          // runs a request's tokens can touch
+  uint32_t* status;
+};
+
+// The request's span of positions, or false where it is skipped.
+__device__ __forceinline__ bool cache_span(const CacheMove& p, int i, int64_t& n, int& L) {
+  n = p.start ? __ldg(p.start + i) : 0;
+  L = p.count ? min(max(__ldg(p.count + i), 0), p.T) : p.T;
+  return n >= 0 && n + L <= p.c.capacity;
+}
+
+// One warp moves 64 channels of one run of one (request, head), keys or values:
+// lane = token pair b (tokens 2b, 2b+1) + 8 * scale group.  A pair of tokens
+// fills one byte of a value's row, so a warp holds whole rows of codes, and no
+// two warps touch the same bytes.  The work is a streaming pass: 128-byte rows
+// in, 256-byte runs of codes out, so it is bound by memory; a lane keeps its 64
+// input bytes in flight, and there are enough warps (a prompt of 8191 tokens
+// has 16 K) to cover the table look-up before the store.
+struct CacheTask {
+  int i, h, chunk, is_v;
+  int64_t run;
+};
+template <int D>
+__device__ __forceinline__ bool cache_task(const CacheMove& p, CacheTask& t) {
+  int64_t w = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
+  constexpr int C = D / 64;
+  t.chunk = static_cast<int>(w % C);
+  w /= C;
+  t.is_v = static_cast<int>(w & 1);
+  w >>= 1;
+  t.h = static_cast<int>(w % p.c.heads);
+  w /= p.c.heads;
+  t.run = w % p.runs;
+  w /= p.runs;
+  t.i = static_cast<int>(w);
+  return w < p.B;
+}
+
+constexpr int kMoveThreads = 128;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
+  CacheTask t;
+  if (!cache_task<D>(p, t)) return;
+  const int lane = threadIdx.x & 31;
+  int64_t n;
+  int L;
+  const bool fits = cache_span(p, t.i, n, L);
+  if (!fits) {
+    if (p.status && t.run == 0 && t.h == 0 && t.chunk == 0 && !t.is_v && lane == 0)
+      atomicOr(p.status + t.i, kDevBadLength);
+    return;
+  }
+  const int64_t run = (n >> 4) + t.run;
+  // the request's tokens of this run: [lo, hi)
+  const int lo = static_cast<int>(max(n - run * kRun, int64_t(0)));
+  const int hi = static_cast<int>(min(n + L - run * kRun, int64_t(kRun)));
+  if (lo >= hi) return;
+  uint8_t* dst = cache_run<D>(p.c, t.i, t.h, run);
+  const int b = lane & 7, g = t.chunk * 4 + (lane >> 3);
+  const CacheRows& rows = t.is_v ? p.v : p.k;
+  const float* gs = t.is_v ? p.c.v_scale : p.c.k_scale;
+  const float rg = gs ? __frcp_rn(__ldg(gs + t.h)) : 1.0f;
+  const T* src = static_cast<const T*>(rows.data) + t.i * rows.sb + t.h * rows.sh + g * kGroup;
+  float x[2][16];
+  bool in[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int tok = 2 * b + u;
+    in[u] = tok >= lo && tok < hi;
+    if (in[u]) {
+      load_group(src + (run * kRun + tok - n) * rows.st, x[u]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[u][e] = 0.0f;
+    }
+  }
+  if (!dst) {
+    if (p.status && t.h == 0 && t.chunk == 0 && !t.is_v && lane == 0)
+      atomicOr(p.status + t.i, kDevBadPage);
+    return;
+  }
+  uint64_t code[2];
+  uint32_t sc[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) sc[u] = quantise_group(x[u], rg, code[u]);
+  if (!t.is_v) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (!in[u]) continue;
+      const int tok = 2 * b + u;
+      *reinterpret_cast<uint64_t*>(dst + (g >> 1) * 256 + tok * 16 + (g & 1) * 8) = code[u];
+      dst[run_k_scales(D) + tok * (D / kGroup) + g] = static_cast<uint8_t>(sc[u]);
+    }
+    return;
+  }
+  // bytes of channel pairs: channel c of tokens (2b, 2b+1) in byte c
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t a = static_cast<uint32_t>(code[0] >> (16 * q)) & 0xffffu;
+    const uint32_t c = static_cast<uint32_t>(code[1] >> (16 * q)) & 0xffffu;
+    // spread the four codes of each token over four bytes
+    const uint32_t sa = (a | (a << 8)) & 0x00ff00ffu, sc2 = (c | (c << 8)) & 0x00ff00ffu;
+    const uint32_t ea = (sa | (sa << 4)) & 0x0f0f0f0fu, ec = (sc2 | (sc2 << 4)) & 0x0f0f0f0fu;
+    w[q] = ea | (ec << 4);
+  }
+  transpose_lanes8(w, b);
+  // now the channels 2b, 2b+1 of the group, interleaved: part them into rows of
+  // eight bytes, one for each token pair
+  {
+    const uint32_t a0 = __byte_perm(w[0], w[1], 0x6420), a1 = __byte_perm(w[2], w[3], 0x6420);
+    const uint32_t b0 = __byte_perm(w[0], w[1], 0x7531), b1 = __byte_perm(w[2], w[3], 0x7531);
+    w[0] = a0, w[1] = a1, w[2] = b0, w[3] = b1;
+  }
+  uint4* row = reinterpret_cast<uint4*>(dst + run_v_codes(D) + (g * kGroup + 2 * b) * 8);
+  if (hi - lo == kRun) {
+    *row = make_uint4(w[0], w[1], w[2], w[3]);
+  } else {
+    const uint64_t mask = ((1ull << (4 * (hi - lo))) - 1) << (4 * lo);
+    const uint32_t ml = static_cast<uint32_t>(mask), mh = static_cast<uint32_t>(mask >> 32);
+    const uint4 o = *row;
+    *row = make_uint4((o.x & ~ml) | (w[0] & ml), (o.y & ~mh) | (w[1] & mh),
+                      (o.z & ~ml) | (w[2] & ml), (o.w & ~mh) | (w[3] & mh));
+  }
+  uint8_t* vs = dst + run_v_scales(D) + g * kRun + 2 * b;
+  if (in[0] && in[1]) {
+    *reinterpret_cast<uint16_t*>(vs) = static_cast<uint16_t>(sc[0] | (sc[1] << 8));
+  } else if (in[0]) {
+    vs[0] = static_cast<uint8_t>(sc[0]);
+  } else if (in[1]) {
+    vs[1] = static_cast<uint8_t>(sc[1]);
+  }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
+  CacheTask t;
+  if (!cache_task<D>(p, t)) return;
+  const int lane = threadIdx.x & 31;
+  int64_t n;
+  int L;
+  if (!cache_span(p, t.i, n, L)) {
+    if (p.status && t.run == 0 && t.h == 0 && t.chunk == 0 && !t.is_v && lane == 0)
+      atomicOr(p.status + t.i, kDevBadLength);
+    return;
+  }
+  const int64_t run = (n >> 4) + t.run;
+  const int lo = static_cast<int>(max(n - run * kRun, int64_t(0)));
+  const int hi = static_cast<int>(min(n + L - run * kRun, int64_t(kRun)));
+  if (lo >= hi) return;
+  const uint8_t* src = cache_run<D>(p.c, t.i, t.h, run);
+  if (!src) {
+    if (p.status && t.h == 0 && t.chunk == 0 && !t.is_v && lane == 0)
+      atomicOr(p.status + t.i, kDevBadPage);
+    return;
+  }
+  const int b = lane & 7, g = t.chunk * 4 + (lane >> 3);
+  const float* gs = t.is_v ? p.c.v_scale : p.c.k_scale;
+  const float gv = gs ? __ldg(gs + t.h) : 1.0f;
+  uint64_t code[2];
+  uint32_t sc[2];
+  if (!t.is_v) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int tok = 2 * b + u;
+      code[u] = *reinterpret_cast<const uint64_t*>(src + (g >> 1) * 256 + tok * 16 + (g & 1) * 8);
+      sc[u] = src[run_k_scales(D) + tok * (D / kGroup) + g];
+    }
+  } else {
+    const uint4 o = *reinterpret_cast<const uint4*>(src + run_v_codes(D) + (g * kGroup + 2 * b) * 8);
+    uint32_t w[4] = {__byte_perm(o.x, o.z, 0x5140), __byte_perm(o.x, o.z, 0x7362),
+                     __byte_perm(o.y, o.w, 0x5140), __byte_perm(o.y, o.w, 0x7362)};
+    transpose_lanes8(w, b);  // byte c: channel c of the tokens 2b (low four bits), 2b+1
+    code[0] = code[1] = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t a = w[q] & 0x0f0f0f0fu, c = (w[q] >> 4) & 0x0f0f0f0fu;
+      a = (a | (a >> 4)) & 0x00ff00ffu, c = (c | (c >> 4)) & 0x00ff00ffu;
+      a = (a | (a >> 8)) & 0xffffu, c = (c | (c >> 8)) & 0xffffu;
+      code[0] |= static_cast<uint64_t>(a) << (16 * q);
+      code[1] |= static_cast<uint64_t>(c) << (16 * q);
+    }
+    const uint32_t two = *reinterpret_cast<const uint16_t*>(src + run_v_scales(D) + g * kRun + 2 * b);
+    sc[0] = two & 0xffu, sc[1] = two >> 8;
+  }
+  const CacheRows& rows = t.is_v ? p.v : p.k;
+  T* out = static_cast<T*>(rows.data) + t.i * rows.sb + t.h * rows.sh + g * kGroup;
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int tok = 2 * b + u;
+    if (tok < lo || tok >= hi) continue;
+    const uint32_t s2 = e4m3x2_to_f16x2(sc[u] | (sc[u] << 8));
+    float x[16];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t h[4];
+      e2m1x8_to_f16(static_cast<uint32_t>(code[u] >> (32 * q)), h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = h2_to_f2(h2_mul(h[e], s2));
+        x[8 * q + 2 * e] = __fmul_rn(f.x, gv);
+        x[8 * q + 2 * e + 1] = __fmul_rn(f.y, gv);
+      }
+    }
+    store_group(out + (run * kRun + tok - n) * rows.st, x);
+  }
+}
+
+}  // namespace sv

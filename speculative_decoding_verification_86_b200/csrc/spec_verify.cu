@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "conf.cuh"
 #include "engine.cuh"
+#include "host.cuh"
 #include "shard.cuh"
 #include "philox.cuh"
 #include "refine.cuh"
@@ -40,21 +41,6 @@ constexpr int kMaxTimed = 4096;
 // Automatic prefix tail: batches whose row segments make at most this many
 // waves of the engine's grid read their requests' later positions together.
 constexpr int64_t kTailWaves = 16;
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev) != cudaSuccess) return;
-    ok = (prev == dev) || (cudaSetDevice(dev) == cudaSuccess);
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-  }
-};
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 }  // namespace
 
@@ -245,8 +231,6 @@ spec_status carve(spec_verify_ctx* c) {
   if (cudaMemset(c->ws, 0, off) != cudaSuccess) return SPEC_ERR_CUDA;
   return SPEC_OK;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 void timing_mark(spec_verify_ctx* c, int cls, bool start, cudaStream_t s) {
   if (!(c->timing_mask & (1u << cls))) return;
@@ -769,6 +753,7 @@ spec_status spec_verify_run_host(spec_verify_ctx* ctx, const void* target_logits
   if (B < 0 || B > ctx->max_batch || k < 0 || k > ctx->max_k || V < 1 || V > ctx->max_vocab)
     return SPEC_ERR_INVALID_ARG;
   if (B == 0) return SPEC_OK;
+  if (dtype != SPEC_F32 && dtype != SPEC_BF16) return SPEC_ERR_INVALID_ARG;
   if (!target_logits || !out_accepted || !out_tokens || (k > 0 && !draft_tokens))
     return SPEC_ERR_INVALID_ARG;
   if (spec_status st = check_conf(ctx, conf); st != SPEC_OK) return st;

@@ -1,0 +1,531 @@
+"""The 4-bit block cache (spec_cache_*) against its definition in 64 bits: stored bytes and read-back
+values exactly, attention within bounds derived from its roundings."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_reference as ref
+from speculative_decoding_verification_86_b200 import binding
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def dev(cuda_device):
+    return cuda_device
+
+
+def make(dev, *, B, T, heads_q, heads_kv, d, page, lens, dtype=torch.bfloat16, seed=0, block=None, spare=2,
+         scales=True, width=None):
+    """A cache object, a pool of random bytes whose visible positions were written with the reference,
+    a table of shuffled pages, and a block's q, k, v."""
+    g = torch.Generator().manual_seed(seed)
+    rng = np.random.RandomState(seed)
+    per = [max(1, (n + T + page - 1) // page) for n in lens]
+    width = width or max(per)
+    num = sum(per) + spare
+    ids = rng.permutation(num)
+    table = np.full((B, width), -1, dtype=np.int32)
+    at = 0
+    for i, m in enumerate(per):
+        table[i, :m] = ids[at:at + m]
+        at += m
+    raw = rng.randint(0, 256, size=(num, heads_kv, page // 16, 18 * d)).astype(np.uint8)
+    ks = (0.01 * (0.5 + rng.rand(heads_kv))).astype(np.float32) if scales else None
+    vs = (0.003 * (0.5 + rng.rand(heads_kv))).astype(np.float32) if scales else None
+    most = max(max(lens), 1)
+    k = torch.randn((B, most, heads_kv, d), generator=g) * torch.exp(0.7 * torch.randn((heads_kv, d), generator=g))
+    v = torch.randn((B, most, heads_kv, d), generator=g)
+    raw = ref.write(raw, page, table, [0] * B, k.to(dtype), v.to(dtype), lens, ks, vs)
+    q = torch.randn((B, T, heads_q, d), generator=g).to(dtype)
+    kb = torch.randn((B, T, heads_kv, d), generator=g).to(dtype)
+    vb = torch.randn((B, T, heads_kv, d), generator=g).to(dtype)
+    return dict(cache=binding.BlockCache(dev, heads_q, heads_kv, d, page, max_batch=max(B, 1)), raw=raw, page=page,
+                table=table, lens=lens, block=block, ks=ks, vs=vs, q=q, k=kb, v=vb, dev=dev)
+
+
+def on(dev, x, dtype=torch.int32):
+    return None if x is None else torch.as_tensor(np.asarray(x)).to(dtype).to(dev)
+
+
+def device_args(s):
+    dev = s["dev"]
+    return dict(table=on(dev, s["table"]), cache_len=on(dev, s["lens"]), block_len=on(dev, s["block"]),
+                k_scale=on(dev, s["ks"], torch.float32), v_scale=on(dev, s["vs"], torch.float32))
+
+
+def check_attend(s, causal=True, window=0, scale=None, out=None, lse=None, q=None, cache=None):
+    """Write the block with the library, attend, compare both with the reference."""
+    dev = s["dev"]
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    cache = cache or s["cache"]
+    q = s["q"] if q is None else q
+    cache.write(s["k"].to(dev), s["v"].to(dev), pages, **a)
+    got, glse = cache.attend(q.to(dev), pages, causal=causal, window=window, scale=scale, out=out, lse=lse, **a)
+    torch.cuda.synchronize(dev)
+    assert cache.errors() == 0
+    raw = ref.write(s["raw"], s["page"], s["table"], s["lens"], s["k"], s["v"], s["block"], s["ks"], s["vs"])
+    assert np.array_equal(pages.cpu().numpy(), raw)
+    compare(s, raw, q, got, glse, causal, window, scale)
+    return got, glse
+
+
+def compare(s, raw, q, got, glse, causal=True, window=0, scale=None):
+    d = q.shape[-1]
+    sc = d ** -0.5 if scale is None else scale
+    out, l, a, size, done = ref.attend(raw, s["page"], s["table"], s["lens"], q, s["block"], sc, causal, window,
+                                       s["ks"], s["vs"])
+    tokens = max(s["lens"]) + q.shape[1]
+    tol, tol_lse = ref.attend_bounds(out, l, a, size, tokens, d, q.dtype)
+    g, gl = ref.to_np(got), ref.to_np(glse)
+    nan = np.isnan(out) & done[..., None, None]
+    assert np.array_equal(np.isnan(g) & done[..., None, None], nan)
+    ok = done[..., None, None] & ~nan
+    err = np.where(ok, np.abs(g - np.where(nan, 0, out)) - tol, -1)
+    assert err.max() <= 0, (err.max(), np.unravel_index(err.argmax(), err.shape))
+    nl = np.isnan(l) & done[..., None]
+    assert np.array_equal(np.isnan(gl) & done[..., None], nl)
+    inf = np.isneginf(l)
+    assert np.all(np.isneginf(gl[inf & done[..., None]]))
+    okl = done[..., None] & ~nl & ~inf
+    errl = np.where(okl, np.abs(np.where(okl, gl, 0) - np.where(okl, l, 0)) - tol_lse, -1)
+    assert errl.max() <= 0, (errl.max(), np.unravel_index(errl.argmax(), errl.shape))
+
+
+# ------------------------------------------------------------ write and read --
+
+@pytest.mark.parametrize("d,heads,page,T,lens,dtype,scales", [
+    (128, 2, 16, 1, [0], torch.bfloat16, True),
+    (128, 1, 64, 6, [0, 1, 15, 16, 17, 63, 64], torch.bfloat16, True),
+    (64, 3, 32, 5, [31, 27, 40], torch.float16, True),
+    (256, 1, 128, 17, [3, 120], torch.float32, True),
+    (128, 2, 256, 35, [250, 5], torch.bfloat16, False),
+    (64, 1, 16, 50, [7], torch.float32, False),
+])
+def test_write_stores_the_defined_bytes_and_read_returns_them(dev, d, heads, page, T, lens, dtype, scales):
+    B = len(lens)
+    block = [T, 0, 1, T, 2, T - 1, T][:B]
+    s = make(dev, B=B, T=T, heads_q=heads, heads_kv=heads, d=d, page=page, lens=lens, dtype=dtype, block=block,
+             scales=scales, seed=d + page)
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    status = torch.zeros(B, dtype=torch.int32, device=dev)
+    s["cache"].write(s["k"].to(dev), s["v"].to(dev), pages, status=status, **a)
+    raw = ref.write(s["raw"], page, s["table"], lens, s["k"], s["v"], block, s["ks"], s["vs"])
+    assert np.array_equal(pages.cpu().numpy(), raw)  # every other byte and half byte as it was
+    assert status.tolist() == [0] * B
+    # read the last positions back, from an odd start
+    pool = ref.Pool(raw, page)
+    start = [max(0, n - 3) for n in lens]
+    count = [n + b - st for n, b, st in zip(lens, block, start)]
+    rows = max(count) + 2
+    for out_dtype in (torch.float32, torch.bfloat16, torch.float16):
+        out = tuple(torch.full((B, rows, heads, d), 7.0, dtype=out_dtype, device=dev) for _ in range(2))
+        s["cache"].read(pages, a["table"], start=on(dev, start), count=on(dev, count), out=out,
+                        k_scale=a["k_scale"], v_scale=a["v_scale"], status=status)
+        for i in range(B):
+            for j in range(rows):
+                got = [o[i, j].cpu() for o in out]
+                if j >= count[i]:
+                    assert all(bool((x == 7.0).all()) for x in got)
+                    continue
+                for x, val, gs in zip(got, pool.get(s["table"][i], start[i] + j), (s["ks"], s["vs"])):
+                    gs = np.ones(heads, np.float32) if gs is None else gs
+                    want = (val.astype(np.float32) * gs[:, None]).astype(np.float32)
+                    assert torch.equal(x, torch.from_numpy(want).to(out_dtype))
+    assert status.tolist() == [0] * B
+
+
+def test_write_rounds_ties_to_even_and_keeps_signs_and_non_finite_groups(dev):
+    """Values on the midpoints of the codes, at the scales' ends, zeros of both signs, the type's
+    extremes, NaN and infinities: the stored bytes are the definition's."""
+    d, page = 64, 16
+    mids = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0])
+    rows = []
+    for s in (1.0, 2.0 ** -9, 448.0, 0.0703125, 1.125, 2.0 ** -6):
+        rows.append(np.concatenate([mids * s, -mids * s]))
+        rows.append(np.concatenate([np.nextafter(np.float32(mids * s), np.float32(0)), -mids[::-1] * s]))
+        rows.append(np.concatenate([np.nextafter(np.float32(mids * s), np.float32(1e9)), mids * s]))
+    rows += [np.zeros(16), -np.zeros(16), np.full(16, 2.0 ** -12), np.full(16, -1e-30), np.full(16, 3e38),
+             np.full(16, -2688.0), np.full(16, 2689.0)]
+    for special in (np.nan, np.inf, -np.inf):
+        x = np.linspace(-3, 3, 16)
+        x[5] = special
+        rows.append(x)
+    rng = np.random.RandomState(3)
+    while len(rows) % 4:
+        rows.append(rng.randn(16))
+    # e4m3 halfway cases of the scale itself
+    x = np.concatenate(rows).astype(np.float32).reshape(1, -1, 1, d)
+    T = x.shape[1]
+    table = np.arange((T + page - 1) // page, dtype=np.int32)[None]
+    raw = np.random.RandomState(0).randint(0, 256, size=(table.shape[1], 1, 1, 18 * d)).astype(np.uint8)
+    for dtype in (torch.float32, torch.bfloat16):
+        k = torch.from_numpy(x).to(dtype)
+        v = torch.flip(k, dims=[3]).contiguous()
+        for g in (None, np.array([0.37], np.float32)):
+            with binding.BlockCache(dev, 1, 1, d, page, max_batch=1) as c:
+                pages = torch.from_numpy(raw).to(dev)
+                c.write(k.to(dev), v.to(dev), pages, on(dev, table), on(dev, [0]),
+                        k_scale=on(dev, g, torch.float32), v_scale=on(dev, g, torch.float32))
+                want = ref.write(raw, page, table, [0], k, v, None, g, g)
+                assert np.array_equal(pages.cpu().numpy(), want)
+
+
+def test_write_takes_slices_of_a_fused_projection(dev):
+    s = make(dev, B=3, T=4, heads_q=4, heads_kv=2, d=64, page=16, lens=[5, 30, 0], seed=5)
+    a = device_args(s)
+    fused = torch.zeros((3, 4 + 2, 8 + 1, 64), dtype=torch.bfloat16, device=dev)
+    fused[:, 1:5, 4:6] = s["k"].to(dev)
+    fused[:, 1:5, 6:8] = s["v"].to(dev)
+    fused[:, 1:5, 0:4] = s["q"].to(dev)
+    part = fused[:, 1:5]
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    s["cache"].write(part[:, :, 4:6], part[:, :, 6:8], pages, **a)
+    raw = ref.write(s["raw"], 16, s["table"], s["lens"], s["k"], s["v"], None, s["ks"], s["vs"])
+    assert np.array_equal(pages.cpu().numpy(), raw)
+    # queries by heads first, outputs into a wider tensor
+    by_head = part[:, :, 0:4].transpose(1, 2).contiguous().transpose(1, 2)
+    wide = torch.full((3, 4, 6, 64), 9.0, dtype=torch.bfloat16, device=dev)
+    out, lse = s["cache"].attend(by_head, pages, out=wide[:, :, 1:5], **a)
+    compare(s, raw, s["q"], out, lse)
+    assert bool((wide[:, :, 0] == 9).all()) and bool((wide[:, :, 5] == 9).all())
+
+
+# ------------------------------------------------------------------ attention --
+
+@pytest.mark.parametrize("d,hq,hkv,page,T,lens,dtype", [
+    (128, 1, 1, 16, 1, [0], torch.bfloat16),
+    (128, 4, 1, 64, 1, [1, 15, 16, 127, 128, 129], torch.bfloat16),
+    (128, 8, 2, 16, 6, [0, 3, 122, 250, 255, 256, 300], torch.bfloat16),
+    (128, 8, 2, 64, 6, [700, 0, 64], torch.float16),
+    (64, 6, 2, 32, 5, [0, 11, 500, 129], torch.bfloat16),
+    (64, 16, 1, 128, 2, [260, 1], torch.float16),
+    (256, 4, 2, 16, 3, [0, 140, 257], torch.bfloat16),
+    (256, 8, 1, 64, 4, [200, 30], torch.float16),
+    (128, 5, 1, 256, 17, [90, 0, 250], torch.bfloat16),
+    (128, 8, 1, 64, 17, [100, 333], torch.float16),
+    (256, 16, 1, 32, 9, [77], torch.bfloat16),
+    (64, 7, 7, 16, 40, [20, 0], torch.bfloat16),
+])
+@pytest.mark.parametrize("mask", ["causal", "all", "window"])
+def test_attend_matches_its_definition(dev, d, hq, hkv, page, T, lens, dtype, mask):
+    B = len(lens)
+    block = None if B == 1 else [T, max(1, T // 2), T, 1, T, T, T][:B]
+    s = make(dev, B=B, T=T, heads_q=hq, heads_kv=hkv, d=d, page=page, lens=lens, dtype=dtype, block=block,
+             seed=d + hq + page)
+    check_attend(s, causal=mask != "all", window=33 if mask == "window" else 0)
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 17, 128, 200, 10 ** 9])
+def test_attend_window_edges(dev, window):
+    s = make(dev, B=3, T=7, heads_q=2, heads_kv=1, d=64, page=16, lens=[0, 150, 271], block=[7, 5, 7], seed=11)
+    check_attend(s, window=window)
+    check_attend(s, window=window, causal=False)
+
+
+def test_attend_scale_signs_and_sizes(dev):
+    """Scores of thousands (a softmax on one token), a negative scale, scale 0 (a plain mean)."""
+    s = make(dev, B=2, T=3, heads_q=4, heads_kv=2, d=128, page=32, lens=[200, 33], seed=21)
+    for scale in (40.0, -0.3, 0.0, 1e-6):
+        check_attend(s, scale=scale)
+
+
+def test_attend_growing_scores_move_the_maximum(dev):
+    """Keys that grow along the context raise each row's running maximum again and again."""
+    d, n = 64, 1000
+    s = make(dev, B=1, T=2, heads_q=2, heads_kv=1, d=d, page=16, lens=[n], seed=31, scales=False)
+    base = torch.randn(d, generator=torch.Generator().manual_seed(1))
+    k = (base * torch.linspace(0.01, 9.0, n)[:, None]).view(1, n, 1, d)
+    v = torch.randn((1, n, 1, d), generator=torch.Generator().manual_seed(2))
+    s["raw"] = ref.write(s["raw"], 16, s["table"], [0], k, v)
+    q = torch.stack([base, -base]).view(1, 1, 2, d).expand(1, 2, 2, d).to(torch.bfloat16).contiguous()
+    check_attend(s, q=q, scale=0.25)
+
+
+def test_attend_queries_of_all_sizes(dev):
+    """Rows at the ends of bf16's range: the row's power-of-two scaling keeps their products exact."""
+    s = make(dev, B=1, T=4, heads_q=4, heads_kv=1, d=128, page=16, lens=[100], seed=41, scales=False)
+    q = s["q"].float()
+    q[0, 0, 0] *= 1e30
+    q[0, 0, 1] *= 1e-30
+    q[0, 1, 2] = 0
+    q[0, 1, 3] = -0.0
+    q[0, 2, 0, :64] *= 1e-9
+    q[0, 2, 1] *= 3e36
+    q[0, 3, 1] = 1e-40
+    q = q.to(torch.bfloat16)
+    check_attend(s, q=q)
+    s["q"] = q
+    check_attend(s, q=(s["q"].float().clamp(-60000, 60000)).half(), scale=1e-3)
+
+
+def test_nothing_behind_the_end_is_judged(dev):
+    """Bytes of ones (NaN scales) in every position that no row sees, and a table whose other entries
+    name no page."""
+    s = make(dev, B=3, T=5, heads_q=4, heads_kv=2, d=128, page=64, lens=[70, 0, 129], block=[5, 2, 3], seed=51,
+             width=9)
+    raw = np.full_like(s["raw"], 255)
+    keep = ref.Pool(s["raw"], 64)
+    pool = ref.Pool(raw, 64)
+    g = torch.Generator().manual_seed(8)
+    for i, n in enumerate(s["lens"]):
+        if n:
+            k = torch.randn((1, n, 2, 128), generator=g)
+            pool.raw = ref.write(pool.raw, 64, s["table"][i:i + 1], [0], k, k.flip(1), None, s["ks"], s["vs"])
+    s["raw"] = pool.raw
+    assert keep.raw.shape == pool.raw.shape
+    s["table"][1, 3:] = 2 ** 31 - 1
+    out = torch.full((3, 5, 4, 128), 5.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((3, 5, 4), 5.0, device=dev)
+    check_attend(s, out=out, lse=lse)
+    for i, b in enumerate(s["block"]):
+        assert bool((out[i, b:] == 5).all()) and bool((lse[i, b:] == 5).all())
+
+
+def test_nan_tokens_reach_only_the_rows_that_see_them(dev):
+    """A NaN key, a NaN value group and an infinite query element; the rows before the token, and those
+    whose window has left it, are as if it were not there."""
+    s = make(dev, B=2, T=6, heads_q=4, heads_kv=2, d=128, page=16, lens=[140, 9], seed=61)
+    s["k"][0, 3, 0, 17] = float("nan")
+    s["v"][0, 4, 1, 40] = float("inf")
+    s["v"][1, 2, 0, 3] = float("nan")
+    check_attend(s)
+    check_attend(s, window=2)
+    check_attend(s, causal=False)
+    q = s["q"].clone()
+    q[0, 1, 2, 5] = float("inf")
+    q[1, 0, 0, 5] = float("nan")
+    q[1, 4, 3] = float("-inf")
+    check_attend(s, q=q)
+
+
+def test_bad_pages_are_masked_and_bad_lengths_skipped(dev):
+    s = make(dev, B=5, T=4, heads_q=2, heads_kv=1, d=64, page=16, lens=[40, 100, 10, 60, 7], seed=71)
+    s["table"][0, 1] = -1               # tokens 16..31 of request 0
+    s["table"][2, 0] = s["raw"].shape[0]  # all of request 2
+    s["lens"][1] = -3
+    s["lens"][3] = 16 * s["table"].shape[1] - 3
+    dev_, a = s["dev"], device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev_)
+    status = torch.zeros(5, dtype=torch.int32, device=dev_)
+    s["cache"].write(s["k"].to(dev_), s["v"].to(dev_), pages, status=status, **a)
+    L, P = binding.DEV_BAD_LENGTH, binding.DEV_BAD_PAGE
+    assert status.tolist() == [0, L, P, L, 0]
+    raw = ref.write(s["raw"], 16, s["table"], s["lens"], s["k"], s["v"], None, s["ks"], s["vs"])
+    assert np.array_equal(pages.cpu().numpy(), raw)
+    out = torch.full((5, 4, 2, 64), 3.0, dtype=torch.bfloat16, device=dev_)
+    lse = torch.full((5, 4, 2), 3.0, device=dev_)
+    status.zero_()
+    s["cache"].attend(s["q"].to(dev_), pages, out=out, lse=lse, status=status, **a)
+    assert status.tolist() == [P, L, P, L, 0]
+    compare(s, raw, s["q"], out, lse)
+    assert bool((out[2] == 0).all()) and bool(torch.isneginf(lse[2]).all())
+    for i in (1, 3):
+        assert bool((out[i] == 3).all()) and bool((lse[i] == 3).all())
+    status.zero_()
+    o = tuple(torch.full((5, 40, 1, 64), 3.0, device=dev_) for _ in range(2))
+    s["cache"].read(pages, a["table"], start=on(dev_, [0, -1, 0, 16 * 30, 0]), count=on(dev_, [40, 3, 3, 40, 7]),
+                    out=o, status=status)
+    assert status.tolist() == [P, L, P, L, 0]
+    assert bool((o[0][0, 16:32] == 3).all()) and bool((o[1][2] == 3).all()) and bool((o[0][3] == 3).all())
+    assert not bool((o[0][0, 32:40] == 3).any())
+
+
+def test_attend_long_context_of_one_request(dev):
+    """One request split over the whole GPU and joined; the reference runs on the device in fp64."""
+    d, hq, hkv, page, n, T = 128, 8, 2, 64, 30011, 6
+    rng = np.random.RandomState(0)
+    width = (n + T + page - 1) // page
+    cache = binding.BlockCache(dev, hq, hkv, d, page, max_batch=1)
+    pages = cache.alloc(width + 3)
+    table = torch.from_numpy(rng.permutation(width + 3)[:width].astype(np.int32)).to(dev)[None]
+    g = torch.Generator(device=dev).manual_seed(3)
+    k = torch.randn((1, n + T, hkv, d), generator=g, device=dev, dtype=torch.bfloat16)
+    v = torch.randn((1, n + T, hkv, d), generator=g, device=dev, dtype=torch.bfloat16)
+    q = torch.randn((1, T, hq, d), generator=g, device=dev, dtype=torch.bfloat16)
+    cache.write(k, v, pages, table, torch.zeros(1, dtype=torch.int32, device=dev))
+    length = torch.tensor([n], dtype=torch.int32, device=dev)
+    kk, vv = cache.read(pages, table, rows=n + T, dtype=torch.float32)
+    for window in (0, 20000):
+        out, lse = cache.attend(q, pages, table, length, window=window)
+        again, lse2 = cache.attend(q, pages, table, length, window=window)
+        assert torch.equal(out, again) and torch.equal(lse, lse2)  # same call, same bits
+        for h in range(hq):
+            x = (q[0, :, h].double() @ kk[0, :, h // 4].double().T) * d ** -0.5
+            pos = torch.arange(n + T, device=dev)
+            j = n + torch.arange(T, device=dev)[:, None]
+            see = (pos <= j) & ((pos > j - window) if window else True)
+            x = x.masked_fill(~see, -math.inf)
+            p = torch.softmax(x, -1)
+            want, a = p @ vv[0, :, h // 4].double(), p @ vv[0, :, h // 4].double().abs()
+            size = (q[0, :, h].double().abs() @ kk[0, :, h // 4].double().abs().T).max() * d ** -0.5
+            # fp32 sums of a tile's 128 tokens and of the tiles: 128 + 30017 / 128 + parts terms deep
+            tol, tol_lse = ref.attend_bounds(want.cpu().numpy(), torch.logsumexp(x, -1).cpu().numpy(),
+                                             a.cpu().numpy(), np.full(T, float(size)), 600, d, q.dtype)
+            assert np.all(np.abs(ref.to_np(out[0, :, h]) - want.cpu().numpy()) <= tol)
+            assert np.all(np.abs(ref.to_np(lse[0, :, h]) - torch.logsumexp(x, -1).cpu().numpy()) <= tol_lse)
+    assert cache.errors() == 0
+
+
+def test_pages_behind_4_gib_and_rows_behind_2_gib(dev):
+    """Page offsets and row offsets that pass 32 bits."""
+    d, page = 256, 256
+    s = make(dev, B=1, T=3, heads_q=2, heads_kv=2, d=d, page=page, lens=[300], seed=81)
+    per = s["raw"][0].size
+    num = (5 << 30) // per
+    pages = torch.empty((num,) + s["raw"].shape[1:], dtype=torch.uint8, device=dev)
+    high = {int(p): num - 1 - 7 * e for e, p in enumerate(s["table"][0])}
+    for p, to in high.items():
+        pages[to] = torch.from_numpy(s["raw"][p]).to(dev)
+    a = device_args(s)
+    a["table"] = on(dev, [[high[int(p)] for p in s["table"][0]]])
+    big = torch.empty(3 * (1 << 29) + 3 * 2 * d, dtype=torch.bfloat16, device=dev)
+    k = torch.as_strided(big, (1, 3, 2, d), (8, 1 << 29, d, 1))
+    k.copy_(s["k"])
+    s["cache"].write(k, s["v"].to(dev), pages, **a)
+    k.copy_(s["q"])
+    out, lse = s["cache"].attend(k, pages, **a)
+    raw = ref.write(s["raw"], page, s["table"], s["lens"], s["k"], s["v"], None, s["ks"], s["vs"])
+    for p, to in high.items():
+        assert np.array_equal(pages[to].cpu().numpy(), raw[p])
+    compare(s, raw, s["q"], out, lse)
+
+
+def test_empty_calls_do_nothing(dev):
+    c = binding.BlockCache(dev, 2, 1, 64, 16, max_batch=4)
+    pages = c.alloc(2)
+    pages.fill_(3)
+    e = torch.zeros((0, 3), dtype=torch.int32, device=dev)
+    n = torch.zeros(0, dtype=torch.int32, device=dev)
+    k = torch.zeros((0, 2, 1, 64), dtype=torch.bfloat16, device=dev)
+    c.write(k, k, pages, e, n)
+    out, lse = c.attend(torch.zeros((0, 2, 2, 64), dtype=torch.bfloat16, device=dev), pages, e, n)
+    assert out.shape == (0, 2, 2, 64) and lse.shape == (0, 2, 2)
+    t = torch.zeros((2, 3), dtype=torch.int32, device=dev)
+    n = torch.zeros(2, dtype=torch.int32, device=dev)
+    k = torch.zeros((2, 0, 1, 64), dtype=torch.bfloat16, device=dev)
+    c.write(k, k, pages, t, n)
+    assert c.attend(torch.zeros((2, 0, 2, 64), dtype=torch.bfloat16, device=dev), pages, t, n)[0].numel() == 0
+    assert c.read(pages, t, rows=0)[0].shape == (2, 0, 1, 64)
+    assert bool((pages == 3).all())
+
+
+def test_captured_step_replays_with_new_lengths(dev):
+    """write + attend in a CUDA graph; cache_len, block_len, the table and the block change between the
+    replays."""
+    s = make(dev, B=3, T=4, heads_q=4, heads_kv=2, d=64, page=16, lens=[60, 7, 130], block=[4, 4, 4], seed=91)
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    k, v, q = s["k"].to(dev), s["v"].to(dev), s["q"].to(dev)
+    out = torch.zeros_like(q)
+    lse = torch.zeros((3, 4, 4), device=dev)
+
+    def step():
+        s["cache"].write(k, v, pages, **a)
+        s["cache"].attend(q, pages, out=out, lse=lse, **a)
+
+    side = torch.cuda.Stream(dev)
+    side.wait_stream(torch.cuda.current_stream(dev))
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream(dev).wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    raw = s["raw"]
+    for lens, block in (([60, 7, 130], [4, 4, 4]), ([2, 9, 40], [1, 4, 0]), ([61, 0, 133], [4, 2, 1])):
+        s["lens"], s["block"] = lens, block
+        a["cache_len"].copy_(on(dev, lens))
+        a["block_len"].copy_(on(dev, block))
+        pages.copy_(torch.from_numpy(raw))
+        graph.replay()
+        torch.cuda.synchronize(dev)
+        want = ref.write(raw, 16, s["table"], lens, s["k"], s["v"], block, s["ks"], s["vs"])
+        assert np.array_equal(pages.cpu().numpy(), want)
+        compare(s, want, s["q"], out, lse)
+    del graph
+
+
+def test_two_streams_with_a_context_each(dev):
+    s = make(dev, B=4, T=3, heads_q=8, heads_kv=2, d=128, page=16, lens=[300, 11, 800, 64], seed=101)
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    s["cache"].write(s["k"].to(dev), s["v"].to(dev), pages, **a)
+    q = s["q"].to(dev)
+    want, wl = s["cache"].attend(q, pages, **a)
+    other = binding.BlockCache(dev, 8, 2, 128, 16, max_batch=4)
+    torch.cuda.synchronize(dev)
+    streams = [torch.cuda.Stream(dev), torch.cuda.Stream(dev)]
+    got = [[], []]
+    for _ in range(20):
+        for st, c, g in zip(streams, (s["cache"], other), got):
+            with torch.cuda.stream(st):
+                g.append(c.attend(q, pages, **a))
+    torch.cuda.synchronize(dev)
+    for g in got:
+        for out, lse in g:
+            assert torch.equal(out, want) and torch.equal(lse, wl)
+    assert s["cache"].errors() == 0 and other.errors() == 0
+
+
+def test_gpu_refusals(dev):
+    c = binding.BlockCache(dev, 4, 2, 64, 16, max_batch=2)
+    pages = c.alloc(4)
+    t = torch.zeros((2, 2), dtype=torch.int32, device=dev)
+    n = torch.zeros(2, dtype=torch.int32, device=dev)
+    k = torch.zeros((2, 3, 2, 64), dtype=torch.bfloat16, device=dev)
+    q = torch.zeros((2, 3, 4, 64), dtype=torch.bfloat16, device=dev)
+    with pytest.raises(ValueError):
+        c.write(k, k[:, :2], pages, t, n)
+    with pytest.raises(TypeError):
+        c.write(k, k.half(), pages, t, n)
+    with pytest.raises(TypeError):
+        c.write(k.double(), k.double(), pages, t, n)
+    with pytest.raises(ValueError):
+        c.write(k[:, :, :1], k[:, :, :1], pages, t, n)
+    with pytest.raises(ValueError):
+        c.write(k.cpu(), k.cpu(), pages, t, n)
+    with pytest.raises(ValueError):
+        c.write(k, k, pages, t, None)
+    with pytest.raises(ValueError):
+        c.write(k, k, pages, t, n[:1])
+    with pytest.raises(TypeError):
+        c.write(k, k, pages, t.long(), n)
+    with pytest.raises(ValueError):
+        c.write(k, k, pages[:, :1], t, n)
+    with pytest.raises(ValueError):
+        c.write(k, k, pages, t.t().contiguous().t(), n)
+    with pytest.raises(TypeError):
+        c.attend(q.float(), pages, t, n)
+    with pytest.raises(ValueError):
+        c.attend(q, pages, t, n, out=q[:, :2])
+    with pytest.raises(ValueError):
+        c.attend(q, pages, t, n, out=q[:, :1].expand(2, 3, 4, 64))
+    with pytest.raises(ValueError):
+        c.attend(q, pages, t, n, lse=torch.zeros((2, 3, 2), device=dev))
+    with pytest.raises(ValueError):
+        c.attend(q, pages, t, n, k_scale=torch.ones(3, device=dev))
+    with pytest.raises(binding.SpecVerifyError) as e:
+        c.attend(q, pages, t, n, window=-1)
+    assert e.value.status == binding.SPEC_ERR_INVALID_ARG
+    with pytest.raises(binding.SpecVerifyError):
+        c.attend(q, pages, t, n, scale=float("nan"))
+    flat = torch.zeros(2 * 3 * 4 * 64 + 8, dtype=torch.bfloat16, device=dev)
+    with pytest.raises(binding.SpecVerifyError) as e:
+        c.attend(flat[1:1 + q.numel()].view(q.shape), pages, t, n)
+    assert e.value.status == binding.SPEC_ERR_UNSUPPORTED
+    with pytest.raises(binding.SpecVerifyError) as e:
+        big = torch.zeros((3, 1, 2, 64), dtype=torch.bfloat16, device=dev)
+        c.write(big, big, pages, torch.zeros((3, 1), dtype=torch.int32, device=dev), torch.zeros(3, dtype=torch.int32, device=dev))
+    assert e.value.status == binding.SPEC_ERR_INVALID_ARG
+    for bad in (dict(head_dim=96), dict(page_size=24), dict(page_size=8), dict(head_dim=512)):
+        with pytest.raises(binding.SpecVerifyError) as e:
+            binding.BlockCache(dev, **dict(dict(heads_q=4, heads_kv=2, head_dim=64, page_size=16), **bad))
+        assert e.value.status == binding.SPEC_ERR_UNSUPPORTED
+    with pytest.raises(binding.SpecVerifyError) as e:
+        binding.BlockCache(dev, heads_q=5, heads_kv=2, head_dim=64, page_size=16)
+    assert e.value.status == binding.SPEC_ERR_INVALID_ARG
