@@ -476,7 +476,7 @@ spec_status spec_lmhead_errors(spec_lmhead_ctx* ctx, uint32_t* out);
  * read a page.
  *
  * Requests that cannot be served.  A request with cache_len < 0, or whose
- * positions pass table_width * page_size, is skipped: nothing is written for
+ * positions pass table_width * page_size (or 2^31 - 256), is skipped: nothing is written for
  * it and its output rows stay as they were (SPEC_DEV_BAD_LENGTH).  A page
  * number outside [0, num_pages) is never followed (SPEC_DEV_BAD_PAGE): tokens
  * on it are not written, read rows of it stay as they were, and the attention
@@ -513,7 +513,7 @@ spec_status spec_cache_page_bytes(int heads_kv, int head_dim, int page_size, siz
  * (a multiple of heads_kv; query head h reads key/value head
  * h / (heads_q / heads_kv)), batches up to max_batch (<= 65535).  It
  * owns the workspace in which attention over one long context is joined, about
- * 0.3 MB per SM at most.  One context per concurrently used stream, as above:
+ * 64 KB per SM at most.  One context per concurrently used stream, as above:
  * captured graphs that use one context must not be replayed at the same time.
  * The context holds no cache contents: any number of layers can use it. */
 spec_status spec_cache_init(spec_cache_ctx** ctx, int device, int max_batch, int heads_q,

@@ -1,8 +1,45 @@
 // Attention of a request's block over its 4-bit cache.
+//
+// For one key/value head, the R = block tokens x query heads of the group rows
+// that share its keys are one problem: S^T = K Q^T and O^T = V^T P^T, with the
+// cache's tokens (for S) and channels (for O) on the 128 rows of a tcgen05 tile
+// and the few query rows on its N.  So every 4-bit code is decoded once for all
+// R rows, and is decoded where the tensor core reads it: a thread owns one token
+// of the keys (or one channel of the values), converts its codes to fp16 times
+// the group's scale -- exact, six significant bits -- and stores them as its
+// lane of the A operand in tensor memory.  Shared memory carries the packed
+// bytes and the small B operands (Q, P) only; the decoded tile, 3.6 times the
+// bytes, never passes through it.
+//
+// One persistent CTA per SM walks an equal share of all (request, head, tile of
+// 128 tokens) units in order, so a long context is split over many CTAs and
+// short ones share one.  Roles (warps):
+//   producer      bulk copies of the runs of a tile into a ring of stages;
+//   K 0-3, V 4-7  decode into tensor memory, lane = token / channel;
+//   MMA           one thread issues S(t+1) before O(t), so the softmax of one
+//                 tile overlaps the products of its neighbours;
+//   softmax       lane = token, registers = query rows: S from tensor memory,
+//                 P (fp16) to shared memory.  The reference maximum of a row
+//                 is raised only when a score passes it by 2^7 (a vote of the
+//                 warps); then, and only then, O is rescaled in tensor memory;
+//   epilogue      loads and converts the next segment's Q, and writes O of the
+//                 finished one: final rows, or (a segment cut by a CTA's share)
+//                 unnormalised fp32 partials, which k_attend_join adds in the
+//                 order of the CTAs.
+// Every wait is bounded in time (mbar_wait); a wait that runs out raises the
+// error word, the roles drain what they issued and leave, and TMEM is freed.
 #pragma once
+#include <climits>
+
 #include "cache.cuh"
+#include "ptx.cuh"
 
 namespace sv {
+
+constexpr int kTile = 128;          // tokens of a tile: the rows of S^T
+constexpr int kTileRuns = kTile / kRun;
+constexpr float kLift = 8.0f;       // P = 2^(x - max + kLift): keeps small P out of fp16's subnormals
+constexpr float kRaise = kLift + 7.0f;  // a P past 2^15 raises the row's reference
 
 struct AttendParams {
   CacheView c;
@@ -10,105 +47,1155 @@ struct AttendParams {
   const int32_t* cache_len;
   const int32_t* block_len;  // nullptr: T
   int B, T, heads_q, group;  // group: query heads per key/value head
+  int rp;                    // query rows of a row tile
+  int bf16;                  // q and out are bf16 (else fp16)
   float scale;
   int causal, window;
   float* lse;  // [B, T, heads_q] or nullptr
   uint32_t* status;
+  // workspace
+  float* part_o;   // [2 grid][NP][D]: unnormalised rows of a CTA's cut segments
+  float2* part_l;  // [2 grid][NP]: (reference exponent, sum)
+  struct AttendCut* cuts;  // [grid]
+  unsigned* error;
 };
 
-// One CTA per query row; thread = token of a tile of 128 for the scores, then
-// thread = channel for the values.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) k_attend(AttendParams p) {
-  __shared__ float q[D], pr[128], red[4];
-  const int hq = blockIdx.x, j = blockIdx.y, i = blockIdx.z, t = threadIdx.x;
-  const int64_t n = __ldg(p.cache_len + i);
-  const int L = p.block_len ? min(max(__ldg(p.block_len + i), 0), p.T) : p.T;
-  if (n < 0 || n + L > p.c.capacity) {
-    if (p.status && hq == 0 && j == 0 && t == 0) atomicOr(p.status + i, kDevBadLength);
-    return;
+// A segment that is cut at the start of a CTA's share: which rows, and which
+// CTAs hold its parts (first: slot 1, the others: slot 0).
+struct AttendCut {
+  int i, h, row0, rows;
+  int first, last;  // last < 0: nothing to join here
+  int pad[2];
+};
+
+template <int D, int NP>
+struct AttendGeo {
+  static constexpr int kMT = (D + 127) / 128;   // tiles of 128 channels of O^T
+  static constexpr int kKB = D > 128 ? 1 : 2;   // K buffers in tensor memory
+  static constexpr int kVB = 2;
+  static constexpr int kOB = D > 128 && NP > 16 ? 1 : 2;
+  static constexpr int kKCols = D / 2;          // 32-bit columns of one K buffer
+  static constexpr int kVCols = 64 * kMT;
+  static constexpr int kTmemK = 0;
+  static constexpr int kTmemV = kTmemK + kKB * kKCols;
+  static constexpr int kTmemS = kTmemV + kVB * kVCols;
+  static constexpr int kTmemO = kTmemS + 2 * NP;
+  static constexpr int kTmemUsed = kTmemO + kOB * kMT * NP;
+  static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
+  static_assert(kTmemUsed <= 512, "tensor memory");
+  static constexpr int kSoftGroups = NP > 32 ? 2 : 1;  // warpgroups of the softmax, by columns
+  static constexpr int kCW = NP / kSoftGroups;         // query rows per softmax thread
+  static constexpr int kSoftWarps = 4 * kSoftGroups;
+  static constexpr int kWarpEpi = 8;
+  static constexpr int kWarpSoft = 12;
+  static constexpr int kWarpLoad = kWarpSoft + kSoftWarps;
+  static constexpr int kWarpMma = kWarpLoad + 1;
+  static constexpr int kThreads = 32 * (kWarpMma + 1);
+  static constexpr int kGroups = D / kGroup;
+  static constexpr uint32_t kStageBytes = kTileRuns * run_bytes(D);
+  static constexpr uint32_t kQBytes = NP * D * 2;
+  static constexpr uint32_t kPBytes = NP * kTile * 2;
+  static constexpr uint32_t kFixed = 2 * kQBytes + 2 * kPBytes + 4 * 512 * kMT + 8192;
+  static constexpr int kStages = static_cast<int>((227 * 1024 - 1024 - kFixed) / kStageBytes) < 8
+                                     ? static_cast<int>((227 * 1024 - 1024 - kFixed) / kStageBytes)
+                                     : 8;
+  static_assert(kStages >= 3, "stages");
+  static constexpr size_t kSmemBytes = 1024 + kFixed + kStages * kStageBytes;
+  static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NP >> 3) << 17) | (8u << 24);
+};
+
+template <int D, int NP>
+struct alignas(16) AttendShared {
+  using G = AttendGeo<D, NP>;
+  uint64_t full[8], empty[8];
+  uint64_t kready[2], kfree[2], vready[2], vfree[2];
+  uint64_t sfull[2], sfree[2], pready[2], pfree[2];
+  uint64_t qready[2], oready[2], ofree[2], lready[2];
+  uint64_t drain;
+  unsigned long long nan_rows[2][G::kGroups];  // rows of O[ob] that see a NaN of the value group
+  uint32_t valid[8];   // per stage: runs that were copied
+  uint32_t kvalid[4];  // the same by tile, for the softmax (which lags the stages)
+  alignas(16) float cs[2][NP];  // log2 units of one unit of S, per query row
+  int2 lim[2][NP];      // visible tokens of a row, counted from the segment's first run
+  float mref[NP];       // running maximum (log2 units)
+  alignas(16) float mr[NP];  // subtracted exponent: mref - kLift, 0 while nothing was seen
+  float fac[NP];
+  float red[4][NP];
+  float lsum[2][4][NP];
+  float mout[2][NP];
+  long long scan[32];
+  long long unit0;      // this CTA's share: first unit, and where it lies
+  long long units;      // number of units
+  long long total;
+  int start_i;
+  long long start_off;
+  uint32_t tmem;
+  int abort;
+};
+
+// ---------------------------------------------------------------- helpers --
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t t, float* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+                 "=f"(r[7])
+               : "r"(t));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t t, const float* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
+               "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16};" ::"r"(t),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem], fp16 operands, fp32 accumulator.
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Barrier `id` of 128 threads; true if `pred` holds in any of them.
+__device__ __forceinline__ bool group_any(int id, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(pred))
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void group_sync(int id) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory");
+}
+
+// ------------------------------------------------------------- work shares --
+// A request's units, in order: head, row tile, token tile.
+struct AttendReq {
+  int64_t n;
+  int L;
+  int64_t per_head;  // units of one head
+};
+
+// Row tile rt of a request: its rows, the positions it reads, and the token
+// tiles that cover them from its first position's run on.
+struct AttendSeg {
+  int i, h, row0, rows;
+  int64_t run0;          // first run
+  int tiles;             // token tiles of the whole segment
+  int t0, t1;            // this CTA's
+  int lo, hi;            // visible to any row, in tokens from run0
+  int full_lo, full_hi;  // visible to every row
+  int j0;
+  int64_t n;
+  int L;
+};
+
+__device__ __forceinline__ void attend_rows(const AttendParams& p, const AttendReq& r, int rt, AttendSeg& s) {
+  s.row0 = rt * p.rp;
+  s.rows = min(p.rp, r.L * p.group - s.row0);
+  s.j0 = s.row0 / p.group;
+  const int j1 = (s.row0 + s.rows - 1) / p.group;
+  const int64_t hi = p.causal ? r.n + j1 + 1 : r.n + r.L;
+  const int64_t lo = p.window ? max(r.n + s.j0 + 1 - p.window, int64_t(0)) : 0;
+  s.run0 = lo >> 4;
+  const int64_t base = s.run0 << 4;
+  s.lo = static_cast<int>(lo - base);
+  s.hi = static_cast<int>(hi - base);
+  s.full_lo = p.window ? static_cast<int>(max(r.n + j1 + 1 - p.window, lo) - base) : s.lo;
+  s.full_hi = p.causal ? static_cast<int>(r.n + s.j0 + 1 - base) : s.hi;
+  s.tiles = (s.hi + kTile - 1) / kTile;
+  s.n = r.n;
+  s.L = r.L;
+}
+
+__device__ __forceinline__ int attend_row_tiles(const AttendParams& p, int L) {
+  return (L * p.group + p.rp - 1) / p.rp;
+}
+
+// Length of request i; per_head = 0 where it has nothing to compute.
+__device__ __forceinline__ bool attend_req(const AttendParams& p, int i, AttendReq& r) {
+  r.n = __ldg(p.cache_len + i);
+  r.L = p.block_len ? min(max(__ldg(p.block_len + i), 0), p.T) : p.T;
+  r.per_head = 0;
+  if (r.n < 0 || r.n + r.L > p.c.capacity) return false;
+  const int nrt = attend_row_tiles(p, r.L);
+  AttendSeg s;
+  for (int rt = 0; rt < nrt; ++rt) {
+    attend_rows(p, r, rt, s);
+    r.per_head += s.tiles;
   }
-  if (j >= L) return;
-  const int h = hq / p.group;
-  const T* src = static_cast<const T*>(p.q.data) + i * p.q.sb + j * p.q.st + hq * p.q.sh;
-  for (int c = t; c < D; c += 128) q[c] = static_cast<float>(src[c]);
-  const int64_t end = p.causal ? n + j + 1 : n + L;
-  const int64_t first = p.window ? max(n + j + 1 - p.window, int64_t(0)) : 0;
-  const float kx = p.scale * (p.c.k_scale ? __ldg(p.c.k_scale + h) : 1.0f);
-  float m = -INFINITY, l = 0.0f, acc[(D + 127) / 128] = {};
-  for (int64_t t0 = first & ~int64_t(15); t0 < end; t0 += 128) {
-    __syncthreads();
-    const int64_t pos = t0 + t;
-    float s = -INFINITY;
-    bool see = pos >= first && pos < end;
-    if (see) {
-      const uint8_t* r = cache_run<D>(p.c, i, h, pos >> 4);
-      const int tok = static_cast<int>(pos & 15);
-      if (!r) {
-        if (p.status) atomicOr(p.status + i, kDevBadPage);
+  return true;
+}
+
+// CTA c of n takes the units [total c / n, total (c + 1) / n); the CTA of a unit.
+__device__ __forceinline__ long long share_start(long long total, int c, int n) { return total * c / n; }
+__device__ __forceinline__ int share_of(long long total, long long unit, int n) {
+  return static_cast<int>(((unit + 1) * n - 1) / total);
+}
+
+struct AttendWalk {
+  long long left, off;
+  int i;
+  AttendReq r;
+  template <class SH>
+  __device__ __forceinline__ AttendWalk(const AttendParams& p, const SH& sh) {
+    left = sh.units;
+    off = sh.start_off;
+    i = sh.start_i;
+    if (left > 0) attend_req(p, i, r);
+  }
+  __device__ __forceinline__ bool next(const AttendParams& p, AttendSeg& s) {
+    if (left <= 0) return false;
+    while (off >= r.per_head * p.c.heads) {
+      off = 0;
+      ++i;
+      attend_req(p, i, r);
+    }
+    s.i = i;
+    s.h = static_cast<int>(off / r.per_head);
+    long long rem = off - s.h * r.per_head;
+    int rt = 0;
+    attend_rows(p, r, rt, s);
+    while (rem >= s.tiles) {
+      rem -= s.tiles;
+      attend_rows(p, r, ++rt, s);
+    }
+    s.t0 = static_cast<int>(rem);
+    s.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), rem + left));
+    off += s.t1 - s.t0;
+    left -= s.t1 - s.t0;
+    return true;
+  }
+};
+
+// All lanes of a warp leave a wait together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, error));
+}
+
+// ------------------------------------------------------------------- roles --
+template <int D, int NP>
+__device__ __forceinline__ void attend_producer(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages) {
+  using G = AttendGeo<D, NP>;
+  const int lane = threadIdx.x & 31;
+  AttendWalk walk(p, sh);
+  AttendSeg s;
+  uint32_t g = 0;
+  bool ok = true;
+  while (ok && walk.next(p, s)) {
+    // a lane looks up one run; 32 runs are four tiles
+    auto look_up = [&](int t) -> const uint8_t* {
+      const int run = t * kTileRuns + lane;
+      if (run * kRun >= s.hi || run >= s.t1 * kTileRuns) return nullptr;
+      const uint8_t* a = cache_run<D>(p.c, s.i, s.h, s.run0 + run);
+      if (!a && p.status) atomicOr(p.status + s.i, kDevBadPage);
+      return a;
+    };
+    const uint8_t* next = look_up(s.t0);
+    for (int t = s.t0; ok && t < s.t1; t += 4) {
+      const uint8_t* src = next;
+      if (t + 4 < s.t1) next = look_up(t + 4);
+      const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr);
+      for (int u = 0; u < 4 && t + u < s.t1; ++u, ++g) {
+        const int st = static_cast<int>(g % G::kStages);
+        if (!warp_wait(&sh.empty[st], ((g / G::kStages) & 1u) ^ 1u, &sh.abort, p.error)) {
+          ok = false;
+          break;
+        }
+        const uint32_t v = (have >> (8 * u)) & 0xffu;
+        if (lane == 0) {
+          sh.valid[st] = v;
+          mbar_expect_tx(&sh.full[st], __popc(v) * run_bytes(D));
+        }
+        __syncwarp();
+        if ((lane >> 3) == u && src)
+          bulk_load(stages + st * G::kStageBytes + (lane & 7) * run_bytes(D), src, run_bytes(D), &sh.full[st]);
+      }
+    }
+  }
+  if (!ok) {  // the copies this warp issued land before the CTA's memory goes away
+    for (uint32_t e = g > G::kStages ? g - G::kStages : 0; e < g; ++e) {
+      volatile int no_abort = 0;
+      mbar_wait(&sh.full[e % G::kStages], (e / G::kStages) & 1u, &no_abort, p.error);
+    }
+  }
+}
+
+template <int D, int NP>
+__device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages) {
+  using G = AttendGeo<D, NP>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tok = warp * 32 + lane;
+  const uint32_t row = (tok >> 4) * run_bytes(D) + (tok & 15) * 16;
+  const uint32_t scales = (tok >> 4) * run_bytes(D) + run_k_scales(D) + (tok & 15) * G::kGroups;
+  const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(warp * 32) << 16) + G::kTmemK;
+  const uint32_t total = static_cast<uint32_t>(sh.units);
+  for (uint32_t g = 0; g < total; ++g) {
+    const int st = static_cast<int>(g % G::kStages);
+    const uint32_t kb = g % G::kKB;
+    if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u, &sh.abort, p.error)) return;
+    const uint32_t base = stages + st * G::kStageBytes;
+    uint32_t sc[G::kGroups / 2];  // pairs of fp16 scales
+#pragma unroll
+    for (int u = 0; u < G::kGroups / 4; ++u) {
+      uint32_t w;
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(base + scales + 4 * u));
+      sc[2 * u] = e4m3x2_to_f16x2(w & 0xffffu);
+      sc[2 * u + 1] = e4m3x2_to_f16x2(w >> 16);
+    }
+    if (!warp_wait(&sh.kfree[kb], ((g / G::kKB) & 1u) ^ 1u, &sh.abort, p.error)) return;
+    tc_fence_after();
+    // K of tile g follows S of tile g - kKB, so the softmax has read S of tile
+    // g - 4 and its mask
+    if (tok == 0) sh.kvalid[g & 3] = sh.valid[st];
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      const uint4 w = lds128(base + row + c * 256);
+      uint32_t v[16];
+      const uint32_t s0 = __byte_perm(sc[c], 0, 0x1010), s1 = __byte_perm(sc[c], 0, 0x3232);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        uint32_t h[4];
+        e2m1x8_to_f16(ww[u], h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * u + e] = h2_mul(h[e], u < 2 ? s0 : s1);
+      }
+      tmem_st16(tmem + kb * G::kKCols + c * 16, v);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&sh.kready[kb]);
+      mbar_arrive(&sh.empty[st]);
+    }
+  }
+}
+
+// Rows of the segment that see a token (counted from run0).
+template <int D, int NP>
+__device__ __noinline__ unsigned long long attend_rows_seeing(const AttendParams& p, const AttendSeg& s, int token) {
+  unsigned long long m = 0;
+  const int64_t pos = (s.run0 << 4) + token;
+  for (int r = 0; r < s.rows; ++r) {
+    const int64_t at = s.n + (s.row0 + r) / p.group;
+    const bool see = (p.causal ? pos <= at : pos < s.n + s.L) && (!p.window || pos > at - p.window);
+    if (see) m |= 1ull << r;
+  }
+  return m;
+}
+
+template <int D, int NP>
+__device__ __forceinline__ void attend_values(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages,
+                                              uint32_t scratch) {
+  using G = AttendGeo<D, NP>;
+  const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+  const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(warp * 32) << 16) + G::kTmemV;
+  const bool mine = warp * 32 < D;  // D = 64 fills half of the tile's rows
+  scratch += warp * 512 * G::kMT;
+  AttendWalk walk(p, sh);
+  AttendSeg s;
+  uint32_t g = 0, ns = 0;
+  for (; walk.next(p, s); ++ns) {
+    for (int t = s.t0; t < s.t1; ++t, ++g) {
+      const int st = static_cast<int>(g % G::kStages);
+      const uint32_t vb = g % G::kVB;
+      if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u, &sh.abort, p.error)) return;
+      const uint32_t base = stages + st * G::kStageBytes;
+      const int tb = t * kTile;
+      const uint32_t valid = sh.valid[st];
+      const bool whole = valid == 0xffu && tb >= s.lo && tb + kTile <= s.hi;
+      if (mine) {
+        // this warp's scales (two groups of every 128 channels) to fp16, eight tokens a lane
+        const int sub = lane >> 2, grp = (lane >> 1) & 1, half = lane & 1;
+#pragma unroll
+        for (int mt = 0; mt < G::kMT; ++mt) {
+          const int group = mt * 8 + warp * 2 + grp;
+          uint2 w = lds64(base + sub * run_bytes(D) + run_v_scales(D) + group * 16 + half * 8);
+          if (!whole) {  // tokens that no row sees weigh nothing, whatever their bytes
+            const int first = tb + sub * 16 + half * 8;
+            uint32_t keep[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const bool in = ((valid >> sub) & 1u) && first + e >= s.lo && first + e < s.hi;
+              if (in) keep[e >> 2] |= 0xffu << (8 * (e & 3));
+            }
+            w.x &= keep[0];
+            w.y &= keep[1];
+          }
+          const uint32_t nan0 = __vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          const uint32_t nan1 = __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          if (__any_sync(0xffffffffu, (nan0 | nan1) != 0)) {
+            // A NaN group must not meet the zeros of P (0 NaN = NaN): it is taken
+            // out here, and the epilogue gives NaN to the rows that see it.
+            const uint32_t ob = ns % G::kOB;
+            if (!warp_wait(&sh.ofree[ob], ((ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error)) return;
+            if (nan0 | nan1) {
+#pragma unroll 1
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t bad = (e < 4 ? nan0 >> (8 * e) : nan1 >> (8 * (e - 4))) & 1u;
+                if (bad)
+                  atomicOr(&sh.nan_rows[ob][group],
+                           attend_rows_seeing<D, NP>(p, s, tb + sub * 16 + half * 8 + e));
+              }
+              w.x &= ~nan0;
+              w.y &= ~nan1;
+            }
+            __syncwarp();
+          }
+          sts128(scratch + mt * 512 + (sub * 2 + grp) * 32 + half * 16,
+                 make_uint4(e4m3x2_to_f16x2(w.x & 0xffffu), e4m3x2_to_f16x2(w.x >> 16),
+                            e4m3x2_to_f16x2(w.y & 0xffffu), e4m3x2_to_f16x2(w.y >> 16)));
+        }
+        __syncwarp();
+      }
+      if (!warp_wait(&sh.vfree[vb], ((g / G::kVB) & 1u) ^ 1u, &sh.abort, p.error)) return;
+      tc_fence_after();
+      if (mine) {
+#pragma unroll
+        for (int mt = 0; mt < G::kMT; ++mt) {
+          const uint32_t codes = base + run_v_codes(D) + (mt * 128 + warp * 32 + lane) * 8;
+          const uint32_t sc = scratch + mt * 512 + (lane >> 4) * 32;
+#pragma unroll
+          for (int sub = 0; sub < kTileRuns; sub += 2) {
+            uint32_t v[16];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint2 w = lds64(codes + (sub + x) * run_bytes(D));
+              const uint4 sa = lds128(sc + (sub + x) * 64), sb = lds128(sc + (sub + x) * 64 + 16);
+              uint32_t h[4];
+              e2m1x8_to_f16(w.x, h);
+              v[8 * x] = h2_mul(h[0], sa.x);
+              v[8 * x + 1] = h2_mul(h[1], sa.y);
+              v[8 * x + 2] = h2_mul(h[2], sa.z);
+              v[8 * x + 3] = h2_mul(h[3], sa.w);
+              e2m1x8_to_f16(w.y, h);
+              v[8 * x + 4] = h2_mul(h[0], sb.x);
+              v[8 * x + 5] = h2_mul(h[1], sb.y);
+              v[8 * x + 6] = h2_mul(h[2], sb.z);
+              v[8 * x + 7] = h2_mul(h[3], sb.w);
+            }
+            tmem_st16(tmem + vb * G::kVCols + mt * 64 + sub * 8, v);
+          }
+        }
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.vready[vb]);
+        mbar_arrive(&sh.empty[st]);
+      }
+    }
+  }
+}
+
+// One thread.  S of tile g is issued before O of tile g - 1.
+template <int D, int NP>
+__device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem,
+                                           uint32_t p_smem) {
+  using G = AttendGeo<D, NP>;
+  AttendWalk walk(p, sh);
+  AttendSeg s;
+  uint32_t g = 0, ns = 0;
+  bool ok = true;
+  int pend = 0;  // O of the previous tile: 0 none, else 1 | first << 1 | last << 2
+  uint32_t pend_ob = 0, pend_ns = 0;
+  auto issue_o = [&](uint32_t t) {  // tile t
+    const uint32_t sb = t & 1u, vb = t % G::kVB;
+    if (!mbar_wait(&sh.vready[vb], (t / G::kVB) & 1u, &sh.abort, p.error) ||
+        !mbar_wait(&sh.pready[sb], (t >> 1) & 1u, &sh.abort, p.error))
+      return false;
+    if ((pend & 2) &&
+        !mbar_wait(&sh.ofree[pend_ob], ((pend_ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error))
+      return false;
+    tc_fence_after();
+#pragma unroll
+    for (int mt = 0; mt < G::kMT; ++mt) {
+      const uint32_t d = sh.tmem + G::kTmemO + (pend_ob * G::kMT + mt) * NP;
+      const uint32_t a = sh.tmem + G::kTmemV + vb * G::kVCols + mt * 64;
+#pragma unroll
+      for (int kk = 0; kk < kTile / 16; ++kk) {
+        const uint64_t b = sw128_desc(p_smem + sb * G::kPBytes + (kk >> 2) * (NP * 128)) + 2 * (kk & 3);
+        umma_ts(d, a + 8 * kk, b, G::kIdesc, ((pend & 2) && kk == 0) ? 0u : 1u);
+      }
+    }
+    umma_commit<1>(&sh.vfree[vb]);
+    umma_commit<1>(&sh.pfree[sb]);
+    if (pend & 4) umma_commit<1>(&sh.oready[pend_ob]);
+    return true;
+  };
+  while (ok && walk.next(p, s)) {
+    const uint32_t qb = ns & 1u;
+    if (!mbar_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error)) {
+      ok = false;
+      break;
+    }
+    for (int t = s.t0; t < s.t1; ++t, ++g) {
+      const uint32_t sb = g & 1u, kb = g % G::kKB;
+      if (!mbar_wait(&sh.kready[kb], (g / G::kKB) & 1u, &sh.abort, p.error) ||
+          !mbar_wait(&sh.sfree[sb], ((g >> 1) & 1u) ^ 1u, &sh.abort, p.error)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t d = sh.tmem + G::kTmemS + sb * NP;
+      const uint32_t a = sh.tmem + G::kTmemK + kb * G::kKCols;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t b = sw128_desc(q_smem + qb * G::kQBytes + (kk >> 2) * (NP * 128)) + 2 * (kk & 3);
+        umma_ts(d, a + 8 * kk, b, G::kIdesc, kk > 0 ? 1u : 0u);
+      }
+      umma_commit<1>(&sh.kfree[kb]);
+      umma_commit<1>(&sh.sfull[sb]);
+      if (pend && !issue_o(g - 1)) {
+        ok = false;
+        break;
+      }
+      pend = 1 | (t == s.t0 ? 2 : 0) | (t == s.t1 - 1 ? 4 : 0);
+      pend_ob = ns % G::kOB;
+      pend_ns = ns;
+    }
+    ++ns;
+  }
+  if (ok && pend) ok = issue_o(g - 1);
+  if (!ok) {  // what was issued completes before tensor memory is released
+    umma_commit<1>(&sh.drain);
+    volatile int no_abort = 0;
+    mbar_wait(&sh.drain, 0, &no_abort, p.error);
+  }
+}
+
+template <int D, int NP>
+__device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t p_smem) {
+  using G = AttendGeo<D, NP>;
+  constexpr int CW = G::kCW;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, wg = (warp - G::kWarpSoft) >> 2;
+  const int c0 = wg * CW, id = 1 + wg;
+  const int tok = quarter * 32 + lane;
+  const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+  const uint32_t pcol = (tok >> 6) * (NP * 128) + c0 * 128;  // this token's column of the P tile
+  const uint32_t pbyte = (tok & 63) * 2;
+  AttendWalk walk(p, sh);
+  AttendSeg s;
+  uint32_t g = 0, ns = 0;
+  bool ok = true;
+  for (; walk.next(p, s); ++ns) {
+    const uint32_t qb = ns & 1u, ob = ns % G::kOB;
+    float l[CW];
+#pragma unroll
+    for (int c = 0; c < CW; ++c) l[c] = 0.0f;
+    bool unset = true;  // some row has seen nothing yet (uniform over the warpgroup)
+    // cs and lim of this segment
+    ok = ok && warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error);
+    // The maximum is taken of rounded products and the fused multiply-add does
+    // not round them: for scores past 2^22 (|S| < 2^35) the two could differ by
+    // more than P's range, so there the products are rounded first.
+    bool big = false;
+#pragma unroll
+    for (int c = 0; c < CW; ++c) big |= fabsf(sh.cs[qb][c0 + c]) > 0x1p-13f;
+    for (int t = s.t0; t < s.t1; ++t, ++g) {
+      const uint32_t sb = g & 1u, use = g >> 1;
+      const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + sb * NP + c0;
+      ok = ok && warp_wait(&sh.sfull[sb], use & 1u, &sh.abort, p.error);
+      tc_fence_after();
+      const int at = t * kTile + tok;
+      float e[CW];
+      const bool whole = t * kTile >= s.full_lo && t * kTile + kTile <= s.full_hi;
+      const bool have = (sh.kvalid[g & 3] >> (tok >> 4)) & 1u;
+      auto scores = [&](bool raw) {
+#pragma unroll
+        for (int c = 0; c < CW; c += 8) tmem_ld8(s_tmem + c, e + c);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < CW; c += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&sh.cs[qb][c0 + c]);
+          if (raw) {
+            e[c] *= f.x, e[c + 1] *= f.y, e[c + 2] *= f.z, e[c + 3] *= f.w;
+          } else if (big) {
+            const float4 m = *reinterpret_cast<const float4*>(&sh.mr[c0 + c]);
+            e[c] = __fsub_rn(__fmul_rn(e[c], f.x), m.x);
+            e[c + 1] = __fsub_rn(__fmul_rn(e[c + 1], f.y), m.y);
+            e[c + 2] = __fsub_rn(__fmul_rn(e[c + 2], f.z), m.z);
+            e[c + 3] = __fsub_rn(__fmul_rn(e[c + 3], f.w), m.w);
+          } else {
+            const float4 m = *reinterpret_cast<const float4*>(&sh.mr[c0 + c]);
+            e[c] = fmaf(e[c], f.x, -m.x);
+            e[c + 1] = fmaf(e[c + 1], f.y, -m.y);
+            e[c + 2] = fmaf(e[c + 2], f.z, -m.z);
+            e[c + 3] = fmaf(e[c + 3], f.w, -m.w);
+          }
+        }
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < CW; ++c) {
+            const int2 v = sh.lim[qb][c0 + c];
+            if (at < v.x || at >= v.y) e[c] = -INFINITY;
+          }
+        }
+        if (!have) {
+#pragma unroll
+          for (int c = 0; c < CW; ++c) e[c] = -INFINITY;
+        }
+      };
+      bool raise = unset || !ok;
+      if (!raise) {
+        scores(false);
+        float top = e[0];
+#pragma unroll
+        for (int c = 1; c < CW; ++c) top = fmaxf(top, e[c]);
+        raise = top > kRaise;
+      }
+      if (group_any(id, raise)) {
+        if (group_any(id, !ok)) return;
+        scores(true);
+        float keep = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CW; ++c) {
+          const float m = warp_max(e[c]);
+          if (lane == c) keep = m;
+        }
+        if (lane < CW) sh.red[quarter][c0 + lane] = keep;
+        group_sync(id);
+        bool none = false;
+        if (tok < CW) {
+          const int c = c0 + tok;
+          const float was = t == s.t0 ? -INFINITY : sh.mref[c];
+          const float m = fmaxf(fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c])), was);
+          const float mr = m == -INFINITY ? 0.0f : (m == INFINITY ? NAN : __fsub_ru(m, kLift));
+          sh.fac[c] = was == -INFINITY ? 0.0f : ex2(sh.mr[c] - mr);
+          sh.mref[c] = m;
+          sh.mr[c] = mr;
+          none = c < s.rows && m == -INFINITY;
+        }
+        unset = group_any(id, none);
+        if (t != s.t0) {
+          // O of the previous tile has to be complete before it is scaled
+          ok = warp_wait(&sh.pfree[(g - 1) & 1u], ((g - 1) >> 1) & 1u, &sh.abort, p.error);
+          tc_fence_after();
+          if (ok) {
+#pragma unroll 1
+            for (int mt = 0; mt < G::kMT; ++mt) {
+              const uint32_t o = sh.tmem + lanes + G::kTmemO + (ob * G::kMT + mt) * NP + c0;
+#pragma unroll 1
+              for (int c = 0; c < CW; c += 8) {
+                float v[8];
+                tmem_ld8(o + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 8; ++x) v[x] *= sh.fac[c0 + c + x];
+                tmem_st8(o + c, v);
+              }
+            }
+            tmem_st_wait();
+          }
+#pragma unroll
+          for (int c = 0; c < CW; ++c) l[c] *= sh.fac[c0 + c];
+        }
+        scores(false);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0 && ok) mbar_arrive(&sh.sfree[sb]);
+      ok = ok && warp_wait(&sh.pfree[sb], (use & 1u) ^ 1u, &sh.abort, p.error);
+      if (!ok) continue;
+      const uint32_t dst = p_smem + sb * G::kPBytes + pcol;
+#pragma unroll
+      for (int c = 0; c < CW; c += 2) {
+        const float a = ex2(e[c]), b = ex2(e[c + 1]);
+        l[c] += a;
+        l[c + 1] += b;
+        const __half2 h = __floats2half2_rn(a, b);
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + c * 128 + (pbyte ^ ((c & 7) << 4))),
+                     "h"(static_cast<unsigned short>(w))
+                     : "memory");
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + (c + 1) * 128 + (pbyte ^ (((c + 1) & 7) << 4))),
+                     "h"(static_cast<unsigned short>(w >> 16))
+                     : "memory");
+      }
+      fence_async_shared();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pready[sb]);
+    }
+    // the segment's sums: over the warp's tokens here, over the warps in the epilogue
+    ok = ok && warp_wait(&sh.ofree[ob], ((ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error);
+    float keep = 0.0f;
+#pragma unroll
+    for (int c = 0; c < CW; ++c) {
+      float v = l[c];
+#pragma unroll
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == c) keep = v;
+    }
+    if (ok) {
+      if (lane < CW) {
+        sh.lsum[ob][quarter][c0 + lane] = keep;
+        if (quarter == 0) sh.mout[ob][c0 + lane] = sh.mr[c0 + lane];
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.lready[ob]);
+    }
+  }
+}
+
+// Q of a segment: rows to fp16 times a power of two that brings the row's
+// largest element into [2^14, 2^15), where bf16 and fp16 values are exact down to
+// 2^-39 of it; the power goes into the row's factor cs.
+template <int D, int NP>
+__device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShared<D, NP>& sh, const AttendSeg& s,
+                                              uint32_t qb, uint32_t q_smem) {
+  using G = AttendGeo<D, NP>;
+  constexpr int E = D / 32;  // elements of a lane
+  constexpr int RW = NP / 4;  // rows of a warp
+  const int warp = (threadIdx.x >> 5) - G::kWarpEpi, lane = threadIdx.x & 31;
+  uint32_t raw[RW][E / 2];
+  const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + s.i * p.q.sb;
+#pragma unroll
+  for (int u = 0; u < RW; ++u) {
+    const int row = s.row0 + 4 * u + warp;
+    if (4 * u + warp < s.rows) {
+      const uint16_t* src = q + (row / p.group) * p.q.st +
+                            static_cast<int64_t>(s.h * p.group + row % p.group) * p.q.sh + lane * E;
+      if constexpr (E == 2) {
+        raw[u][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+      } else if constexpr (E == 4) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+        raw[u][0] = w.x, raw[u][1] = w.y;
       } else {
-        float dot = 0.0f;
-        for (int g = 0; g < D / 16; ++g) {
-          const uint32_t sc = r[run_k_scales(D) + tok * (D / 16) + g];
-          const uint32_t s2 = e4m3x2_to_f16x2(sc | (sc << 8));
-          for (int u = 0; u < 2; ++u) {
-            uint32_t hh[4];
-            e2m1x8_to_f16(*reinterpret_cast<const uint32_t*>(r + (g >> 1) * 256 + tok * 16 + (g & 1) * 8 + 4 * u), hh);
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = h2_to_f2(h2_mul(hh[e], s2));
-              dot = fmaf(q[g * 16 + u * 8 + 2 * e], f.x, dot);
-              dot = fmaf(q[g * 16 + u * 8 + 2 * e + 1], f.y, dot);
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+        raw[u][0] = w.x, raw[u][1] = w.y, raw[u][2] = w.z, raw[u][3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) raw[u][e] = 0;
+    }
+  }
+  const float gk = p.c.k_scale ? __ldg(p.c.k_scale + s.h) : 1.0f;
+  const int ch = lane * E;
+#pragma unroll
+  for (int u = 0; u < RW; ++u) {
+    const int r = 4 * u + warp;
+    float x[E];
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      float2 f;
+      if (p.bf16) f = make_float2(__uint_as_float(raw[u][e] << 16), __uint_as_float(raw[u][e] & 0xffff0000u));
+      else f = h2_to_f2(raw[u][e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+      top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool bad = top >= 0x7f800000u;  // NaN or infinity: the whole row is NaN
+    const int k = 14 + 127 - static_cast<int>(bad ? 141u : top >> 23);
+    // 2^k in two factors: k reaches 141
+    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (k >> 1)) << 23);
+    const float f2 = __uint_as_float(static_cast<uint32_t>(127 + (k - (k >> 1))) << 23);
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) {
+      const __half2 h = __floats2half2_rn(bad ? 0.0f : x[2 * e] * f1 * f2, bad ? 0.0f : x[2 * e + 1] * f1 * f2);
+      w[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const uint32_t a = q_smem + qb * G::kQBytes + (ch >> 6) * (NP * 128) + r * 128 +
+                       (((ch & 63) * 2) ^ ((r & 7) << 4));
+    if constexpr (E == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w[0]) : "memory");
+    else if constexpr (E == 4)
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(w[0]), "r"(w[1]) : "memory");
+    else sts128(a, make_uint4(w[0], w[1], w[2], w[3]));
+    if (lane == 0) {
+      const bool real = r < s.rows;
+      const float b1 = __uint_as_float(static_cast<uint32_t>(127 - (k >> 1)) << 23);
+      const float b2 = __uint_as_float(static_cast<uint32_t>(127 - (k - (k >> 1))) << 23);
+      const float c = p.scale * 1.4426950408889634f * gk;
+      sh.cs[qb][r] = !real ? 0.0f : (bad ? NAN : c * b1 * b2);
+      int2 v = make_int2(0, INT_MAX);
+      if (real) {
+        const int64_t base = s.run0 << 4, pos = s.n + (s.row0 + r) / p.group;
+        v.x = p.window ? static_cast<int>(max(pos + 1 - p.window - base, int64_t(0))) : 0;
+        v.y = static_cast<int>((p.causal ? pos + 1 : s.n + s.L) - base);
+      }
+      sh.lim[qb][r] = v;
+    }
+  }
+  fence_async_shared();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&sh.qready[qb]);
+}
+
+template <int D, int NP>
+__device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem) {
+  using G = AttendGeo<D, NP>;
+  const int warp = (threadIdx.x >> 5) - G::kWarpEpi, lane = threadIdx.x & 31;
+  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+  AttendWalk ahead(p, sh), walk(p, sh);
+  AttendSeg s;
+  for (uint32_t q = 0; q < 2; ++q)
+    if (ahead.next(p, s)) attend_load_q<D, NP>(p, sh, s, q, q_smem);
+  uint32_t ns = 0;
+  for (; walk.next(p, s); ++ns) {
+    const uint32_t ob = ns % G::kOB, par = (ns / G::kOB) & 1u;
+    if (!warp_wait(&sh.lready[ob], par, &sh.abort, p.error)) return;
+    if (!warp_wait(&sh.oready[ob], par, &sh.abort, p.error)) return;
+    tc_fence_after();
+    const bool cut = s.t0 > 0 || s.t1 < s.tiles;
+    const int slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 > 0 ? 0 : 1);
+    const float gv = p.c.v_scale ? __ldg(p.c.v_scale + s.h) : 1.0f;
+    // a lane looks after the rows `lane` and `lane + 32`
+    float inv[2];
+    int64_t at[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = lane + 32 * u;
+      inv[u] = 0.0f;
+      at[u] = 0;
+      if (r < s.rows && r < NP) {
+        const float l = (sh.lsum[ob][0][r] + sh.lsum[ob][1][r]) + (sh.lsum[ob][2][r] + sh.lsum[ob][3][r]);
+        const float mr = sh.mout[ob][r];
+        const int row = s.row0 + r, j = row / p.group, hq = s.h * p.group + row % p.group;
+        if (cut) {
+          if (warp == 0) p.part_l[slot * NP + r] = make_float2(mr, l);
+        } else {
+          inv[u] = l == 0.0f ? 0.0f : __frcp_rn(l);
+          at[u] = s.i * p.out.sb + j * p.out.st + hq * p.out.sh;
+          if (p.lse && warp == 0)
+            p.lse[(static_cast<int64_t>(s.i) * p.T + j) * p.heads_q + hq] =
+                l == 0.0f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
+        }
+      }
+    }
+#pragma unroll 1
+    for (int mt = 0; mt < G::kMT; ++mt) {
+      const int ch = mt * 128 + warp * 32 + lane;
+      const bool mine = ch < D;
+      unsigned long long nan = 0;
+      if (mine) nan = *static_cast<volatile unsigned long long*>(&sh.nan_rows[ob][ch / kGroup]);
+#pragma unroll
+      for (int c = 0; c < NP; c += 8) {
+        if (c >= s.rows) break;
+        float v[8];
+        tmem_ld8(sh.tmem + lanes + G::kTmemO + (ob * G::kMT + mt) * NP + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int r = c + x;
+          if (r >= s.rows) break;
+          float o = ((nan >> r) & 1ull) ? NAN : v[x];
+          if (cut) {
+            if (mine) p.part_o[(static_cast<int64_t>(slot) * NP + r) * D + ch] = o;
+          } else {
+            o = o * __shfl_sync(0xffffffffu, inv[r >> 5], r & 31) * gv;
+            const int64_t to = __shfl_sync(0xffffffffu, at[r >> 5], r & 31) + ch;
+            if (mine) {
+              if (p.bf16) static_cast<__nv_bfloat16*>(p.out.data)[to] = __float2bfloat16_rn(o);
+              else static_cast<__half*>(p.out.data)[to] = __float2half_rn(o);
             }
           }
         }
-        s = dot * kx;
       }
+      __syncwarp();
+      if (mine && nan && (lane & 15) == 0) sh.nan_rows[ob][ch / kGroup] = 0;
     }
-    float mx = s;
-    bool nan = s != s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    if ((t & 31) == 0) red[t >> 5] = mx;
-    nan = __syncthreads_or(nan);
-    mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.0f : mn;
-    const float f = expf(m - ref);
-    float pe = expf(s - ref);
-    pr[t] = pe;
-    for (int o = 16; o; o >>= 1) pe += __shfl_xor_sync(0xffffffffu, pe, o);
-    __syncthreads();
-    if ((t & 31) == 0) red[t >> 5] = pe;
-    __syncthreads();
-    l = l * f + red[0] + red[1] + red[2] + red[3];
-    if (nan) l = NAN;
-    m = mn;
-    for (int u = 0; u < (D + 127) / 128; ++u) {
-      const int c = t + 128 * u;
-      if (c >= D) continue;
-      float a = acc[u] * f;
-      for (int e = 0; e < 128; ++e) {
-        const int64_t pe2 = t0 + e;
-        if (pe2 < first || pe2 >= end) continue;
-        const uint8_t* r = cache_run<D>(p.c, i, h, pe2 >> 4);
-        if (!r) continue;
-        const int tok = static_cast<int>(pe2 & 15);
-        uint32_t b = r[run_v_codes(D) + c * 8 + (tok >> 1)];
-        b = tok & 1 ? b >> 4 : b & 15u;
-        uint32_t hh[4];
-        e2m1x8_to_f16(b, hh);
-        const uint32_t sc = r[run_v_scales(D) + (c >> 4) * 16 + tok];
-        a = fmaf(pr[e], h2_to_f2(h2_mul(hh[0], e4m3x2_to_f16x2(sc))).x, a);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.ofree[ob]);
+    // both buffers' readers are done with segment ns: its Q buffer is free
+    AttendSeg nx;
+    if (ahead.next(p, nx)) attend_load_q<D, NP>(p, sh, nx, ns & 1u, q_smem);
+  }
+}
+
+// Exclusive prefix of v over the CTA, and the total.
+template <class SH>
+__device__ __forceinline__ long long block_scan(SH& sh, long long v, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  long long x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) sh.scan[warp] = x;
+  __syncthreads();
+  long long before = 0;
+  total = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += sh.scan[w];
+    total += sh.scan[w];
+  }
+  return before + x - v;
+}
+
+template <int D, int NP>
+__global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const __grid_constant__ AttendParams p) {
+  using G = AttendGeo<D, NP>;
+  extern __shared__ uint8_t attend_smem[];
+  static_assert(sizeof(AttendShared<D, NP>) <= 8192, "shared block");
+  const uint32_t pad = (1024u - (smem_addr(attend_smem) & 1023u)) & 1023u;
+  uint8_t* base = attend_smem + pad;
+  const uint32_t q_smem = smem_addr(base), p_smem = q_smem + 2 * G::kQBytes;
+  const uint32_t stages = p_smem + 2 * G::kPBytes;
+  const uint32_t scratch = stages + G::kStages * G::kStageBytes;
+  AttendShared<D, NP>& sh = *reinterpret_cast<AttendShared<D, NP>*>(
+      base + 2 * G::kQBytes + 2 * G::kPBytes + G::kStages * G::kStageBytes + 4 * 512 * G::kMT);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int u = 0; u < G::kStages; ++u) {
+      mbar_init(&sh.full[u], 1);
+      mbar_init(&sh.empty[u], 8);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&sh.kready[u], 4);
+      mbar_init(&sh.kfree[u], 1);
+      mbar_init(&sh.vready[u], 4);
+      mbar_init(&sh.vfree[u], 1);
+      mbar_init(&sh.sfull[u], 1);
+      mbar_init(&sh.sfree[u], G::kSoftWarps);
+      mbar_init(&sh.pready[u], G::kSoftWarps);
+      mbar_init(&sh.pfree[u], 1);
+      mbar_init(&sh.qready[u], 4);
+      mbar_init(&sh.oready[u], 1);
+      mbar_init(&sh.ofree[u], 4);
+      mbar_init(&sh.lready[u], G::kSoftWarps);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.abort = 0;
+    sh.start_i = 0;
+    sh.start_off = 0;
+    mbar_init_fence();
+  }
+  if (threadIdx.x < 2 * G::kGroups) (&sh.nan_rows[0][0])[threadIdx.x] = 0;
+  if (warp == G::kWarpMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                 "r"(G::kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  // this CTA's share of the units
+  long long mine = 0, total = 0, before = 0;
+  for (int i0 = 0; i0 < p.B; i0 += G::kThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    AttendReq r;
+    mine = 0;
+    if (i < p.B) {
+      if (!attend_req(p, i, r) && p.status && blockIdx.x == 0) atomicOr(p.status + i, kDevBadLength);
+      mine = r.per_head * p.c.heads;
+    }
+    long long sum;
+    before = total + block_scan(sh, mine, sum);
+    total += sum;
+  }
+  const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  const int c = static_cast<int>(blockIdx.x);
+  const long long u0 = c < n ? share_start(total, c, n) : 0, u1 = c < n ? share_start(total, c + 1, n) : 0;
+  if (p.B <= G::kThreads) {
+    if (u0 >= before && u0 < before + mine) {
+      sh.start_i = static_cast<int>(threadIdx.x);
+      sh.start_off = u0 - before;
+    }
+  } else {
+    long long run = 0;
+    for (int i0 = 0; i0 < p.B; i0 += G::kThreads) {
+      const int i = i0 + static_cast<int>(threadIdx.x);
+      AttendReq r;
+      mine = 0;
+      if (i < p.B) {
+        attend_req(p, i, r);
+        mine = r.per_head * p.c.heads;
       }
-      acc[u] = a;
+      long long sum;
+      before = run + block_scan(sh, mine, sum);
+      if (u0 >= before && u0 < before + mine) {
+        sh.start_i = i;
+        sh.start_off = u0 - before;
+      }
+      run += sum;
     }
   }
-  const float vx = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f;
-  T* dst = static_cast<T*>(p.out.data) + i * p.out.sb + j * p.out.st + hq * p.out.sh;
-  for (int u = 0; u < (D + 127) / 128; ++u) {
-    const int c = t + 128 * u;
-    if (c < D) dst[c] = static_cast<T>(l == 0.0f ? 0.0f : acc[u] * vx / l);
+  if (threadIdx.x == 0) sh.units = u1 - u0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+
+  if (warp == G::kWarpLoad) {
+    attend_producer<D, NP>(p, sh, stages);
+  } else if (warp == G::kWarpMma) {
+    if (lane == 0) attend_mma<D, NP>(p, sh, q_smem, p_smem);
+    __syncwarp();
+  } else if (warp < 4) {
+    attend_keys<D, NP>(p, sh, stages);
+  } else if (warp < 8) {
+    attend_values<D, NP>(p, sh, stages, scratch);
+  } else if (warp < G::kWarpSoft) {
+    attend_epilogue<D, NP>(p, sh, q_smem);
+  } else {
+    attend_softmax<D, NP>(p, sh, p_smem);
   }
-  if (p.lse && t == 0)
-    p.lse[(static_cast<int64_t>(i) * p.T + j) * p.heads_q + hq] = l == 0.0f ? -INFINITY : m + logf(l);
+  // the cut at the start of this share, for k_attend_join
+  if (warp == 0 && lane == 0) {
+    AttendCut cut;
+    cut.last = -1;
+    if (u1 > u0) {
+      AttendWalk walk(p, sh);
+      AttendSeg s;
+      walk.next(p, s);
+      const long long first = u0 - s.t0;
+      if (s.t0 > 0 && share_of(total, first, n) == c - 1) {
+        cut.i = s.i;
+        cut.h = s.h;
+        cut.row0 = s.row0;
+        cut.rows = s.rows;
+        cut.first = c - 1;
+        cut.last = share_of(total, first + s.tiles - 1, n);
+      }
+    }
+    p.cuts[c] = cut;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == G::kWarpMma) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem), "r"(G::kTmemCols)
+                 : "memory");
+  }
+}
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 4;      // rows of a CTA
+constexpr int kJoinMaxParts = 1024;
+
+// Join the parts of the segments that were cut: block (x, y) takes the rows
+// [4 y, 4 y + 4) of the segment that CTA x + 1's share starts inside of, where
+// that is the segment's first cut.  Parts are added in the order of the CTAs
+// (in D == 128: two interleaved halves, then their sum), so the result does not
+// depend on timing.
+template <int D, int NP>
+__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ AttendParams p) {
+  constexpr int S = kJoinThreads / D;  // threads of a channel
+  __shared__ float weight[kJoinRows][kJoinMaxParts];
+  __shared__ float inv[kJoinRows];
+  __shared__ float sum[kJoinRows][kJoinThreads];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const AttendCut& cut = p.cuts[blockIdx.x + 1];
+  const int last = __ldcg(&cut.last);
+  if (last < 0) return;
+  const int i = __ldcg(&cut.i), h = __ldcg(&cut.h), row0 = __ldcg(&cut.row0), rows = __ldcg(&cut.rows),
+            first = __ldcg(&cut.first);
+  const int r0 = static_cast<int>(blockIdx.y) * kJoinRows;
+  if (r0 >= rows) return;
+  const int parts = last - first + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto slot = [&](int e) { return 2 * (first + e) + (e == 0 ? 1 : 0); };
+  const int nr = min(kJoinRows, rows - r0);
+  if (warp < nr) {
+    const int r = r0 + warp;
+    float m = -INFINITY;
+    for (int e = lane; e < parts; e += 32) {
+      const float2 v = __ldcg(p.part_l + slot(e) * NP + r);
+      if (v.y != 0.0f) m = fmaxf(m, v.x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float l = 0.0f;
+    for (int e = lane; e < parts; e += 32) {
+      const float2 v = __ldcg(p.part_l + slot(e) * NP + r);
+      const float w = v.y == 0.0f ? 0.0f : ex2(v.x - m);
+      weight[warp][e] = w;
+      l += w * v.y;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      inv[warp] = l == 0.0f ? 0.0f : __frcp_rn(l);
+      if (p.lse && blockIdx.y * kJoinRows + warp < rows) {
+        const int row = row0 + r, j = row / p.group, hq = h * p.group + row % p.group;
+        p.lse[(static_cast<int64_t>(i) * p.T + j) * p.heads_q + hq] =
+            l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      }
+    }
+  }
+  __syncthreads();
+  const int ch = threadIdx.x % D, part = threadIdx.x / D;
+  float acc[kJoinRows] = {};
+#pragma unroll 4
+  for (int e = part; e < parts; e += S) {
+    const float* src = p.part_o + (static_cast<int64_t>(slot(e)) * NP + r0) * D + ch;
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r)
+      if (r < nr) acc[r] = fmaf(weight[r][e], __ldcg(src + r * D), acc[r]);
+  }
+#pragma unroll
+  for (int r = 0; r < kJoinRows; ++r) sum[r][threadIdx.x] = acc[r];
+  __syncthreads();
+  const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f;
+  for (int e = threadIdx.x; e < nr * D; e += kJoinThreads) {
+    const int r = e / D, cc = e % D;
+    float o = 0.0f;
+#pragma unroll
+    for (int u = 0; u < S; ++u) o += sum[r][u * D + cc];
+    o = o * inv[r] * gv;
+    const int row = row0 + r0 + r, j = row / p.group, hq = h * p.group + row % p.group;
+    const int64_t to = i * p.out.sb + j * p.out.st + hq * p.out.sh + cc;
+    if (p.bf16) static_cast<__nv_bfloat16*>(p.out.data)[to] = __float2bfloat16_rn(o);
+    else static_cast<__half*>(p.out.data)[to] = __float2half_rn(o);
+  }
 }
 
 }  // namespace sv

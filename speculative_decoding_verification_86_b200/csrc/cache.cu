@@ -2,6 +2,7 @@
 // argument checks, the context's workspace and the launches.
 #include "spec_verify.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <new>
@@ -16,10 +17,15 @@ struct spec_cache_ctx {
   int max_batch = 0;
   int heads_q = 0, heads_kv = 0, head_dim = 0, page_size = 0;
   void* ws = nullptr;
+  float* part_o = nullptr;
+  float2* part_l = nullptr;
+  sv::AttendCut* cuts = nullptr;
   unsigned* error = nullptr;
 };
 
 namespace {
+
+constexpr int64_t kMaxPositions = 2147483392;  // 2^31 - 256
 
 bool geometry_ok(int heads_kv, int head_dim, int page_size) {
   return heads_kv >= 1 && heads_kv <= 1024 && (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
@@ -47,7 +53,8 @@ spec_status check_pages(const spec_cache_ctx* c, const spec_cache_pages* p, sv::
   out->num_pages = p->num_pages;
   out->table = p->table;
   out->table_stride = p->table_stride;
-  out->capacity = static_cast<int64_t>(p->table_width) * c->page_size;
+  // positions are counted in 32 bits from a segment's first run
+  out->capacity = std::min(static_cast<int64_t>(p->table_width) * c->page_size, kMaxPositions);
   out->heads = c->heads_kv;
   out->page_shift = log2_of(c->page_size);
   out->k_scale = p->k_scale;
@@ -112,11 +119,50 @@ spec_status move(spec_cache_ctx* c, const spec_cache_pages* cache, const spec_ca
   return launch_move<WRITE, 256>(p, dtype, stream);
 }
 
+// Query rows of a row tile at most: the accumulators of 128 (256) channels
+// share 512 columns of tensor memory with the decoded tiles.
+int max_rows(int head_dim) { return head_dim == 256 ? 32 : 64; }
+
+template <int D, int NP>
+spec_status launch_attend(const spec_cache_ctx* c, const sv::AttendParams& p, cudaStream_t stream) {
+  using G = sv::AttendGeo<D, NP>;
+  sv::k_attend<D, NP><<<c->num_sms, G::kThreads, G::kSmemBytes, stream>>>(p);
+  // the join starts while the attention drains, and waits for its end by itself
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(c->num_sms - 1, (p.rp + sv::kJoinRows - 1) / sv::kJoinRows);
+  cfg.blockDim = dim3(sv::kJoinThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (c->num_sms > 1 && cudaLaunchKernelEx(&cfg, sv::k_attend_join<D, NP>, p) != cudaSuccess) return SPEC_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
 template <int D>
-void launch_attend(const sv::AttendParams& p, spec_dtype dtype, cudaStream_t stream) {
-  const dim3 g(p.heads_q, p.T, p.B);
-  if (dtype == SPEC_BF16) sv::k_attend<D, __nv_bfloat16><<<g, 128, 0, stream>>>(p);
-  else sv::k_attend<D, __half><<<g, 128, 0, stream>>>(p);
+spec_status launch_attend(const spec_cache_ctx* c, const sv::AttendParams& p, cudaStream_t stream) {
+  if (p.rp <= 16) return launch_attend<D, 16>(c, p, stream);
+  if (p.rp <= 32) return launch_attend<D, 32>(c, p, stream);
+  if constexpr (D < 256) {
+    if (p.rp <= 48) return launch_attend<D, 48>(c, p, stream);
+    return launch_attend<D, 64>(c, p, stream);
+  }
+  return SPEC_ERR_INVALID_ARG;
+}
+
+template <int D, int NP>
+bool attend_smem() {
+  return cudaFuncSetAttribute(sv::k_attend<D, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              static_cast<int>(sv::AttendGeo<D, NP>::kSmemBytes)) == cudaSuccess;
+}
+
+bool attend_prepare(int head_dim) {
+  if (head_dim == 64) return attend_smem<64, 16>() && attend_smem<64, 32>() && attend_smem<64, 48>() && attend_smem<64, 64>();
+  if (head_dim == 128)
+    return attend_smem<128, 16>() && attend_smem<128, 32>() && attend_smem<128, 48>() && attend_smem<128, 64>();
+  return attend_smem<256, 16>() && attend_smem<256, 32>();
 }
 
 }  // namespace
@@ -159,13 +205,22 @@ spec_status spec_cache_init(spec_cache_ctx** out, int device, int max_batch, int
     delete c;
     return SPEC_ERR_CUDA;
   }
-  if (cudaMalloc(&c->ws, 256) != cudaSuccess) {
+  // two cut segments per CTA (one CTA per SM): fp32 rows, their sums, the list of cuts
+  const size_t rows = 2 * static_cast<size_t>(c->num_sms) * max_rows(head_dim);
+  const size_t o_l = align_up(rows * head_dim * sizeof(float), 256);
+  const size_t o_cuts = align_up(o_l + rows * sizeof(float2), 256);
+  const size_t o_err = align_up(o_cuts + c->num_sms * sizeof(sv::AttendCut), 256);
+  if (c->num_sms > sv::kJoinMaxParts || cudaMalloc(&c->ws, o_err + 256) != cudaSuccess) {
     cudaGetLastError();
     delete c;
     return SPEC_ERR_NOMEM;
   }
-  c->error = static_cast<unsigned*>(c->ws);
-  if (cudaMemset(c->ws, 0, 256) != cudaSuccess) {
+  char* b = static_cast<char*>(c->ws);
+  c->part_o = reinterpret_cast<float*>(b);
+  c->part_l = reinterpret_cast<float2*>(b + o_l);
+  c->cuts = reinterpret_cast<sv::AttendCut*>(b + o_cuts);
+  c->error = reinterpret_cast<unsigned*>(b + o_err);
+  if (cudaMemset(c->error, 0, 256) != cudaSuccess || !attend_prepare(head_dim)) {
     cudaFree(c->ws);
     delete c;
     return SPEC_ERR_CUDA;
@@ -227,13 +282,22 @@ spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
   p.window = window;
   p.lse = out_lse;
   p.status = out_status;
+  p.bf16 = dtype == SPEC_BF16;
+  // row tiles of equal size
+  const int64_t rows = static_cast<int64_t>(T) * p.group;
+  const int64_t tiles = (rows + max_rows(c->head_dim) - 1) / max_rows(c->head_dim);
+  p.rp = static_cast<int>((rows + tiles - 1) / tiles);
+  if (rows > INT_MAX) return SPEC_ERR_INVALID_ARG;
+  p.part_o = c->part_o;
+  p.part_l = c->part_l;
+  p.cuts = c->cuts;
+  p.error = c->error;
   DeviceGuard g(c->device);
   if (!g.ok) return SPEC_ERR_CUDA;
   cudaGetLastError();
-  if (c->head_dim == 64) launch_attend<64>(p, dtype, stream);
-  else if (c->head_dim == 128) launch_attend<128>(p, dtype, stream);
-  else launch_attend<256>(p, dtype, stream);
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  if (c->head_dim == 64) return launch_attend<64>(c, p, stream);
+  if (c->head_dim == 128) return launch_attend<128>(c, p, stream);
+  return launch_attend<256>(c, p, stream);
 }
 
 spec_status spec_cache_errors(spec_cache_ctx* c, uint32_t* out) {
