@@ -14,6 +14,8 @@
 // One persistent CTA per SM walks an equal share of all (request, head, tile of
 // 128 tokens) units in order, so a long context is split over many CTAs and
 // short ones share one.  Roles (warps):
+//   plan          writes the share's segments (one request, head, row tile each)
+//                 into a ring that the other roles read;
 //   producer      bulk copies of the runs of a tile into a ring of stages;
 //   K 0-3, V 4-7  decode into tensor memory, lane = token / channel;
 //   MMA           one thread issues S(t+1) before O(t), so the softmax of one
@@ -50,6 +52,7 @@ struct AttendParams {
   int rp;                    // query rows of a row tile
   int bf16;                  // q and out are bf16 (else fp16)
   float scale;
+  float one;  // 1.0f (mul_add_2)
   int causal, window;
   float* lse;  // [B, T, heads_q] or nullptr
   uint32_t* status;
@@ -67,6 +70,9 @@ struct AttendCut {
   int first, last;  // last < 0: nothing to join here
   int pad[2];
 };
+
+constexpr int kSegs = 8;  // ring of planned segments
+constexpr int kSharedBytes = 14336;
 
 template <int D, int NP>
 struct AttendGeo {
@@ -90,18 +96,33 @@ struct AttendGeo {
   static constexpr int kWarpSoft = 12;
   static constexpr int kWarpLoad = kWarpSoft + kSoftWarps;
   static constexpr int kWarpMma = kWarpLoad + 1;
-  static constexpr int kThreads = 32 * (kWarpMma + 1);
+  static constexpr int kWarpPlan = kWarpMma + 1;
+  static constexpr int kThreads = 32 * (kWarpPlan + 1);
+  static constexpr int kSegReaders = 1 + 1 + 4 + kSoftWarps + 4;  // warps that read a segment
   static constexpr int kGroups = D / kGroup;
   static constexpr uint32_t kStageBytes = kTileRuns * run_bytes(D);
   static constexpr uint32_t kQBytes = NP * D * 2;
   static constexpr uint32_t kPBytes = NP * kTile * 2;
-  static constexpr uint32_t kFixed = 2 * kQBytes + 2 * kPBytes + 4 * 512 * kMT + 8192;
+  static constexpr uint32_t kFixed = 2 * kQBytes + 2 * kPBytes + 4 * 512 * kMT + kSharedBytes;
   static constexpr int kStages = static_cast<int>((227 * 1024 - 1024 - kFixed) / kStageBytes) < 8
                                      ? static_cast<int>((227 * 1024 - 1024 - kFixed) / kStageBytes)
                                      : 8;
   static_assert(kStages >= 3, "stages");
   static constexpr size_t kSmemBytes = 1024 + kFixed + kStages * kStageBytes;
   static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NP >> 3) << 17) | (8u << 24);
+};
+
+// One row tile of one request and head: its rows, the positions it reads, and
+// the token tiles that cover them from its first position's run on.
+struct AttendSeg {
+  int i, h, row0, rows;  // rows = 0: the share's end
+  int64_t run0;          // first run
+  int64_t n;
+  int L;
+  int tiles;             // token tiles of the whole segment
+  int t0, t1;            // this CTA's
+  int lo, hi;            // visible to any row, in tokens from run0
+  int full_lo, full_hi;  // visible to every row
 };
 
 template <int D, int NP>
@@ -111,22 +132,24 @@ struct alignas(16) AttendShared {
   uint64_t kready[2], kfree[2], vready[2], vfree[2];
   uint64_t sfull[2], sfree[2], pready[2], pfree[2];
   uint64_t qready[2], oready[2], ofree[2], lready[2];
+  uint64_t segfull[kSegs], segfree[kSegs];
   uint64_t drain;
+  AttendSeg seg[kSegs];
+  uint32_t row[kSegs][NP];  // block token << 16 | query head of the group
+  int2 lim[kSegs][NP];      // visible tokens of a row, counted from the segment's first run
   unsigned long long nan_rows[2][G::kGroups];  // rows of O[ob] that see a NaN of the value group
   uint32_t valid[8];   // per stage: runs that were copied
   uint32_t kvalid[4];  // the same by tile, for the softmax (which lags the stages)
   alignas(16) float cs[2][NP];  // log2 units of one unit of S, per query row
-  int2 lim[2][NP];      // visible tokens of a row, counted from the segment's first run
+  alignas(16) float nmr[NP];    // minus the subtracted exponent: kLift - mref, 0 while nothing was seen
+  alignas(16) float fac[NP];
   float mref[NP];       // running maximum (log2 units)
-  alignas(16) float mr[NP];  // subtracted exponent: mref - kLift, 0 while nothing was seen
-  float fac[NP];
   float red[4][NP];
   float lsum[2][4][NP];
   float mout[2][NP];
+  float inv[4][NP];
   long long scan[32];
-  long long unit0;      // this CTA's share: first unit, and where it lies
-  long long units;      // number of units
-  long long total;
+  long long units;      // this CTA's share: number of units, and where it starts
   int start_i;
   long long start_off;
   uint32_t tmem;
@@ -196,6 +219,41 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// (a, b) = (a, b) * (fa, fb), rounded, + (ma, mb).  A packed product and a packed
+// sum get joined into one rounding (measured), so the sum is a multiply-add by
+// `one`, a 1.0f that the compiler does not know.
+__device__ __forceinline__ void mul_add_2(float& a, float& b, float fa, float fb, float ma, float mb, float one) {
+  asm("{\n\t.reg .b64 x, f, m, one;\n\t"
+      "mov.b64 x, {%0, %1};\n\t"
+      "mov.b64 f, {%2, %3};\n\t"
+      "mov.b64 m, {%4, %5};\n\t"
+      "mov.b64 one, {%6, %6};\n\t"
+      "mul.rn.f32x2 x, x, f;\n\t"
+      "fma.rn.f32x2 x, x, one, m;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(fa), "f"(fb), "f"(ma), "f"(mb), "f"(one));
+}
+// Sum of v[c] over the warp's lanes, in lane c (< N): the lanes trade halves of
+// the columns, 31 exchanges for 32 columns.
+template <int N>
+__device__ __forceinline__ float warp_column_sums(const float (&v)[N]) {
+  const int lane = threadIdx.x & 31;
+  float x[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c) x[c] = c < N ? v[c] : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int c = 0; c < o; ++c) {
+      const float send = up ? x[c] : x[c + o];
+      const float got = __shfl_xor_sync(0xffffffffu, send, o);
+      x[c] = (up ? x[c + o] : x[c]) + got;
+    }
+  }
+  return x[0];
+}
 __device__ __forceinline__ float warp_max(float x) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
@@ -220,61 +278,43 @@ __device__ __forceinline__ void group_sync(int id) {
 
 // ------------------------------------------------------------- work shares --
 // A request's units, in order: head, row tile, token tile.
-struct AttendReq {
-  int64_t n;
-  int L;
-  int64_t per_head;  // units of one head
-};
+__device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t& n, int& L) {
+  n = __ldg(p.cache_len + i);
+  L = p.block_len ? min(max(__ldg(p.block_len + i), 0), p.T) : p.T;
+  return n >= 0 && n + L <= p.c.capacity;
+}
 
-// Row tile rt of a request: its rows, the positions it reads, and the token
-// tiles that cover them from its first position's run on.
-struct AttendSeg {
-  int i, h, row0, rows;
-  int64_t run0;          // first run
-  int tiles;             // token tiles of the whole segment
-  int t0, t1;            // this CTA's
-  int lo, hi;            // visible to any row, in tokens from run0
-  int full_lo, full_hi;  // visible to every row
-  int j0;
-  int64_t n;
-  int L;
-};
-
-__device__ __forceinline__ void attend_rows(const AttendParams& p, const AttendReq& r, int rt, AttendSeg& s) {
+__device__ __forceinline__ void attend_rows(const AttendParams& p, int64_t n, int L, int rt, AttendSeg& s) {
   s.row0 = rt * p.rp;
-  s.rows = min(p.rp, r.L * p.group - s.row0);
-  s.j0 = s.row0 / p.group;
-  const int j1 = (s.row0 + s.rows - 1) / p.group;
-  const int64_t hi = p.causal ? r.n + j1 + 1 : r.n + r.L;
-  const int64_t lo = p.window ? max(r.n + s.j0 + 1 - p.window, int64_t(0)) : 0;
+  s.rows = min(p.rp, L * p.group - s.row0);
+  const int j0 = s.row0 / p.group, j1 = (s.row0 + s.rows - 1) / p.group;
+  const int64_t hi = p.causal ? n + j1 + 1 : n + L;
+  const int64_t lo = p.window ? max(n + j0 + 1 - p.window, int64_t(0)) : 0;
   s.run0 = lo >> 4;
   const int64_t base = s.run0 << 4;
   s.lo = static_cast<int>(lo - base);
   s.hi = static_cast<int>(hi - base);
-  s.full_lo = p.window ? static_cast<int>(max(r.n + j1 + 1 - p.window, lo) - base) : s.lo;
-  s.full_hi = p.causal ? static_cast<int>(r.n + s.j0 + 1 - base) : s.hi;
+  s.full_lo = p.window ? static_cast<int>(max(n + j1 + 1 - p.window, lo) - base) : s.lo;
+  s.full_hi = p.causal ? static_cast<int>(n + j0 + 1 - base) : s.hi;
   s.tiles = (s.hi + kTile - 1) / kTile;
-  s.n = r.n;
-  s.L = r.L;
+  s.n = n;
+  s.L = L;
 }
 
-__device__ __forceinline__ int attend_row_tiles(const AttendParams& p, int L) {
-  return (L * p.group + p.rp - 1) / p.rp;
-}
-
-// Length of request i; per_head = 0 where it has nothing to compute.
-__device__ __forceinline__ bool attend_req(const AttendParams& p, int i, AttendReq& r) {
-  r.n = __ldg(p.cache_len + i);
-  r.L = p.block_len ? min(max(__ldg(p.block_len + i), 0), p.T) : p.T;
-  r.per_head = 0;
-  if (r.n < 0 || r.n + r.L > p.c.capacity) return false;
-  const int nrt = attend_row_tiles(p, r.L);
+// Units of one head of request i; -1 where the request is skipped.
+__device__ __noinline__ long long attend_units(const AttendParams& p, int i) {
+  int64_t n;
+  int L;
+  if (!attend_len(p, i, n, L)) return -1;
+  const int nrt = (L * p.group + p.rp - 1) / p.rp;
+  long long u = 0;
   AttendSeg s;
+#pragma unroll 1
   for (int rt = 0; rt < nrt; ++rt) {
-    attend_rows(p, r, rt, s);
-    r.per_head += s.tiles;
+    attend_rows(p, n, L, rt, s);
+    u += s.tiles;
   }
-  return true;
+  return u;
 }
 
 // CTA c of n takes the units [total c / n, total (c + 1) / n); the CTA of a unit.
@@ -283,56 +323,115 @@ __device__ __forceinline__ int share_of(long long total, long long unit, int n) 
   return static_cast<int>(((unit + 1) * n - 1) / total);
 }
 
-struct AttendWalk {
-  long long left, off;
-  int i;
-  AttendReq r;
-  template <class SH>
-  __device__ __forceinline__ AttendWalk(const AttendParams& p, const SH& sh) {
-    left = sh.units;
-    off = sh.start_off;
-    i = sh.start_i;
-    if (left > 0) attend_req(p, i, r);
-  }
-  __device__ __forceinline__ bool next(const AttendParams& p, AttendSeg& s) {
-    if (left <= 0) return false;
-    while (off >= r.per_head * p.c.heads) {
-      off = 0;
-      ++i;
-      attend_req(p, i, r);
-    }
-    s.i = i;
-    s.h = static_cast<int>(off / r.per_head);
-    long long rem = off - s.h * r.per_head;
-    int rt = 0;
-    attend_rows(p, r, rt, s);
-    while (rem >= s.tiles) {
-      rem -= s.tiles;
-      attend_rows(p, r, ++rt, s);
-    }
-    s.t0 = static_cast<int>(rem);
-    s.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), rem + left));
-    off += s.t1 - s.t0;
-    left -= s.t1 - s.t0;
-    return true;
-  }
-};
-
 // All lanes of a warp leave a wait together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, error));
 }
 
 // ------------------------------------------------------------------- roles --
+// One warp.  Also leaves the cut at the start of the share for k_attend_join.
+template <int D, int NP>
+__device__ __forceinline__ void attend_plan(const AttendParams& p, AttendShared<D, NP>& sh, long long u0,
+                                            long long total, int n_ctas) {
+  const int lane = threadIdx.x & 31;
+  long long left = sh.units, off = sh.start_off;
+  int i = sh.start_i, h = 0, rt = 0;
+  AttendSeg s;
+  uint32_t ns = 0;
+  int64_t n = 0;
+  int L = 0, nrt = 0;
+  bool open = false;  // request i is under way at (h, rt, off tiles into it)
+  AttendCut cut;
+  cut.last = -1;
+  while (left > 0) {
+    if (!open) {
+      long long per_head = 0;
+      while ((per_head = attend_units(p, i)) <= 0) ++i;  // requests without units
+      attend_len(p, i, n, L);
+      nrt = (L * p.group + p.rp - 1) / p.rp;
+      h = static_cast<int>(off / per_head);
+      off -= h * per_head;
+      rt = 0;
+      open = true;
+    }
+    attend_rows(p, n, L, rt, s);
+    if (off >= s.tiles) {  // only where the share starts behind a row tile
+      off -= s.tiles;
+      ++rt;
+      continue;
+    }
+    s.i = i;
+    s.h = h;
+    s.t0 = static_cast<int>(off);
+    s.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), off + left));
+    if (ns == 0 && s.t0 > 0) {
+      const long long first = u0 - s.t0;
+      if (share_of(total, first, n_ctas) == static_cast<int>(blockIdx.x) - 1) {
+        cut.i = s.i;
+        cut.h = s.h;
+        cut.row0 = s.row0;
+        cut.rows = s.rows;
+        cut.first = static_cast<int>(blockIdx.x) - 1;
+        cut.last = share_of(total, first + s.tiles - 1, n_ctas);
+      }
+    }
+    left -= s.t1 - s.t0;
+    off = 0;
+    const int slot = static_cast<int>(ns % kSegs);
+    if (!warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u, &sh.abort, p.error)) break;
+    for (int r = lane; r < NP; r += 32) {
+      const int row = s.row0 + r, j = row / p.group;
+      sh.row[slot][r] = static_cast<uint32_t>(j) << 16 | static_cast<uint32_t>(row - j * p.group);
+      int2 v = make_int2(0, INT_MAX);
+      if (r < s.rows) {
+        const int64_t base = s.run0 << 4, pos = n + j;
+        v.x = p.window ? static_cast<int>(max(pos + 1 - p.window - base, int64_t(0))) : 0;
+        v.y = static_cast<int>((p.causal ? pos + 1 : n + L) - base);
+      }
+      sh.lim[slot][r] = v;
+    }
+    if (lane == 0) sh.seg[slot] = s;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.segfull[slot]);
+    ++ns;
+    if (++rt == nrt) {
+      rt = 0;
+      if (++h == p.c.heads) {
+        open = false;
+        ++i;
+      }
+    }
+  }
+  const int slot = static_cast<int>(ns % kSegs);
+  if (warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u, &sh.abort, p.error) && lane == 0) {
+    sh.seg[slot].rows = 0;
+    mbar_arrive(&sh.segfull[slot]);
+  }
+  if (lane == 0) p.cuts[blockIdx.x] = cut;
+}
+
+// The roles' view of the ring.
+template <class SH>
+__device__ __forceinline__ bool seg_wait(const AttendParams& p, SH& sh, uint32_t ns, AttendSeg& s) {
+  const int slot = static_cast<int>(ns % kSegs);
+  if (!warp_wait(&sh.segfull[slot], (ns / kSegs) & 1u, &sh.abort, p.error)) return false;
+  s = sh.seg[slot];
+  return s.rows > 0;
+}
+template <class SH>
+__device__ __forceinline__ void seg_done(SH& sh, uint32_t ns) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.segfree[ns % kSegs]);
+}
+
 template <int D, int NP>
 __device__ __forceinline__ void attend_producer(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages) {
   using G = AttendGeo<D, NP>;
   const int lane = threadIdx.x & 31;
-  AttendWalk walk(p, sh);
   AttendSeg s;
   uint32_t g = 0;
   bool ok = true;
-  while (ok && walk.next(p, s)) {
+  for (uint32_t ns = 0; ok && seg_wait(p, sh, ns, s); ++ns) {
     // a lane looks up one run; 32 runs are four tiles
     auto look_up = [&](int t) -> const uint8_t* {
       const int run = t * kTileRuns + lane;
@@ -342,10 +441,12 @@ __device__ __forceinline__ void attend_producer(const AttendParams& p, AttendSha
       return a;
     };
     const uint8_t* next = look_up(s.t0);
+#pragma unroll 1
     for (int t = s.t0; ok && t < s.t1; t += 4) {
       const uint8_t* src = next;
       if (t + 4 < s.t1) next = look_up(t + 4);
       const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr);
+#pragma unroll 1
       for (int u = 0; u < 4 && t + u < s.t1; ++u, ++g) {
         const int st = static_cast<int>(g % G::kStages);
         if (!warp_wait(&sh.empty[st], ((g / G::kStages) & 1u) ^ 1u, &sh.abort, p.error)) {
@@ -362,8 +463,9 @@ __device__ __forceinline__ void attend_producer(const AttendParams& p, AttendSha
           bulk_load(stages + st * G::kStageBytes + (lane & 7) * run_bytes(D), src, run_bytes(D), &sh.full[st]);
       }
     }
+    seg_done(sh, ns);
   }
-  if (!ok) {  // the copies this warp issued land before the CTA's memory goes away
+  if (!ok || sh.abort) {  // the copies this warp issued land before the CTA's memory goes away
     for (uint32_t e = g > G::kStages ? g - G::kStages : 0; e < g; ++e) {
       volatile int no_abort = 0;
       mbar_wait(&sh.full[e % G::kStages], (e / G::kStages) & 1u, &no_abort, p.error);
@@ -380,6 +482,7 @@ __device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<
   const uint32_t scales = (tok >> 4) * run_bytes(D) + run_k_scales(D) + (tok & 15) * G::kGroups;
   const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(warp * 32) << 16) + G::kTmemK;
   const uint32_t total = static_cast<uint32_t>(sh.units);
+#pragma unroll 1
   for (uint32_t g = 0; g < total; ++g) {
     const int st = static_cast<int>(g % G::kStages);
     const uint32_t kb = g % G::kKB;
@@ -444,10 +547,10 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
   const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(warp * 32) << 16) + G::kTmemV;
   const bool mine = warp * 32 < D;  // D = 64 fills half of the tile's rows
   scratch += warp * 512 * G::kMT;
-  AttendWalk walk(p, sh);
   AttendSeg s;
-  uint32_t g = 0, ns = 0;
-  for (; walk.next(p, s); ++ns) {
+  uint32_t g = 0;
+  for (uint32_t ns = 0; seg_wait(p, sh, ns, s); ++ns) {
+#pragma unroll 1
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const int st = static_cast<int>(g % G::kStages);
       const uint32_t vb = g % G::kVB;
@@ -538,82 +641,90 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
         mbar_arrive(&sh.empty[st]);
       }
     }
+    seg_done(sh, ns);
   }
 }
 
-// One thread.  S of tile g is issued before O of tile g - 1.
+// One thread issues; its warp stays together.  S of tile g goes before O of tile g - 1.
 template <int D, int NP>
 __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem,
                                            uint32_t p_smem) {
   using G = AttendGeo<D, NP>;
-  AttendWalk walk(p, sh);
+  const int lane = threadIdx.x & 31;
   AttendSeg s;
   uint32_t g = 0, ns = 0;
   bool ok = true;
   int pend = 0;  // O of the previous tile: 0 none, else 1 | first << 1 | last << 2
-  uint32_t pend_ob = 0, pend_ns = 0;
+  uint32_t pend_ns = 0;
+  const uint64_t q_desc = sw128_desc(q_smem), p_desc = sw128_desc(p_smem);
   auto issue_o = [&](uint32_t t) {  // tile t
-    const uint32_t sb = t & 1u, vb = t % G::kVB;
-    if (!mbar_wait(&sh.vready[vb], (t / G::kVB) & 1u, &sh.abort, p.error) ||
-        !mbar_wait(&sh.pready[sb], (t >> 1) & 1u, &sh.abort, p.error))
+    const uint32_t sb = t & 1u, vb = t % G::kVB, ob = pend_ns % G::kOB;
+    if (!warp_wait(&sh.vready[vb], (t / G::kVB) & 1u, &sh.abort, p.error) ||
+        !warp_wait(&sh.pready[sb], (t >> 1) & 1u, &sh.abort, p.error))
       return false;
-    if ((pend & 2) &&
-        !mbar_wait(&sh.ofree[pend_ob], ((pend_ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error))
+    if ((pend & 2) && !warp_wait(&sh.ofree[ob], ((pend_ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error))
       return false;
     tc_fence_after();
+    if (lane == 0) {
 #pragma unroll
-    for (int mt = 0; mt < G::kMT; ++mt) {
-      const uint32_t d = sh.tmem + G::kTmemO + (pend_ob * G::kMT + mt) * NP;
-      const uint32_t a = sh.tmem + G::kTmemV + vb * G::kVCols + mt * 64;
+      for (int mt = 0; mt < G::kMT; ++mt) {
+        const uint32_t d = sh.tmem + G::kTmemO + (ob * G::kMT + mt) * NP;
+        const uint32_t a = sh.tmem + G::kTmemV + vb * G::kVCols + mt * 64;
 #pragma unroll
-      for (int kk = 0; kk < kTile / 16; ++kk) {
-        const uint64_t b = sw128_desc(p_smem + sb * G::kPBytes + (kk >> 2) * (NP * 128)) + 2 * (kk & 3);
-        umma_ts(d, a + 8 * kk, b, G::kIdesc, ((pend & 2) && kk == 0) ? 0u : 1u);
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          umma_ts(d, a + 8 * kk, p_desc + ((sb * G::kPBytes + (kk >> 2) * (NP * 128) + 32 * (kk & 3)) >> 4),
+                  G::kIdesc, ((pend & 2) && kk == 0) ? 0u : 1u);
       }
+      umma_commit<1>(&sh.vfree[vb]);
+      umma_commit<1>(&sh.pfree[sb]);
+      if (pend & 4) umma_commit<1>(&sh.oready[ob]);
     }
-    umma_commit<1>(&sh.vfree[vb]);
-    umma_commit<1>(&sh.pfree[sb]);
-    if (pend & 4) umma_commit<1>(&sh.oready[pend_ob]);
+    __syncwarp();
     return true;
   };
-  while (ok && walk.next(p, s)) {
-    const uint32_t qb = ns & 1u;
-    if (!mbar_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error)) {
-      ok = false;
-      break;
-    }
-    for (int t = s.t0; t < s.t1; ++t, ++g) {
-      const uint32_t sb = g & 1u, kb = g % G::kKB;
-      if (!mbar_wait(&sh.kready[kb], (g / G::kKB) & 1u, &sh.abort, p.error) ||
-          !mbar_wait(&sh.sfree[sb], ((g >> 1) & 1u) ^ 1u, &sh.abort, p.error)) {
-        ok = false;
-        break;
-      }
+  // one place issues O: the loop runs once more for the last tile
+  bool more = seg_wait(p, sh, ns, s);
+  int t = more ? s.t0 : 0;
+  while (ok && (more || pend)) {
+    if (more) {
+      const uint32_t qb = ns & 1u, sb = g & 1u, kb = g % G::kKB;
+      ok = (t > s.t0 || warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error)) &&
+           warp_wait(&sh.kready[kb], (g / G::kKB) & 1u, &sh.abort, p.error) &&
+           warp_wait(&sh.sfree[sb], ((g >> 1) & 1u) ^ 1u, &sh.abort, p.error);
+      if (!ok) break;
       tc_fence_after();
-      const uint32_t d = sh.tmem + G::kTmemS + sb * NP;
-      const uint32_t a = sh.tmem + G::kTmemK + kb * G::kKCols;
+      if (lane == 0) {
+        const uint32_t d = sh.tmem + G::kTmemS + sb * NP;
+        const uint32_t a = sh.tmem + G::kTmemK + kb * G::kKCols;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t b = sw128_desc(q_smem + qb * G::kQBytes + (kk >> 2) * (NP * 128)) + 2 * (kk & 3);
-        umma_ts(d, a + 8 * kk, b, G::kIdesc, kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < D / 16; ++kk)
+          umma_ts(d, a + 8 * kk, q_desc + ((qb * G::kQBytes + (kk >> 2) * (NP * 128) + 32 * (kk & 3)) >> 4),
+                  G::kIdesc, kk > 0 ? 1u : 0u);
+        umma_commit<1>(&sh.kfree[kb]);
+        umma_commit<1>(&sh.sfull[sb]);
       }
-      umma_commit<1>(&sh.kfree[kb]);
-      umma_commit<1>(&sh.sfull[sb]);
-      if (pend && !issue_o(g - 1)) {
-        ok = false;
-        break;
-      }
-      pend = 1 | (t == s.t0 ? 2 : 0) | (t == s.t1 - 1 ? 4 : 0);
-      pend_ob = ns % G::kOB;
-      pend_ns = ns;
+      __syncwarp();
     }
-    ++ns;
+    if (pend) ok = issue_o(g - 1);
+    pend = 0;
+    if (more) {
+      pend = 1 | (t == s.t0 ? 2 : 0) | (t == s.t1 - 1 ? 4 : 0);
+      pend_ns = ns;
+      ++g;
+      if (++t == s.t1) {
+        seg_done(sh, ns);
+        more = seg_wait(p, sh, ++ns, s);
+        t = s.t0;
+      }
+    }
   }
-  if (ok && pend) ok = issue_o(g - 1);
-  if (!ok) {  // what was issued completes before tensor memory is released
-    umma_commit<1>(&sh.drain);
-    volatile int no_abort = 0;
-    mbar_wait(&sh.drain, 0, &no_abort, p.error);
+  if (!ok || sh.abort) {  // what was issued completes before tensor memory is released
+    if (lane == 0) {
+      umma_commit<1>(&sh.drain);
+      volatile int no_abort = 0;
+      mbar_wait(&sh.drain, 0, &no_abort, p.error);
+    }
+    __syncwarp();
   }
 }
 
@@ -628,60 +739,47 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
   const uint32_t pcol = (tok >> 6) * (NP * 128) + c0 * 128;  // this token's column of the P tile
   const uint32_t pbyte = (tok & 63) * 2;
-  AttendWalk walk(p, sh);
   AttendSeg s;
-  uint32_t g = 0, ns = 0;
+  uint32_t g = 0;
   bool ok = true;
-  for (; walk.next(p, s); ++ns) {
+  for (uint32_t ns = 0; seg_wait(p, sh, ns, s); ++ns) {
     const uint32_t qb = ns & 1u, ob = ns % G::kOB;
+    const int slot = static_cast<int>(ns % kSegs);
     float l[CW];
 #pragma unroll
     for (int c = 0; c < CW; ++c) l[c] = 0.0f;
     bool unset = true;  // some row has seen nothing yet (uniform over the warpgroup)
-    // cs and lim of this segment
+    // cs of this segment
     ok = ok && warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error);
-    // The maximum is taken of rounded products and the fused multiply-add does
-    // not round them: for scores past 2^22 (|S| < 2^35) the two could differ by
-    // more than P's range, so there the products are rounded first.
-    bool big = false;
-#pragma unroll
-    for (int c = 0; c < CW; ++c) big |= fabsf(sh.cs[qb][c0 + c]) > 0x1p-13f;
+#pragma unroll 1
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const uint32_t sb = g & 1u, use = g >> 1;
       const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + sb * NP + c0;
       ok = ok && warp_wait(&sh.sfull[sb], use & 1u, &sh.abort, p.error);
       tc_fence_after();
       const int at = t * kTile + tok;
-      float e[CW];
       const bool whole = t * kTile >= s.full_lo && t * kTile + kTile <= s.full_hi;
       const bool have = (sh.kvalid[g & 3] >> (tok >> 4)) & 1u;
-      auto scores = [&](bool raw) {
+      float e[CW];
+      bool first = true;  // pass over the tile: a second one follows a raised reference
+#pragma unroll 1
+      for (;; first = false) {
+        // x - reference, with x = S cs rounded: the maximum is taken of the same
+        // rounded x, so P stays in range at any size of the scores
 #pragma unroll
         for (int c = 0; c < CW; c += 8) tmem_ld8(s_tmem + c, e + c);
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < CW; c += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&sh.cs[qb][c0 + c]);
-          if (raw) {
-            e[c] *= f.x, e[c + 1] *= f.y, e[c + 2] *= f.z, e[c + 3] *= f.w;
-          } else if (big) {
-            const float4 m = *reinterpret_cast<const float4*>(&sh.mr[c0 + c]);
-            e[c] = __fsub_rn(__fmul_rn(e[c], f.x), m.x);
-            e[c + 1] = __fsub_rn(__fmul_rn(e[c + 1], f.y), m.y);
-            e[c + 2] = __fsub_rn(__fmul_rn(e[c + 2], f.z), m.z);
-            e[c + 3] = __fsub_rn(__fmul_rn(e[c + 3], f.w), m.w);
-          } else {
-            const float4 m = *reinterpret_cast<const float4*>(&sh.mr[c0 + c]);
-            e[c] = fmaf(e[c], f.x, -m.x);
-            e[c + 1] = fmaf(e[c + 1], f.y, -m.y);
-            e[c + 2] = fmaf(e[c + 2], f.z, -m.z);
-            e[c + 3] = fmaf(e[c + 3], f.w, -m.w);
-          }
+          const float4 m = *reinterpret_cast<const float4*>(&sh.nmr[c0 + c]);
+          mul_add_2(e[c], e[c + 1], f.x, f.y, m.x, m.y, p.one);
+          mul_add_2(e[c + 2], e[c + 3], f.z, f.w, m.z, m.w, p.one);
         }
         if (!whole) {
 #pragma unroll
           for (int c = 0; c < CW; ++c) {
-            const int2 v = sh.lim[qb][c0 + c];
+            const int2 v = sh.lim[slot][c0 + c];
             if (at < v.x || at >= v.y) e[c] = -INFINITY;
           }
         }
@@ -689,35 +787,38 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
 #pragma unroll
           for (int c = 0; c < CW; ++c) e[c] = -INFINITY;
         }
-      };
-      bool raise = unset || !ok;
-      if (!raise) {
-        scores(false);
-        float top = e[0];
+        float top[4] = {e[0], e[1], e[2], e[3]};
 #pragma unroll
-        for (int c = 1; c < CW; ++c) top = fmaxf(top, e[c]);
-        raise = top > kRaise;
-      }
-      if (group_any(id, raise)) {
+        for (int c = 4; c < CW; ++c) top[c & 3] = fmaxf(top[c & 3], e[c]);
+        const bool raise = first && (unset || !ok || fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kRaise);
+        if (!group_any(id, raise)) break;
         if (group_any(id, !ok)) return;
-        scores(true);
-        float keep = 0.0f;
+        // new references: the maximum over the tile's tokens of every row
+#pragma unroll 1
+        for (int c = 0; c < CW; c += 8) {
+          float x[8], keep = 0.0f;
+          tmem_ld8(s_tmem + c, x);
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < CW; ++c) {
-          const float m = warp_max(e[c]);
-          if (lane == c) keep = m;
+          for (int u = 0; u < 8; ++u) {
+            const int2 v = sh.lim[slot][c0 + c + u];
+            const bool see = have && at >= v.x && at < v.y;
+            const float m = warp_max(see ? __fmul_rn(x[u], sh.cs[qb][c0 + c + u]) : -INFINITY);
+            if (lane == u) keep = m;
+          }
+          if (lane < 8) sh.red[quarter][c0 + c + lane] = keep;
         }
-        if (lane < CW) sh.red[quarter][c0 + lane] = keep;
         group_sync(id);
         bool none = false;
         if (tok < CW) {
           const int c = c0 + tok;
           const float was = t == s.t0 ? -INFINITY : sh.mref[c];
           const float m = fmaxf(fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c])), was);
+          // rounded up, so that x - reference is at most kLift; +inf gives NaN
           const float mr = m == -INFINITY ? 0.0f : (m == INFINITY ? NAN : __fsub_ru(m, kLift));
-          sh.fac[c] = was == -INFINITY ? 0.0f : ex2(sh.mr[c] - mr);
+          sh.fac[c] = was == -INFINITY ? 0.0f : ex2(-sh.nmr[c] - mr);
           sh.mref[c] = m;
-          sh.mr[c] = mr;
+          sh.nmr[c] = -mr;
           none = c < s.rows && m == -INFINITY;
         }
         unset = group_any(id, none);
@@ -744,7 +845,6 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
 #pragma unroll
           for (int c = 0; c < CW; ++c) l[c] *= sh.fac[c0 + c];
         }
-        scores(false);
       }
       tc_fence_before();
       __syncwarp();
@@ -760,11 +860,9 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
         const __half2 h = __floats2half2_rn(a, b);
         const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + c * 128 + (pbyte ^ ((c & 7) << 4))),
-                     "h"(static_cast<unsigned short>(w))
-                     : "memory");
+                     "h"(static_cast<unsigned short>(w)));
         asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + (c + 1) * 128 + (pbyte ^ (((c + 1) & 7) << 4))),
-                     "h"(static_cast<unsigned short>(w >> 16))
-                     : "memory");
+                     "h"(static_cast<unsigned short>(w >> 16)));
       }
       fence_async_shared();
       tc_fence_before();
@@ -773,22 +871,16 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
     }
     // the segment's sums: over the warp's tokens here, over the warps in the epilogue
     ok = ok && warp_wait(&sh.ofree[ob], ((ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error);
-    float keep = 0.0f;
-#pragma unroll
-    for (int c = 0; c < CW; ++c) {
-      float v = l[c];
-#pragma unroll
-      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == c) keep = v;
-    }
+    const float sum = warp_column_sums<CW>(l);
     if (ok) {
       if (lane < CW) {
-        sh.lsum[ob][quarter][c0 + lane] = keep;
-        if (quarter == 0) sh.mout[ob][c0 + lane] = sh.mr[c0 + lane];
+        sh.lsum[ob][quarter][c0 + lane] = sum;
+        if (quarter == 0) sh.mout[ob][c0 + lane] = -sh.nmr[c0 + lane];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.lready[ob]);
     }
+    seg_done(sh, ns);
   }
 }
 
@@ -797,80 +889,77 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
 // 2^-39 of it; the power goes into the row's factor cs.
 template <int D, int NP>
 __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShared<D, NP>& sh, const AttendSeg& s,
-                                              uint32_t qb, uint32_t q_smem) {
+                                              uint32_t ns, uint32_t q_smem) {
   using G = AttendGeo<D, NP>;
   constexpr int E = D / 32;  // elements of a lane
-  constexpr int RW = NP / 4;  // rows of a warp
+  constexpr int RB = 4;      // rows of a warp in flight
   const int warp = (threadIdx.x >> 5) - G::kWarpEpi, lane = threadIdx.x & 31;
-  uint32_t raw[RW][E / 2];
-  const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + s.i * p.q.sb;
-#pragma unroll
-  for (int u = 0; u < RW; ++u) {
-    const int row = s.row0 + 4 * u + warp;
-    if (4 * u + warp < s.rows) {
-      const uint16_t* src = q + (row / p.group) * p.q.st +
-                            static_cast<int64_t>(s.h * p.group + row % p.group) * p.q.sh + lane * E;
-      if constexpr (E == 2) {
-        raw[u][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-      } else if constexpr (E == 4) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-        raw[u][0] = w.x, raw[u][1] = w.y;
-      } else {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
-        raw[u][0] = w.x, raw[u][1] = w.y, raw[u][2] = w.z, raw[u][3] = w.w;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) raw[u][e] = 0;
-    }
-  }
-  const float gk = p.c.k_scale ? __ldg(p.c.k_scale + s.h) : 1.0f;
+  const uint32_t qb = ns & 1u;
   const int ch = lane * E;
+  const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + s.i * p.q.sb +
+                      static_cast<int64_t>(s.h * p.group) * p.q.sh + ch;
+  const float gk = p.c.k_scale ? __ldg(p.c.k_scale + s.h) : 1.0f;
+  const float unit = p.scale * 1.4426950408889634f * gk;
+#pragma unroll 1
+  for (int r0 = 0; r0 < NP; r0 += 4 * RB) {
+    uint32_t raw[RB][E / 2];
 #pragma unroll
-  for (int u = 0; u < RW; ++u) {
-    const int r = 4 * u + warp;
-    float x[E];
-    uint32_t top = 0;
+    for (int u = 0; u < RB; ++u) {
+      const int r = r0 + 4 * u + warp;
+      if (r < s.rows) {
+        const uint32_t at = sh.row[ns % kSegs][r];
+        const uint16_t* src = q + (at >> 16) * p.q.st + (at & 0xffffu) * p.q.sh;
+        if constexpr (E == 2) {
+          raw[u][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
+        } else if constexpr (E == 4) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
+          raw[u][0] = w.x, raw[u][1] = w.y;
+        } else {
+          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+          raw[u][0] = w.x, raw[u][1] = w.y, raw[u][2] = w.z, raw[u][3] = w.w;
+        }
+      } else {
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      float2 f;
-      if (p.bf16) f = make_float2(__uint_as_float(raw[u][e] << 16), __uint_as_float(raw[u][e] & 0xffff0000u));
-      else f = h2_to_f2(raw[u][e]);
-      x[2 * e] = f.x;
-      x[2 * e + 1] = f.y;
-      top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    const bool bad = top >= 0x7f800000u;  // NaN or infinity: the whole row is NaN
-    const int k = 14 + 127 - static_cast<int>(bad ? 141u : top >> 23);
-    // 2^k in two factors: k reaches 141
-    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (k >> 1)) << 23);
-    const float f2 = __uint_as_float(static_cast<uint32_t>(127 + (k - (k >> 1))) << 23);
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int e = 0; e < E / 2; ++e) {
-      const __half2 h = __floats2half2_rn(bad ? 0.0f : x[2 * e] * f1 * f2, bad ? 0.0f : x[2 * e + 1] * f1 * f2);
-      w[e] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    const uint32_t a = q_smem + qb * G::kQBytes + (ch >> 6) * (NP * 128) + r * 128 +
-                       (((ch & 63) * 2) ^ ((r & 7) << 4));
-    if constexpr (E == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w[0]) : "memory");
-    else if constexpr (E == 4)
-      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(w[0]), "r"(w[1]) : "memory");
-    else sts128(a, make_uint4(w[0], w[1], w[2], w[3]));
-    if (lane == 0) {
-      const bool real = r < s.rows;
-      const float b1 = __uint_as_float(static_cast<uint32_t>(127 - (k >> 1)) << 23);
-      const float b2 = __uint_as_float(static_cast<uint32_t>(127 - (k - (k >> 1))) << 23);
-      const float c = p.scale * 1.4426950408889634f * gk;
-      sh.cs[qb][r] = !real ? 0.0f : (bad ? NAN : c * b1 * b2);
-      int2 v = make_int2(0, INT_MAX);
-      if (real) {
-        const int64_t base = s.run0 << 4, pos = s.n + (s.row0 + r) / p.group;
-        v.x = p.window ? static_cast<int>(max(pos + 1 - p.window - base, int64_t(0))) : 0;
-        v.y = static_cast<int>((p.causal ? pos + 1 : s.n + s.L) - base);
+        for (int e = 0; e < E / 2; ++e) raw[u][e] = 0;
       }
-      sh.lim[qb][r] = v;
+    }
+#pragma unroll
+    for (int u = 0; u < RB; ++u) {
+      const int r = r0 + 4 * u + warp;
+      float x[E];
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        float2 f;
+        if (p.bf16) f = make_float2(__uint_as_float(raw[u][e] << 16), __uint_as_float(raw[u][e] & 0xffff0000u));
+        else f = h2_to_f2(raw[u][e]);
+        x[2 * e] = f.x;
+        x[2 * e + 1] = f.y;
+        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      const bool bad = top >= 0x7f800000u;  // NaN or infinity: the whole row is NaN
+      const int k = bad ? 0 : 14 + 127 - static_cast<int>(top >> 23);
+      // 2^k in two factors: k reaches 141
+      const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (k >> 1)) << 23);
+      const float f2 = __uint_as_float(static_cast<uint32_t>(127 + (k - (k >> 1))) << 23);
+      uint32_t w[E / 2];
+#pragma unroll
+      for (int e = 0; e < E / 2; ++e) {
+        const __half2 h = __floats2half2_rn(bad ? 0.0f : x[2 * e] * f1 * f2, bad ? 0.0f : x[2 * e + 1] * f1 * f2);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      const uint32_t a = q_smem + qb * G::kQBytes + (ch >> 6) * (NP * 128) + r * 128 +
+                         (((ch & 63) * 2) ^ ((r & 7) << 4));
+      if constexpr (E == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w[0]) : "memory");
+      else if constexpr (E == 4)
+        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(w[0]), "r"(w[1]) : "memory");
+      else sts128(a, make_uint4(w[0], w[1], w[2], w[3]));
+      if (lane == 0) {
+        const float b1 = __uint_as_float(static_cast<uint32_t>(127 - (k >> 1)) << 23);
+        const float b2 = __uint_as_float(static_cast<uint32_t>(127 - (k - (k >> 1))) << 23);
+        sh.cs[qb][r] = r >= s.rows ? 0.0f : (bad ? NAN : unit * b1 * b2);
+      }
     }
   }
   fence_async_shared();
@@ -883,65 +972,71 @@ __device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendSha
   using G = AttendGeo<D, NP>;
   const int warp = (threadIdx.x >> 5) - G::kWarpEpi, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-  AttendWalk ahead(p, sh), walk(p, sh);
-  AttendSeg s;
-  for (uint32_t q = 0; q < 2; ++q)
-    if (ahead.next(p, s)) attend_load_q<D, NP>(p, sh, s, q, q_smem);
-  uint32_t ns = 0;
-  for (; walk.next(p, s); ++ns) {
-    const uint32_t ob = ns % G::kOB, par = (ns / G::kOB) & 1u;
+  AttendSeg s, ahead;
+  bool more = true;
+  // Q of segment na goes before O of segment na - 1: the two Q buffers are then
+  // free in turn, since O of segment na - 2 was the last that used its own
+#pragma unroll 1
+  for (uint32_t na = 0; more; ++na) {
+    more = seg_wait(p, sh, na, ahead);
+    if (more) attend_load_q<D, NP>(p, sh, ahead, na, q_smem);
+    if (na == 0) {
+      s = ahead;
+      continue;
+    }
+    const uint32_t ns = na - 1, ob = ns % G::kOB, par = (ns / G::kOB) & 1u;
     if (!warp_wait(&sh.lready[ob], par, &sh.abort, p.error)) return;
     if (!warp_wait(&sh.oready[ob], par, &sh.abort, p.error)) return;
     tc_fence_after();
     const bool cut = s.t0 > 0 || s.t1 < s.tiles;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 > 0 ? 0 : 1);
+    const uint32_t* row = sh.row[ns % kSegs];
     const float gv = p.c.v_scale ? __ldg(p.c.v_scale + s.h) : 1.0f;
-    // a lane looks after the rows `lane` and `lane + 32`
-    float inv[2];
-    int64_t at[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = lane + 32 * u;
-      inv[u] = 0.0f;
-      at[u] = 0;
-      if (r < s.rows && r < NP) {
-        const float l = (sh.lsum[ob][0][r] + sh.lsum[ob][1][r]) + (sh.lsum[ob][2][r] + sh.lsum[ob][3][r]);
-        const float mr = sh.mout[ob][r];
-        const int row = s.row0 + r, j = row / p.group, hq = s.h * p.group + row % p.group;
-        if (cut) {
-          if (warp == 0) p.part_l[slot * NP + r] = make_float2(mr, l);
-        } else {
-          inv[u] = l == 0.0f ? 0.0f : __frcp_rn(l);
-          at[u] = s.i * p.out.sb + j * p.out.st + hq * p.out.sh;
-          if (p.lse && warp == 0)
-            p.lse[(static_cast<int64_t>(s.i) * p.T + j) * p.heads_q + hq] =
-                l == 0.0f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
+    for (int r = lane; r < s.rows; r += 32) {
+      const float l = (sh.lsum[ob][0][r] + sh.lsum[ob][1][r]) + (sh.lsum[ob][2][r] + sh.lsum[ob][3][r]);
+      const float mr = sh.mout[ob][r];
+      if (cut) {
+        if (warp == 0) p.part_l[slot * NP + r] = make_float2(mr, l);
+      } else {
+        sh.inv[warp][r] = l == 0.0f ? 0.0f : __frcp_rn(l);
+        if (p.lse && warp == 0) {
+          const uint32_t at = row[r];
+          p.lse[(static_cast<int64_t>(s.i) * p.T + (at >> 16)) * p.heads_q + s.h * p.group + (at & 0xffffu)] =
+              l == 0.0f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
         }
       }
     }
+    __syncwarp();
+    const int64_t out = s.i * p.out.sb + static_cast<int64_t>(s.h * p.group) * p.out.sh;
 #pragma unroll 1
     for (int mt = 0; mt < G::kMT; ++mt) {
       const int ch = mt * 128 + warp * 32 + lane;
       const bool mine = ch < D;
       unsigned long long nan = 0;
       if (mine) nan = *static_cast<volatile unsigned long long*>(&sh.nan_rows[ob][ch / kGroup]);
-#pragma unroll
-      for (int c = 0; c < NP; c += 8) {
-        if (c >= s.rows) break;
+#pragma unroll 1
+      for (int c = 0; c < s.rows; c += 8) {
         float v[8];
         tmem_ld8(sh.tmem + lanes + G::kTmemO + (ob * G::kMT + mt) * NP + c, v);
         tmem_ld_wait();
+        if (!mine) continue;
+        if (nan >> c) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int r = c + x;
-          if (r >= s.rows) break;
-          float o = ((nan >> r) & 1ull) ? NAN : v[x];
-          if (cut) {
-            if (mine) p.part_o[(static_cast<int64_t>(slot) * NP + r) * D + ch] = o;
-          } else {
-            o = o * __shfl_sync(0xffffffffu, inv[r >> 5], r & 31) * gv;
-            const int64_t to = __shfl_sync(0xffffffffu, at[r >> 5], r & 31) + ch;
-            if (mine) {
+          for (int x = 0; x < 8; ++x)
+            if ((nan >> (c + x)) & 1ull) v[x] = NAN;
+        }
+        if (cut) {
+          float* dst = p.part_o + (static_cast<int64_t>(slot) * NP + c) * D + ch;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (c + x < s.rows) dst[x * D] = v[x];
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            if (c + x < s.rows) {
+              const uint32_t at = row[c + x];
+              const int64_t to = out + (at >> 16) * p.out.st + (at & 0xffffu) * p.out.sh + ch;
+              const float o = v[x] * sh.inv[warp][c + x] * gv;
               if (p.bf16) static_cast<__nv_bfloat16*>(p.out.data)[to] = __float2bfloat16_rn(o);
               else static_cast<__half*>(p.out.data)[to] = __float2half_rn(o);
             }
@@ -952,11 +1047,9 @@ __device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendSha
       if (mine && nan && (lane & 15) == 0) sh.nan_rows[ob][ch / kGroup] = 0;
     }
     tc_fence_before();
-    __syncwarp();
+    seg_done(sh, ns);
     if (lane == 0) mbar_arrive(&sh.ofree[ob]);
-    // both buffers' readers are done with segment ns: its Q buffer is free
-    AttendSeg nx;
-    if (ahead.next(p, nx)) attend_load_q<D, NP>(p, sh, nx, ns & 1u, q_smem);
+    s = ahead;
   }
 }
 
@@ -975,6 +1068,7 @@ __device__ __forceinline__ long long block_scan(SH& sh, long long v, long long& 
   __syncthreads();
   long long before = 0;
   total = 0;
+#pragma unroll 1
   for (int w = 0; w < warps; ++w) {
     if (w < warp) before += sh.scan[w];
     total += sh.scan[w];
@@ -986,7 +1080,7 @@ template <int D, int NP>
 __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const __grid_constant__ AttendParams p) {
   using G = AttendGeo<D, NP>;
   extern __shared__ uint8_t attend_smem[];
-  static_assert(sizeof(AttendShared<D, NP>) <= 8192, "shared block");
+  static_assert(sizeof(AttendShared<D, NP>) <= kSharedBytes, "shared block");
   const uint32_t pad = (1024u - (smem_addr(attend_smem) & 1023u)) & 1023u;
   uint8_t* base = attend_smem + pad;
   const uint32_t q_smem = smem_addr(base), p_smem = q_smem + 2 * G::kQBytes;
@@ -994,7 +1088,7 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   const uint32_t scratch = stages + G::kStages * G::kStageBytes;
   AttendShared<D, NP>& sh = *reinterpret_cast<AttendShared<D, NP>*>(
       base + 2 * G::kQBytes + 2 * G::kPBytes + G::kStages * G::kStageBytes + 4 * 512 * G::kMT);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int u = 0; u < G::kStages; ++u) {
@@ -1015,6 +1109,10 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
       mbar_init(&sh.ofree[u], 4);
       mbar_init(&sh.lready[u], G::kSoftWarps);
     }
+    for (int u = 0; u < kSegs; ++u) {
+      mbar_init(&sh.segfull[u], 1);
+      mbar_init(&sh.segfree[u], G::kSegReaders);
+    }
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
     sh.start_i = 0;
@@ -1030,13 +1128,16 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   }
   // this CTA's share of the units
   long long mine = 0, total = 0, before = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < p.B; i0 += G::kThreads) {
     const int i = i0 + static_cast<int>(threadIdx.x);
-    AttendReq r;
     mine = 0;
     if (i < p.B) {
-      if (!attend_req(p, i, r) && p.status && blockIdx.x == 0) atomicOr(p.status + i, kDevBadLength);
-      mine = r.per_head * p.c.heads;
+      mine = attend_units(p, i) * p.c.heads;
+      if (mine < 0) {
+        mine = 0;
+        if (p.status && blockIdx.x == 0) atomicOr(p.status + i, kDevBadLength);
+      }
     }
     long long sum;
     before = total + block_scan(sh, mine, sum);
@@ -1045,28 +1146,21 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   const int c = static_cast<int>(blockIdx.x);
   const long long u0 = c < n ? share_start(total, c, n) : 0, u1 = c < n ? share_start(total, c + 1, n) : 0;
-  if (p.B <= G::kThreads) {
-    if (u0 >= before && u0 < before + mine) {
-      sh.start_i = static_cast<int>(threadIdx.x);
-      sh.start_off = u0 - before;
-    }
-  } else {
-    long long run = 0;
-    for (int i0 = 0; i0 < p.B; i0 += G::kThreads) {
-      const int i = i0 + static_cast<int>(threadIdx.x);
-      AttendReq r;
-      mine = 0;
-      if (i < p.B) {
-        attend_req(p, i, r);
-        mine = r.per_head * p.c.heads;
-      }
+  // whose request holds unit u0: known from the scan, or from a second one where
+  // the batch is larger than the CTA
+#pragma unroll 1
+  for (int i0 = 0, once = p.B <= G::kThreads; i0 < p.B; i0 += G::kThreads) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    if (!once) {
+      if (i0 == 0) total = 0;
+      mine = i < p.B ? max(attend_units(p, i), 0ll) * p.c.heads : 0;
       long long sum;
-      before = run + block_scan(sh, mine, sum);
-      if (u0 >= before && u0 < before + mine) {
-        sh.start_i = i;
-        sh.start_off = u0 - before;
-      }
-      run += sum;
+      before = total + block_scan(sh, mine, sum);
+      total += sum;
+    }
+    if (u0 >= before && u0 < before + mine) {
+      sh.start_i = i;
+      sh.start_off = u0 - before;
     }
   }
   if (threadIdx.x == 0) sh.units = u1 - u0;
@@ -1077,8 +1171,9 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   if (warp == G::kWarpLoad) {
     attend_producer<D, NP>(p, sh, stages);
   } else if (warp == G::kWarpMma) {
-    if (lane == 0) attend_mma<D, NP>(p, sh, q_smem, p_smem);
-    __syncwarp();
+    attend_mma<D, NP>(p, sh, q_smem, p_smem);
+  } else if (warp == G::kWarpPlan) {
+    attend_plan<D, NP>(p, sh, u0, total, n);
   } else if (warp < 4) {
     attend_keys<D, NP>(p, sh, stages);
   } else if (warp < 8) {
@@ -1087,26 +1182,6 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
     attend_epilogue<D, NP>(p, sh, q_smem);
   } else {
     attend_softmax<D, NP>(p, sh, p_smem);
-  }
-  // the cut at the start of this share, for k_attend_join
-  if (warp == 0 && lane == 0) {
-    AttendCut cut;
-    cut.last = -1;
-    if (u1 > u0) {
-      AttendWalk walk(p, sh);
-      AttendSeg s;
-      walk.next(p, s);
-      const long long first = u0 - s.t0;
-      if (s.t0 > 0 && share_of(total, first, n) == c - 1) {
-        cut.i = s.i;
-        cut.h = s.h;
-        cut.row0 = s.row0;
-        cut.rows = s.rows;
-        cut.first = c - 1;
-        cut.last = share_of(total, first + s.tiles - 1, n);
-      }
-    }
-    p.cuts[c] = cut;
   }
   tc_fence_before();
   __syncthreads();

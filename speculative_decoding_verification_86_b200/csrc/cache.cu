@@ -278,6 +278,7 @@ spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
   p.heads_q = c->heads_q;
   p.group = c->heads_q / c->heads_kv;
   p.scale = scale;
+  p.one = 1.0f;
   p.causal = causal != 0;
   p.window = window;
   p.lse = out_lse;
