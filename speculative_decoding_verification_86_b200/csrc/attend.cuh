@@ -89,8 +89,8 @@ struct AttendGeo {
   static constexpr int kTmemUsed = kTmemO + kOB * kMT * NP;
   static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kTmemUsed <= 512, "tensor memory");
-  static constexpr int kSoftGroups = NP > 32 ? 2 : 1;  // warpgroups of the softmax, by columns
-  static constexpr int kCW = NP / kSoftGroups;         // query rows per softmax thread
+  static constexpr int kCW = 16;                // query rows per softmax thread
+  static constexpr int kSoftGroups = NP / kCW;  // warpgroups of the softmax, by columns
   static constexpr int kSoftWarps = 4 * kSoftGroups;
   static constexpr int kWarpEpi = 8;
   static constexpr int kWarpSoft = 12;
@@ -488,24 +488,19 @@ __device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<
     const uint32_t kb = g % G::kKB;
     if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u, &sh.abort, p.error)) return;
     const uint32_t base = stages + st * G::kStageBytes;
-    uint32_t sc[G::kGroups / 2];  // pairs of fp16 scales
-#pragma unroll
-    for (int u = 0; u < G::kGroups / 4; ++u) {
-      uint32_t w;
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(base + scales + 4 * u));
-      sc[2 * u] = e4m3x2_to_f16x2(w & 0xffffu);
-      sc[2 * u + 1] = e4m3x2_to_f16x2(w >> 16);
-    }
     if (!warp_wait(&sh.kfree[kb], ((g / G::kKB) & 1u) ^ 1u, &sh.abort, p.error)) return;
     tc_fence_after();
     // K of tile g follows S of tile g - kKB, so the softmax has read S of tile
     // g - 4 and its mask
     if (tok == 0) sh.kvalid[g & 3] = sh.valid[st];
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       const uint4 w = lds128(base + row + c * 256);
+      uint32_t two;  // the scales of the chunk's two groups
+      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(two) : "r"(base + scales + 2 * c));
+      const uint32_t sc = e4m3x2_to_f16x2(two);
       uint32_t v[16];
-      const uint32_t s0 = __byte_perm(sc[c], 0, 0x1010), s1 = __byte_perm(sc[c], 0, 0x3232);
+      const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
       const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -610,7 +605,7 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
         for (int mt = 0; mt < G::kMT; ++mt) {
           const uint32_t codes = base + run_v_codes(D) + (mt * 128 + warp * 32 + lane) * 8;
           const uint32_t sc = scratch + mt * 512 + (lane >> 4) * 32;
-#pragma unroll
+#pragma unroll 1
           for (int sub = 0; sub < kTileRuns; sub += 2) {
             uint32_t v[16];
 #pragma unroll
