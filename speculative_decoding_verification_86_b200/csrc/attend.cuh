@@ -204,14 +204,39 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// D[tmem] (+)= A[tmem] B[smem], fp16 operands, fp32 accumulator.
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t accumulate) {
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(r));
+  return r;
+}
+// D[tmem] (+)= A[tmem] B[smem] over 64 values of K, fp16 operands, fp32
+// accumulator: four instructions of K = 16 (8 columns of A, 32 bytes of B's
+// swizzled rows apart).  The whole warp runs this and one lane's predicate
+// issues: in a branch that only one lane takes, an instruction needs 50 cycles
+// (operands move to uniform registers one by one), so it takes 18 at N = 32.
+__device__ __forceinline__ void umma_ts64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t elected) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 e, %5, 0;\n\t"
+      "setp.eq.b32 t, %3, %3;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 2;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t elected) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(smem_addr(bar)),
+      "r"(elected)
       : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -323,9 +348,14 @@ __device__ __forceinline__ int share_of(long long total, long long unit, int n) 
   return static_cast<int>(((unit + 1) * n - 1) / total);
 }
 
-// All lanes of a warp leave a wait together.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
+// All lanes of a warp leave a wait together.  The patient part is out of line:
+// six roles share the SM's instruction caches, and it has some twenty sites.
+__device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, error));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return warp_wait_long(bar, parity, abort, error);
 }
 
 // ------------------------------------------------------------------- roles --
@@ -645,12 +675,12 @@ template <int D, int NP>
 __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem,
                                            uint32_t p_smem) {
   using G = AttendGeo<D, NP>;
-  const int lane = threadIdx.x & 31;
   AttendSeg s;
   uint32_t g = 0, ns = 0;
   bool ok = true;
   int pend = 0;  // O of the previous tile: 0 none, else 1 | first << 1 | last << 2
   uint32_t pend_ns = 0;
+  const uint32_t tm = sh.tmem, el = elect_one();
   const uint64_t q_desc = sw128_desc(q_smem), p_desc = sw128_desc(p_smem);
   auto issue_o = [&](uint32_t t) {  // tile t
     const uint32_t sb = t & 1u, vb = t % G::kVB, ob = pend_ns % G::kOB;
@@ -660,21 +690,17 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
     if ((pend & 2) && !warp_wait(&sh.ofree[ob], ((pend_ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error))
       return false;
     tc_fence_after();
-    if (lane == 0) {
 #pragma unroll
-      for (int mt = 0; mt < G::kMT; ++mt) {
-        const uint32_t d = sh.tmem + G::kTmemO + (ob * G::kMT + mt) * NP;
-        const uint32_t a = sh.tmem + G::kTmemV + vb * G::kVCols + mt * 64;
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          umma_ts(d, a + 8 * kk, p_desc + ((sb * G::kPBytes + (kk >> 2) * (NP * 128) + 32 * (kk & 3)) >> 4),
-                  G::kIdesc, ((pend & 2) && kk == 0) ? 0u : 1u);
-      }
-      umma_commit<1>(&sh.vfree[vb]);
-      umma_commit<1>(&sh.pfree[sb]);
-      if (pend & 4) umma_commit<1>(&sh.oready[ob]);
+    for (int mt = 0; mt < G::kMT; ++mt) {
+      const uint32_t d = tm + G::kTmemO + (ob * G::kMT + mt) * NP;
+      const uint32_t a = tm + G::kTmemV + vb * G::kVCols + mt * 64;
+      const uint64_t b = p_desc + sb * (G::kPBytes >> 4);
+      umma_ts64(d, a, b, G::kIdesc, (pend & 2) ? 0u : 1u, el);
+      umma_ts64(d, a + 32, b + (NP * 128 >> 4), G::kIdesc, 1u, el);
     }
-    __syncwarp();
+    umma_commit_if(&sh.vfree[vb], el);
+    umma_commit_if(&sh.pfree[sb], el);
+    if (pend & 4) umma_commit_if(&sh.oready[ob], el);
     return true;
   };
   // one place issues O: the loop runs once more for the last tile
@@ -688,17 +714,12 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
            warp_wait(&sh.sfree[sb], ((g >> 1) & 1u) ^ 1u, &sh.abort, p.error);
       if (!ok) break;
       tc_fence_after();
-      if (lane == 0) {
-        const uint32_t d = sh.tmem + G::kTmemS + sb * NP;
-        const uint32_t a = sh.tmem + G::kTmemK + kb * G::kKCols;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          umma_ts(d, a + 8 * kk, q_desc + ((qb * G::kQBytes + (kk >> 2) * (NP * 128) + 32 * (kk & 3)) >> 4),
-                  G::kIdesc, kk > 0 ? 1u : 0u);
-        umma_commit<1>(&sh.kfree[kb]);
-        umma_commit<1>(&sh.sfull[sb]);
-      }
-      __syncwarp();
+      for (int kk = 0; kk < D / 64; ++kk)
+        umma_ts64(tm + G::kTmemS + sb * NP, tm + G::kTmemK + kb * G::kKCols + 32 * kk,
+                  q_desc + qb * (G::kQBytes >> 4) + kk * (NP * 128 >> 4), G::kIdesc, kk > 0 ? 1u : 0u, el);
+      umma_commit_if(&sh.kfree[kb], el);
+      umma_commit_if(&sh.sfull[sb], el);
     }
     if (pend) ok = issue_o(g - 1);
     pend = 0;
@@ -714,11 +735,9 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
     }
   }
   if (!ok || sh.abort) {  // what was issued completes before tensor memory is released
-    if (lane == 0) {
-      umma_commit<1>(&sh.drain);
-      volatile int no_abort = 0;
-      mbar_wait(&sh.drain, 0, &no_abort, p.error);
-    }
+    umma_commit_if(&sh.drain, el);
+    volatile int no_abort = 0;
+    mbar_wait(&sh.drain, 0, &no_abort, p.error);
     __syncwarp();
   }
 }
