@@ -22,8 +22,8 @@
 //                 tile overlaps the products of its neighbours;
 //   softmax       lane = token, registers = query rows: S from tensor memory,
 //                 P (fp16) to shared memory.  The reference maximum of a row
-//                 is raised only when a score passes it by 2^7 (a vote of the
-//                 warps); then, and only then, O is rescaled in tensor memory;
+//                 is raised only when a P passes 2^15 (a vote of the warps);
+//                 then, and only then, O is rescaled in tensor memory;
 //   epilogue      loads and converts the next segment's Q, and writes O of the
 //                 finished one: final rows, or (a segment cut by a CTA's share)
 //                 unnormalised fp32 partials, which k_attend_join adds in the
@@ -41,7 +41,7 @@ namespace sv {
 constexpr int kTile = 128;          // tokens of a tile: the rows of S^T
 constexpr int kTileRuns = kTile / kRun;
 constexpr float kLift = 8.0f;       // P = 2^(x - max + kLift): keeps small P out of fp16's subnormals
-constexpr float kRaise = kLift + 7.0f;  // a P past 2^15 raises the row's reference
+constexpr uint32_t kRaise = 0x7800u;  // fp16 2^15: a larger P raises the row's reference
 
 struct AttendParams {
   CacheView c;
@@ -77,16 +77,19 @@ constexpr int kSharedBytes = 14336;
 template <int D, int NP>
 struct AttendGeo {
   static constexpr int kMT = (D + 127) / 128;   // tiles of 128 channels of O^T
-  static constexpr int kKB = D > 128 ? 1 : 2;   // K buffers in tensor memory
+  // buffers in tensor memory (512 columns)
+  static constexpr int kKB = D > 128 ? 1 : 2;
   static constexpr int kVB = 2;
+  static constexpr int kSB = 2;
   static constexpr int kOB = D > 128 && NP > 16 ? 1 : 2;
   static constexpr int kKCols = D / 2;          // 32-bit columns of one K buffer
   static constexpr int kVCols = 64 * kMT;
+  static constexpr int kOCols = kMT * NP;
   static constexpr int kTmemK = 0;
   static constexpr int kTmemV = kTmemK + kKB * kKCols;
   static constexpr int kTmemS = kTmemV + kVB * kVCols;
-  static constexpr int kTmemO = kTmemS + 2 * NP;
-  static constexpr int kTmemUsed = kTmemO + kOB * kMT * NP;
+  static constexpr int kTmemO = kTmemS + kSB * NP;
+  static constexpr int kTmemUsed = kTmemO + kOB * kOCols;
   static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kTmemUsed <= 512, "tensor memory");
   static constexpr int kCW = 16;                // query rows per softmax thread
@@ -109,7 +112,9 @@ struct AttendGeo {
                                      : 8;
   static_assert(kStages >= 3, "stages");
   static constexpr size_t kSmemBytes = 1024 + kFixed + kStages * kStageBytes;
-  static constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(NP >> 3) << 17) | (8u << 24);
+  // fp32 accumulator, fp16 operands, M = 128, N = NP; B of O is N-major
+  static constexpr uint32_t kIdescS = (1u << 4) | (static_cast<uint32_t>(NP >> 3) << 17) | (8u << 24);
+  static constexpr uint32_t kIdescO = kIdescS | (1u << 16);
 };
 
 // One row tile of one request and head: its rows, the positions it reads, and
@@ -145,8 +150,8 @@ struct alignas(16) AttendShared {
   alignas(16) float fac[NP];
   float mref[NP];       // running maximum (log2 units)
   float red[4][NP];
+  float mout[2][NP];    // references and sums (by warp) of a finished segment
   float lsum[2][4][NP];
-  float mout[2][NP];
   float inv[4][NP];
   long long scan[32];
   long long units;      // this CTA's share: number of units, and where it starts
@@ -211,26 +216,37 @@ __device__ __forceinline__ uint32_t elect_one() {
   return r;
 }
 // D[tmem] (+)= A[tmem] B[smem] over 64 values of K, fp16 operands, fp32
-// accumulator: four instructions of K = 16 (8 columns of A, 32 bytes of B's
-// swizzled rows apart).  The whole warp runs this and one lane's predicate
+// accumulator: four instructions of K = 16 (A 8 columns apart, B `step` units of
+// 16 bytes).  The whole warp runs this and one lane's predicate
 // issues: in a branch that only one lane takes, an instruction needs 50 cycles
 // (operands move to uniform registers one by one), so it takes 18 at N = 32.
-__device__ __forceinline__ void umma_ts64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void umma_ts64(uint32_t d, uint32_t a, uint64_t b, uint64_t step, uint32_t idesc,
                                           uint32_t accumulate, uint32_t elected) {
   asm volatile(
       "{\n\t.reg .pred e, p, t;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 e, %5, 0;\n\t"
-      "setp.eq.b32 t, %3, %3;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, 2;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.u32 a, %1, 16;\n\tadd.s64 b, %2, 4;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
-      "add.u32 a, %1, 24;\n\tadd.s64 b, %2, 6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(elected)
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 e, %6, 0;\n\t"
+      "setp.eq.b32 t, %4, %4;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.s64 b, %2, %3;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.s64 b, b, %3;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.s64 b, b, %3;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %4, t;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(b), "l"(step), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
+}
+// Matrix descriptor of P^T, N-major with the 32-byte swizzle: rows of 16 query
+// rows (32 bytes) per token, eight tokens 256 bytes apart (stride byte offset),
+// blocks of 16 query rows `block` bytes apart (leading byte offset).
+__device__ __forceinline__ uint64_t sw32_n_desc(uint32_t saddr, uint32_t block) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(block >> 4) << 16;
+  d |= static_cast<uint64_t>(256 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(6) << 61;
+  return d;
 }
 __device__ __forceinline__ void umma_commit_if(uint64_t* bar, uint32_t elected) {
   asm volatile(
@@ -259,16 +275,24 @@ __device__ __forceinline__ void mul_add_2(float& a, float& b, float fa, float fb
       : "+f"(a), "+f"(b)
       : "f"(fa), "f"(fb), "f"(ma), "f"(mb), "f"(one));
 }
-// Sum of v[c] over the warp's lanes, in lane c (< N): the lanes trade halves of
-// the columns, 31 exchanges for 32 columns.
-template <int N>
-__device__ __forceinline__ float warp_column_sums(const float (&v)[N]) {
+__device__ __forceinline__ void add_2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 s, t;\n\t"
+      "mov.b64 s, {%0, %1};\n\t"
+      "mov.b64 t, {%2, %3};\n\t"
+      "add.rn.f32x2 s, s, t;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+// Sum of v[c] over the warp's lanes, in lane c (< N = 16): the lanes trade
+// halves of the columns.
+__device__ __forceinline__ float warp_column_sums(const float (&v)[16]) {
   const int lane = threadIdx.x & 31;
-  float x[32];
+  float x[16];
 #pragma unroll
-  for (int c = 0; c < 32; ++c) x[c] = c < N ? v[c] : 0.0f;
+  for (int c = 0; c < 16; ++c) x[c] = v[c] + __shfl_xor_sync(0xffffffffu, v[c], 16);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
+  for (int o = 8; o; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int c = 0; c < o; ++c) {
@@ -278,6 +302,11 @@ __device__ __forceinline__ float warp_column_sums(const float (&v)[N]) {
     }
   }
   return x[0];
+}
+__device__ __forceinline__ uint32_t h2_max(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 __device__ __forceinline__ float warp_max(float x) {
   float r;
@@ -524,22 +553,25 @@ __device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<
     // g - 4 and its mask
     if (tok == 0) sh.kvalid[g & 3] = sh.valid[st];
 #pragma unroll 1
-    for (int c = 0; c < D / 32; ++c) {
-      const uint4 w = lds128(base + row + c * 256);
-      uint32_t two;  // the scales of the chunk's two groups
-      asm volatile("ld.shared.u16 %0, [%1];" : "=r"(two) : "r"(base + scales + 2 * c));
-      const uint32_t sc = e4m3x2_to_f16x2(two);
-      uint32_t v[16];
-      const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    for (int c = 0; c < D / 32; c += 2) {
+      uint32_t four;  // the scales of two chunks' groups
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(four) : "r"(base + scales + 2 * c));
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t h[4];
-        e2m1x8_to_f16(ww[u], h);
+      for (int u = 0; u < 2; ++u) {
+        const uint4 w = lds128(base + row + (c + u) * 256);
+        const uint32_t sc = e4m3x2_to_f16x2(u ? four >> 16 : four & 0xffffu);
+        const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        uint32_t v[16];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * u + e] = h2_mul(h[e], u < 2 ? s0 : s1);
+        for (int x = 0; x < 4; ++x) {
+          uint32_t h[4];
+          e2m1x8_to_f16(ww[x], h);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * x + e] = h2_mul(h[e], x < 2 ? s0 : s1);
+        }
+        tmem_st16(tmem + kb * G::kKCols + (c + u) * 16, v);
       }
-      tmem_st16(tmem + kb * G::kKCols + c * 16, v);
     }
     tmem_st_wait();
     tc_fence_before();
@@ -681,7 +713,7 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
   int pend = 0;  // O of the previous tile: 0 none, else 1 | first << 1 | last << 2
   uint32_t pend_ns = 0;
   const uint32_t tm = sh.tmem, el = elect_one();
-  const uint64_t q_desc = sw128_desc(q_smem), p_desc = sw128_desc(p_smem);
+  const uint64_t q_desc = sw128_desc(q_smem), p_desc = sw32_n_desc(p_smem, kTile * 32);
   auto issue_o = [&](uint32_t t) {  // tile t
     const uint32_t sb = t & 1u, vb = t % G::kVB, ob = pend_ns % G::kOB;
     if (!warp_wait(&sh.vready[vb], (t / G::kVB) & 1u, &sh.abort, p.error) ||
@@ -690,13 +722,14 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
     if ((pend & 2) && !warp_wait(&sh.ofree[ob], ((pend_ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error))
       return false;
     tc_fence_after();
+    // a step is 16 tokens: 512 bytes of P
+    const uint64_t b = p_desc + sb * (G::kPBytes >> 4);
+    const uint32_t d = tm + G::kTmemO + ob * G::kOCols, old = (pend & 2) ? 0u : 1u;
 #pragma unroll
     for (int mt = 0; mt < G::kMT; ++mt) {
-      const uint32_t d = tm + G::kTmemO + (ob * G::kMT + mt) * NP;
       const uint32_t a = tm + G::kTmemV + vb * G::kVCols + mt * 64;
-      const uint64_t b = p_desc + sb * (G::kPBytes >> 4);
-      umma_ts64(d, a, b, G::kIdesc, (pend & 2) ? 0u : 1u, el);
-      umma_ts64(d, a + 32, b + (NP * 128 >> 4), G::kIdesc, 1u, el);
+      umma_ts64(d + mt * NP, a, b, 32, G::kIdescO, old, el);
+      umma_ts64(d + mt * NP, a + 32, b + 128, 32, G::kIdescO, 1u, el);
     }
     umma_commit_if(&sh.vfree[vb], el);
     umma_commit_if(&sh.pfree[sb], el);
@@ -708,16 +741,16 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
   int t = more ? s.t0 : 0;
   while (ok && (more || pend)) {
     if (more) {
-      const uint32_t qb = ns & 1u, sb = g & 1u, kb = g % G::kKB;
+      const uint32_t qb = ns & 1u, sb = g % G::kSB, kb = g % G::kKB;
       ok = (t > s.t0 || warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error)) &&
            warp_wait(&sh.kready[kb], (g / G::kKB) & 1u, &sh.abort, p.error) &&
-           warp_wait(&sh.sfree[sb], ((g >> 1) & 1u) ^ 1u, &sh.abort, p.error);
+           warp_wait(&sh.sfree[sb], ((g / G::kSB) & 1u) ^ 1u, &sh.abort, p.error);
       if (!ok) break;
       tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < D / 64; ++kk)
         umma_ts64(tm + G::kTmemS + sb * NP, tm + G::kTmemK + kb * G::kKCols + 32 * kk,
-                  q_desc + qb * (G::kQBytes >> 4) + kk * (NP * 128 >> 4), G::kIdesc, kk > 0 ? 1u : 0u, el);
+                  q_desc + qb * (G::kQBytes >> 4) + kk * (NP * 128 >> 4), 2, G::kIdescS, kk > 0 ? 1u : 0u, el);
       umma_commit_if(&sh.kfree[kb], el);
       umma_commit_if(&sh.sfull[sb], el);
     }
@@ -751,65 +784,85 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
   const int c0 = wg * CW, id = 1 + wg;
   const int tok = quarter * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-  const uint32_t pcol = (tok >> 6) * (NP * 128) + c0 * 128;  // this token's column of the P tile
-  const uint32_t pbyte = (tok & 63) * 2;
+  // this token's 32 bytes of the P tile (sw32_n_desc)
+  const uint32_t prow = p_smem + wg * (kTile * 32) + tok * 32, pflip = (tok & 4) << 2;
   AttendSeg s;
   uint32_t g = 0;
   bool ok = true;
   for (uint32_t ns = 0; seg_wait(p, sh, ns, s); ++ns) {
     const uint32_t qb = ns & 1u, ob = ns % G::kOB;
     const int slot = static_cast<int>(ns % kSegs);
+    const int cols = min(CW, ((s.rows - c0 + 7) & ~7));  // columns with rows in them: <= 0, 8 or 16
+    bool unset = true;  // some row has seen nothing yet (uniform over the warpgroup)
+    ok = ok && warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error);
     float l[CW];
 #pragma unroll
     for (int c = 0; c < CW; ++c) l[c] = 0.0f;
-    bool unset = true;  // some row has seen nothing yet (uniform over the warpgroup)
-    // cs of this segment
-    ok = ok && warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error);
 #pragma unroll 1
     for (int t = s.t0; t < s.t1; ++t, ++g) {
-      const uint32_t sb = g & 1u, use = g >> 1;
+      const uint32_t sb = g % G::kSB, pb = g & 1u;
       const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + sb * NP + c0;
-      ok = ok && warp_wait(&sh.sfull[sb], use & 1u, &sh.abort, p.error);
+      // S of tile g was issued behind O of tile g - 2, so P's buffer is free too
+      ok = ok && warp_wait(&sh.sfull[sb], (g / G::kSB) & 1u, &sh.abort, p.error);
       tc_fence_after();
       const int at = t * kTile + tok;
       const bool whole = t * kTile >= s.full_lo && t * kTile + kTile <= s.full_hi;
       const bool have = (sh.kvalid[g & 3] >> (tok >> 4)) & 1u;
-      float e[CW];
-      bool first = true;  // pass over the tile: a second one follows a raised reference
+      float e[CW];         // S, then x - reference, then P
+      bool again = false;  // a second pass follows a raised reference
 #pragma unroll 1
-      for (;; first = false) {
-        // x - reference, with x = S cs rounded: the maximum is taken of the same
-        // rounded x, so P stays in range at any size of the scores
+      for (;; again = true) {
+        uint32_t top = 0;
+        if (!unset || again) {
+          // x - reference, with x = S cs rounded: the maximum is taken of the same
+          // rounded x, so P stays in range at any size of the scores
 #pragma unroll
-        for (int c = 0; c < CW; c += 8) tmem_ld8(s_tmem + c, e + c);
-        tmem_ld_wait();
+          for (int half = 0; half < CW; half += 8)
+            if (half < cols) tmem_ld8(s_tmem + half, e + half);
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < CW; c += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&sh.cs[qb][c0 + c]);
-          const float4 m = *reinterpret_cast<const float4*>(&sh.nmr[c0 + c]);
-          mul_add_2(e[c], e[c + 1], f.x, f.y, m.x, m.y, p.one);
-          mul_add_2(e[c + 2], e[c + 3], f.z, f.w, m.z, m.w, p.one);
-        }
-        if (!whole) {
+          for (int half = 0; half < CW; half += 8) {
+            if (half < cols) {
 #pragma unroll
-          for (int c = 0; c < CW; ++c) {
-            const int2 v = sh.lim[slot][c0 + c];
-            if (at < v.x || at >= v.y) e[c] = -INFINITY;
+              for (int c = half; c < half + 8; c += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(&sh.cs[qb][c0 + c]);
+                const float4 m = *reinterpret_cast<const float4*>(&sh.nmr[c0 + c]);
+                mul_add_2(e[c], e[c + 1], f.x, f.y, m.x, m.y, p.one);
+                mul_add_2(e[c + 2], e[c + 3], f.z, f.w, m.z, m.w, p.one);
+              }
+              if (!whole) {
+#pragma unroll
+                for (int c = half; c < half + 8; ++c) {
+                  const int2 v = sh.lim[slot][c0 + c];
+                  if (at < v.x || at >= v.y) e[c] = -INFINITY;
+                }
+              }
+              if (!have) {
+#pragma unroll
+                for (int c = half; c < half + 8; ++c) e[c] = -INFINITY;
+              }
+              uint32_t w[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float &a = e[half + 2 * c], &b = e[half + 2 * c + 1];
+                a = ex2(a);
+                b = ex2(b);
+                const __half2 h = __floats2half2_rn(a, b);
+                w[c] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              top = h2_max(top, h2_max(h2_max(w[0], w[1]), h2_max(w[2], w[3])));
+              sts128(prow + pb * G::kPBytes + ((half * 2) ^ pflip), make_uint4(w[0], w[1], w[2], w[3]));
+            }
           }
+          fence_async_shared();
         }
-        if (!have) {
-#pragma unroll
-          for (int c = 0; c < CW; ++c) e[c] = -INFINITY;
-        }
-        float top[4] = {e[0], e[1], e[2], e[3]};
-#pragma unroll
-        for (int c = 4; c < CW; ++c) top[c & 3] = fmaxf(top[c & 3], e[c]);
-        const bool raise = first && (unset || !ok || fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) > kRaise);
+        tc_fence_before();
+        const bool raise = !again && (unset || !ok || (top & 0xffffu) > kRaise || (top >> 16) > kRaise);
         if (!group_any(id, raise)) break;
         if (group_any(id, !ok)) return;
         // new references: the maximum over the tile's tokens of every row
 #pragma unroll 1
-        for (int c = 0; c < CW; c += 8) {
+        for (int c = 0; c < cols; c += 8) {
           float x[8], keep = 0.0f;
           tmem_ld8(s_tmem + c, x);
           tmem_ld_wait();
@@ -824,7 +877,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
         }
         group_sync(id);
         bool none = false;
-        if (tok < CW) {
+        if (tok < cols) {
           const int c = c0 + tok;
           const float was = t == s.t0 ? -INFINITY : sh.mref[c];
           const float m = fmaxf(fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c])), was);
@@ -843,9 +896,9 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
           if (ok) {
 #pragma unroll 1
             for (int mt = 0; mt < G::kMT; ++mt) {
-              const uint32_t o = sh.tmem + lanes + G::kTmemO + (ob * G::kMT + mt) * NP + c0;
+              const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + mt * NP + c0;
 #pragma unroll 1
-              for (int c = 0; c < CW; c += 8) {
+              for (int c = 0; c < cols; c += 8) {
                 float v[8];
                 tmem_ld8(o + c, v);
                 tmem_ld_wait();
@@ -857,35 +910,21 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
             tmem_st_wait();
           }
 #pragma unroll
-          for (int c = 0; c < CW; ++c) l[c] *= sh.fac[c0 + c];
+          for (int c = 0; c < CW; ++c)
+            if (c < cols) l[c] *= sh.fac[c0 + c];
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(&sh.sfree[sb]);
-      ok = ok && warp_wait(&sh.pfree[sb], (use & 1u) ^ 1u, &sh.abort, p.error);
-      if (!ok) continue;
-      const uint32_t dst = p_smem + sb * G::kPBytes + pcol;
-#pragma unroll
-      for (int c = 0; c < CW; c += 2) {
-        const float a = ex2(e[c]), b = ex2(e[c + 1]);
-        l[c] += a;
-        l[c + 1] += b;
-        const __half2 h = __floats2half2_rn(a, b);
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(&h);
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + c * 128 + (pbyte ^ ((c & 7) << 4))),
-                     "h"(static_cast<unsigned short>(w)));
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + (c + 1) * 128 + (pbyte ^ (((c + 1) & 7) << 4))),
-                     "h"(static_cast<unsigned short>(w >> 16)));
+      // behind the vote: every thread of the group has read S and stored P
+      if (tok == 0 && ok) {
+        mbar_arrive(&sh.sfree[sb]);
+        mbar_arrive(&sh.pready[pb]);
       }
-      fence_async_shared();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.pready[sb]);
+#pragma unroll
+      for (int c = 0; c < CW; c += 2) add_2(l[c], l[c + 1], e[c], e[c + 1]);
     }
-    // the segment's sums: over the warp's tokens here, over the warps in the epilogue
+    // the references and sums: over the warp's tokens here, over the warps in the epilogue
     ok = ok && warp_wait(&sh.ofree[ob], ((ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error);
-    const float sum = warp_column_sums<CW>(l);
+    const float sum = warp_column_sums(l);
     if (ok) {
       if (lane < CW) {
         sh.lsum[ob][quarter][c0 + lane] = sum;
@@ -1009,11 +1048,11 @@ __device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendSha
     for (int r = lane; r < s.rows; r += 32) {
       const float l = (sh.lsum[ob][0][r] + sh.lsum[ob][1][r]) + (sh.lsum[ob][2][r] + sh.lsum[ob][3][r]);
       const float mr = sh.mout[ob][r];
-      if (cut) {
-        if (warp == 0) p.part_l[slot * NP + r] = make_float2(mr, l);
-      } else {
-        sh.inv[warp][r] = l == 0.0f ? 0.0f : __frcp_rn(l);
-        if (p.lse && warp == 0) {
+      sh.inv[warp][r] = l == 0.0f ? 0.0f : __frcp_rn(l);
+      if (warp == 0) {
+        if (cut) {
+          p.part_l[slot * NP + r] = make_float2(mr, l);
+        } else if (p.lse) {
           const uint32_t at = row[r];
           p.lse[(static_cast<int64_t>(s.i) * p.T + (at >> 16)) * p.heads_q + s.h * p.group + (at & 0xffffu)] =
               l == 0.0f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
@@ -1031,7 +1070,7 @@ __device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendSha
 #pragma unroll 1
       for (int c = 0; c < s.rows; c += 8) {
         float v[8];
-        tmem_ld8(sh.tmem + lanes + G::kTmemO + (ob * G::kMT + mt) * NP + c, v);
+        tmem_ld8(sh.tmem + lanes + G::kTmemO + ob * G::kOCols + mt * NP + c, v);
         tmem_ld_wait();
         if (!mine) continue;
         if (nan >> c) {
@@ -1050,9 +1089,9 @@ __device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendSha
             if (c + x < s.rows) {
               const uint32_t at = row[c + x];
               const int64_t to = out + (at >> 16) * p.out.st + (at & 0xffffu) * p.out.sh + ch;
-              const float o = v[x] * sh.inv[warp][c + x] * gv;
-              if (p.bf16) static_cast<__nv_bfloat16*>(p.out.data)[to] = __float2bfloat16_rn(o);
-              else static_cast<__half*>(p.out.data)[to] = __float2half_rn(o);
+              const float f = v[x] * sh.inv[warp][c + x] * gv;
+              if (p.bf16) static_cast<__nv_bfloat16*>(p.out.data)[to] = __float2bfloat16_rn(f);
+              else static_cast<__half*>(p.out.data)[to] = __float2half_rn(f);
             }
           }
         }
@@ -1115,8 +1154,8 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
       mbar_init(&sh.vready[u], 4);
       mbar_init(&sh.vfree[u], 1);
       mbar_init(&sh.sfull[u], 1);
-      mbar_init(&sh.sfree[u], G::kSoftWarps);
-      mbar_init(&sh.pready[u], G::kSoftWarps);
+      mbar_init(&sh.sfree[u], G::kSoftGroups);
+      mbar_init(&sh.pready[u], G::kSoftGroups);
       mbar_init(&sh.pfree[u], 1);
       mbar_init(&sh.qready[u], 4);
       mbar_init(&sh.oready[u], 1);
