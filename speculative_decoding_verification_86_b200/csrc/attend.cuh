@@ -79,16 +79,14 @@ struct AttendGeo {
   static constexpr int kMT = (D + 127) / 128;   // tiles of 128 channels of O^T
   // buffers in tensor memory (512 columns)
   static constexpr int kKB = D > 128 ? 1 : 2;
-  static constexpr int kVB = 2;
-  static constexpr int kSB = 2;
   static constexpr int kOB = D > 128 && NP > 16 ? 1 : 2;
   static constexpr int kKCols = D / 2;          // 32-bit columns of one K buffer
   static constexpr int kVCols = 64 * kMT;
   static constexpr int kOCols = kMT * NP;
   static constexpr int kTmemK = 0;
   static constexpr int kTmemV = kTmemK + kKB * kKCols;
-  static constexpr int kTmemS = kTmemV + kVB * kVCols;
-  static constexpr int kTmemO = kTmemS + kSB * NP;
+  static constexpr int kTmemS = kTmemV + 2 * kVCols;
+  static constexpr int kTmemO = kTmemS + 2 * NP;
   static constexpr int kTmemUsed = kTmemO + kOB * kOCols;
   static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kTmemUsed <= 512, "tensor memory");
@@ -134,8 +132,10 @@ template <int D, int NP>
 struct alignas(16) AttendShared {
   using G = AttendGeo<D, NP>;
   uint64_t full[8], empty[8];
-  uint64_t kready[2], kfree[2], vready[2], vfree[2];
-  uint64_t sfull[2], sfree[2], pready[2], pfree[2];
+  // By tile, two of each: K and V decoded; S complete (K's buffer is free too);
+  // P stored (S has been read too); O complete (V's and P's buffers are free too).
+  uint64_t kready[2], vready[2], sdone[2], pready[2], odone[2];
+  // By segment: Q loaded; O's last product complete, O read; sums stored.
   uint64_t qready[2], oready[2], ofree[2], lready[2];
   uint64_t segfull[kSegs], segfree[kSegs];
   uint64_t drain;
@@ -379,8 +379,30 @@ __device__ __forceinline__ int share_of(long long total, long long unit, int n) 
 
 // All lanes of a warp leave a wait together.  The patient part is out of line:
 // six roles share the SM's instruction caches, and it has some twenty sites.
+// It counts SM cycles (a read of the nanosecond clock holds up the unit that
+// also does the exponentials) and gives up, like mbar_wait, when another role
+// raised *abort, or after kWaitCycles, raising *abort and the error word.
+constexpr long long kWaitCycles = 4000000000ll;  // 2 s: legitimate waits are microseconds
 __device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, error));
+  long long t0 = 0;
+  bool ok = true;
+#pragma unroll 1
+  for (uint32_t it = 1; !mbar_test(bar, parity); ++it) {
+    if ((it & 255u) != 0) continue;
+    if (*static_cast<volatile int*>(abort)) {
+      ok = false;
+      break;
+    }
+    const long long t = clock64();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitCycles) {
+      *static_cast<volatile int*>(abort) = 1;
+      atomicOr(error, 1u);
+      ok = false;
+      break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
   if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
@@ -547,7 +569,10 @@ __device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<
     const uint32_t kb = g % G::kKB;
     if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u, &sh.abort, p.error)) return;
     const uint32_t base = stages + st * G::kStageBytes;
-    if (!warp_wait(&sh.kfree[kb], ((g / G::kKB) & 1u) ^ 1u, &sh.abort, p.error)) return;
+    // the buffer's last reader: S of tile g - kKB
+    if (g >= G::kKB &&
+        !warp_wait(&sh.sdone[(g - G::kKB) & 1u], ((g - G::kKB) >> 1) & 1u, &sh.abort, p.error))
+      return;
     tc_fence_after();
     // K of tile g follows S of tile g - kKB, so the softmax has read S of tile
     // g - 4 and its mask
@@ -577,7 +602,7 @@ __device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&sh.kready[kb]);
+      mbar_arrive(&sh.kready[g & 1u]);
       mbar_arrive(&sh.empty[st]);
     }
   }
@@ -610,7 +635,7 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
 #pragma unroll 1
     for (int t = s.t0; t < s.t1; ++t, ++g) {
       const int st = static_cast<int>(g % G::kStages);
-      const uint32_t vb = g % G::kVB;
+      const uint32_t vb = g & 1u;
       if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u, &sh.abort, p.error)) return;
       const uint32_t base = stages + st * G::kStageBytes;
       const int tb = t * kTile;
@@ -660,7 +685,8 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
         }
         __syncwarp();
       }
-      if (!warp_wait(&sh.vfree[vb], ((g / G::kVB) & 1u) ^ 1u, &sh.abort, p.error)) return;
+      // the buffer's last reader: O of tile g - 2
+      if (!warp_wait(&sh.odone[vb], ((g >> 1) & 1u) ^ 1u, &sh.abort, p.error)) return;
       tc_fence_after();
       if (mine) {
 #pragma unroll
@@ -702,7 +728,10 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
   }
 }
 
-// One thread issues; its warp stays together.  S of tile g goes before O of tile g - 1.
+// One lane issues; the warp stays together.  S of tile g goes before O of tile
+// g - 1.  This warp's own path is on the critical cycle (three waits, two commits
+// and the products of a tile), so it waits for nothing that another wait implies:
+// P of tile g - 2 stored (awaited for its O) means that S of that tile was read.
 template <int D, int NP>
 __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem,
                                            uint32_t p_smem) {
@@ -710,61 +739,57 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
   AttendSeg s;
   uint32_t g = 0, ns = 0;
   bool ok = true;
-  int pend = 0;  // O of the previous tile: 0 none, else 1 | first << 1 | last << 2
-  uint32_t pend_ns = 0;
   const uint32_t tm = sh.tmem, el = elect_one();
   const uint64_t q_desc = sw128_desc(q_smem), p_desc = sw32_n_desc(p_smem, kTile * 32);
-  auto issue_o = [&](uint32_t t) {  // tile t
-    const uint32_t sb = t & 1u, vb = t % G::kVB, ob = pend_ns % G::kOB;
-    if (!warp_wait(&sh.vready[vb], (t / G::kVB) & 1u, &sh.abort, p.error) ||
-        !warp_wait(&sh.pready[sb], (t >> 1) & 1u, &sh.abort, p.error))
-      return false;
-    if ((pend & 2) && !warp_wait(&sh.ofree[ob], ((pend_ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error))
-      return false;
-    tc_fence_after();
-    // a step is 16 tokens: 512 bytes of P
-    const uint64_t b = p_desc + sb * (G::kPBytes >> 4);
-    const uint32_t d = tm + G::kTmemO + ob * G::kOCols, old = (pend & 2) ? 0u : 1u;
-#pragma unroll
-    for (int mt = 0; mt < G::kMT; ++mt) {
-      const uint32_t a = tm + G::kTmemV + vb * G::kVCols + mt * 64;
-      umma_ts64(d + mt * NP, a, b, 32, G::kIdescO, old, el);
-      umma_ts64(d + mt * NP, a + 32, b + 128, 32, G::kIdescO, 1u, el);
-    }
-    umma_commit_if(&sh.vfree[vb], el);
-    umma_commit_if(&sh.pfree[sb], el);
-    if (pend & 4) umma_commit_if(&sh.oready[ob], el);
-    return true;
-  };
-  // one place issues O: the loop runs once more for the last tile
+  // O of the tile before: 1 there is one, 2 the first of its segment, 4 the last
+  int pend = 0;
   bool more = seg_wait(p, sh, ns, s);
-  int t = more ? s.t0 : 0;
-  while (ok && (more || pend)) {
+  int left = more ? s.t1 - s.t0 : 0;
+  bool first = true;
+#pragma unroll 1
+  while (more || pend) {
+    const uint32_t b = g & 1u, use = (g >> 1) & 1u;
     if (more) {
-      const uint32_t qb = ns & 1u, sb = g % G::kSB, kb = g % G::kKB;
-      ok = (t > s.t0 || warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error)) &&
-           warp_wait(&sh.kready[kb], (g / G::kKB) & 1u, &sh.abort, p.error) &&
-           warp_wait(&sh.sfree[sb], ((g / G::kSB) & 1u) ^ 1u, &sh.abort, p.error);
+      if (first) ok = warp_wait(&sh.qready[ns & 1u], (ns >> 1) & 1u, &sh.abort, p.error);
+      ok = ok && warp_wait(&sh.kready[b], use, &sh.abort, p.error);
       if (!ok) break;
       tc_fence_after();
+      const uint64_t q = q_desc + (ns & 1u) * (G::kQBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 64; ++kk)
-        umma_ts64(tm + G::kTmemS + sb * NP, tm + G::kTmemK + kb * G::kKCols + 32 * kk,
-                  q_desc + qb * (G::kQBytes >> 4) + kk * (NP * 128 >> 4), 2, G::kIdescS, kk > 0 ? 1u : 0u, el);
-      umma_commit_if(&sh.kfree[kb], el);
-      umma_commit_if(&sh.sfull[sb], el);
+        umma_ts64(tm + G::kTmemS + b * NP, tm + G::kTmemK + (G::kKB == 2 ? b * G::kKCols : 0) + 32 * kk,
+                  q + kk * (NP * 128 >> 4), 2, G::kIdescS, kk > 0 ? 1u : 0u, el);
+      umma_commit_if(&sh.sdone[b], el);
     }
-    if (pend) ok = issue_o(g - 1);
-    pend = 0;
-    if (more) {
-      pend = 1 | (t == s.t0 ? 2 : 0) | (t == s.t1 - 1 ? 4 : 0);
-      pend_ns = ns;
-      ++g;
-      if (++t == s.t1) {
-        seg_done(sh, ns);
-        more = seg_wait(p, sh, ++ns, s);
-        t = s.t0;
+    if (pend) {
+      const uint32_t pb = b ^ 1u, puse = ((g - 1) >> 1) & 1u;
+      // the segment whose tile it is: this one, or the one before where this tile is its first
+      const uint32_t pns = first || !more ? ns - 1 : ns, ob = pns % G::kOB;
+      ok = warp_wait(&sh.vready[pb], puse, &sh.abort, p.error) &&
+           warp_wait(&sh.pready[pb], puse, &sh.abort, p.error) &&
+           (!(pend & 2) || warp_wait(&sh.ofree[ob], ((pns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error));
+      if (!ok) break;
+      tc_fence_after();
+      // a step is 16 tokens: 512 bytes of P
+      const uint64_t pd = p_desc + pb * (G::kPBytes >> 4);
+      const uint32_t d = tm + G::kTmemO + ob * G::kOCols, a = tm + G::kTmemV + pb * G::kVCols;
+#pragma unroll
+      for (int mt = 0; mt < G::kMT; ++mt) {
+        umma_ts64(d + mt * NP, a + mt * 64, pd, 32, G::kIdescO, (pend & 2) ? 0u : 1u, el);
+        umma_ts64(d + mt * NP, a + mt * 64 + 32, pd + 128, 32, G::kIdescO, 1u, el);
       }
+      umma_commit_if(&sh.odone[pb], el);
+      if (pend & 4) umma_commit_if(&sh.oready[ob], el);
+    }
+    if (!more) break;
+    pend = 1 | (first ? 2 : 0) | (left == 1 ? 4 : 0);
+    first = false;
+    ++g;
+    if (--left == 0) {
+      seg_done(sh, ns);
+      more = seg_wait(p, sh, ++ns, s);
+      left = s.t1 - s.t0;
+      first = true;
     }
   }
   if (!ok || sh.abort) {  // what was issued completes before tensor memory is released
@@ -800,10 +825,10 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
     for (int c = 0; c < CW; ++c) l[c] = 0.0f;
 #pragma unroll 1
     for (int t = s.t0; t < s.t1; ++t, ++g) {
-      const uint32_t sb = g % G::kSB, pb = g & 1u;
-      const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + sb * NP + c0;
+      const uint32_t b = g & 1u;
+      const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + b * NP + c0;
       // S of tile g was issued behind O of tile g - 2, so P's buffer is free too
-      ok = ok && warp_wait(&sh.sfull[sb], (g / G::kSB) & 1u, &sh.abort, p.error);
+      ok = ok && warp_wait(&sh.sdone[b], (g >> 1) & 1u, &sh.abort, p.error);
       tc_fence_after();
       const int at = t * kTile + tok;
       const bool whole = t * kTile >= s.full_lo && t * kTile + kTile <= s.full_hi;
@@ -851,7 +876,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
                 w[c] = *reinterpret_cast<const uint32_t*>(&h);
               }
               top = h2_max(top, h2_max(h2_max(w[0], w[1]), h2_max(w[2], w[3])));
-              sts128(prow + pb * G::kPBytes + ((half * 2) ^ pflip), make_uint4(w[0], w[1], w[2], w[3]));
+              sts128(prow + b * G::kPBytes + ((half * 2) ^ pflip), make_uint4(w[0], w[1], w[2], w[3]));
             }
           }
           fence_async_shared();
@@ -891,7 +916,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
         unset = group_any(id, none);
         if (t != s.t0) {
           // O of the previous tile has to be complete before it is scaled
-          ok = warp_wait(&sh.pfree[(g - 1) & 1u], ((g - 1) >> 1) & 1u, &sh.abort, p.error);
+          ok = warp_wait(&sh.odone[b ^ 1u], ((g - 1) >> 1) & 1u, &sh.abort, p.error);
           tc_fence_after();
           if (ok) {
 #pragma unroll 1
@@ -915,10 +940,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
         }
       }
       // behind the vote: every thread of the group has read S and stored P
-      if (tok == 0 && ok) {
-        mbar_arrive(&sh.sfree[sb]);
-        mbar_arrive(&sh.pready[pb]);
-      }
+      if (tok == 0 && ok) mbar_arrive(&sh.pready[b]);
 #pragma unroll
       for (int c = 0; c < CW; c += 2) add_2(l[c], l[c + 1], e[c], e[c + 1]);
     }
@@ -1150,13 +1172,10 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
     }
     for (int u = 0; u < 2; ++u) {
       mbar_init(&sh.kready[u], 4);
-      mbar_init(&sh.kfree[u], 1);
       mbar_init(&sh.vready[u], 4);
-      mbar_init(&sh.vfree[u], 1);
-      mbar_init(&sh.sfull[u], 1);
-      mbar_init(&sh.sfree[u], G::kSoftGroups);
+      mbar_init(&sh.sdone[u], 1);
       mbar_init(&sh.pready[u], G::kSoftGroups);
-      mbar_init(&sh.pfree[u], 1);
+      mbar_init(&sh.odone[u], 1);
       mbar_init(&sh.qready[u], 4);
       mbar_init(&sh.oready[u], 1);
       mbar_init(&sh.ofree[u], 4);
