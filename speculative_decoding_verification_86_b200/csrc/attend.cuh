@@ -377,25 +377,34 @@ __device__ __forceinline__ int share_of(long long total, long long unit, int n) 
   return static_cast<int>(((unit + 1) * n - 1) / total);
 }
 
-// All lanes of a warp leave a wait together.  The patient part is out of line:
-// six roles share the SM's instruction caches, and it has some twenty sites.
-// It counts SM cycles (a read of the nanosecond clock holds up the unit that
-// also does the exponentials) and gives up, like mbar_wait, when another role
-// raised *abort, or after kWaitCycles, raising *abort and the error word.
+// Sleep on a barrier until its phase completes, or for about a millisecond.
+__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
+      : "memory");
+  return ok != 0;
+}
+// All lanes of a warp leave a wait together.  Most warps wait most of the time
+// and share the issue slots with the few that work, so a wait sleeps; and the
+// patient part is out of line, since six roles share the instruction caches.
+// Like mbar_wait it gives up when another role raised *abort, or after
+// kWaitCycles, raising *abort and the error word.
 constexpr long long kWaitCycles = 4000000000ll;  // 2 s: legitimate waits are microseconds
 __device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
-  long long t0 = 0;
+  const long long t0 = clock64();
   bool ok = true;
 #pragma unroll 1
-  for (uint32_t it = 1; !mbar_test(bar, parity); ++it) {
-    if ((it & 255u) != 0) continue;
+  while (!mbar_sleep(bar, parity)) {
     if (*static_cast<volatile int*>(abort)) {
       ok = false;
       break;
     }
-    const long long t = clock64();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitCycles) {
+    if (clock64() - t0 > kWaitCycles) {
       *static_cast<volatile int*>(abort) = 1;
       atomicOr(error, 1u);
       ok = false;
@@ -405,7 +414,7 @@ __device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, int*
   return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
-  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  if (__all_sync(0xffffffffu, mbar_sleep(bar, parity))) return true;
   return warp_wait_long(bar, parity, abort, error);
 }
 
@@ -659,9 +668,11 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
             w.x &= keep[0];
             w.y &= keep[1];
           }
-          const uint32_t nan0 = __vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          const uint32_t nan1 = __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          if (__any_sync(0xffffffffu, (nan0 | nan1) != 0)) {
+          // scales are 0..0x7e; 0x7f (NaN) plus one, or a sign, sets a byte's top bit
+          const uint32_t odd = ((w.x + 0x01010101u) | w.x | (w.y + 0x01010101u) | w.y) & 0x80808080u;
+          if (__any_sync(0xffffffffu, odd != 0)) {
+            const uint32_t nan0 = __vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            const uint32_t nan1 = __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
             // A NaN group must not meet the zeros of P (0 NaN = NaN): it is taken
             // out here, and the epilogue gives NaN to the rows that see it.
             const uint32_t ob = ns % G::kOB;
@@ -800,6 +811,18 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
   }
 }
 
+// Which of a thread's 16 rows see the token `at` (counted from the segment's
+// first run).
+__device__ __noinline__ uint32_t attend_see(const int2* lim, int at, uint32_t have) {
+  uint32_t m = 0;
+#pragma unroll 1
+  for (int c = 0; c < 16; ++c) {
+    const int2 v = lim[c];
+    if (at >= v.x && at < v.y) m |= 1u << c;
+  }
+  return have ? m : 0u;
+}
+
 template <int D, int NP>
 __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t p_smem) {
   using G = AttendGeo<D, NP>;
@@ -831,8 +854,10 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
       ok = ok && warp_wait(&sh.sdone[b], (g >> 1) & 1u, &sh.abort, p.error);
       tc_fence_after();
       const int at = t * kTile + tok;
-      const bool whole = t * kTile >= s.full_lo && t * kTile + kTile <= s.full_hi;
-      const bool have = (sh.kvalid[g & 3] >> (tok >> 4)) & 1u;
+      const uint32_t valid = sh.kvalid[g & 3];
+      const bool whole = t * kTile >= s.full_lo && t * kTile + kTile <= s.full_hi && valid == 0xffu;
+      uint32_t see = 0xffffu;  // rows that see this token
+      if (!whole) see = attend_see(&sh.lim[slot][c0], at, (valid >> (tok >> 4)) & 1u);
       float e[CW];         // S, then x - reference, then P
       bool again = false;  // a second pass follows a raised reference
 #pragma unroll 1
@@ -857,14 +882,8 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
               }
               if (!whole) {
 #pragma unroll
-                for (int c = half; c < half + 8; ++c) {
-                  const int2 v = sh.lim[slot][c0 + c];
-                  if (at < v.x || at >= v.y) e[c] = -INFINITY;
-                }
-              }
-              if (!have) {
-#pragma unroll
-                for (int c = half; c < half + 8; ++c) e[c] = -INFINITY;
+                for (int c = half; c < half + 8; ++c)
+                  if (!((see >> c) & 1u)) e[c] = -INFINITY;
               }
               uint32_t w[4];
 #pragma unroll
@@ -893,9 +912,7 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
           tmem_ld_wait();
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
-            const int2 v = sh.lim[slot][c0 + c + u];
-            const bool see = have && at >= v.x && at < v.y;
-            const float m = warp_max(see ? __fmul_rn(x[u], sh.cs[qb][c0 + c + u]) : -INFINITY);
+            const float m = warp_max(((see >> (c + u)) & 1u) ? __fmul_rn(x[u], sh.cs[qb][c0 + c + u]) : -INFINITY);
             if (lane == u) keep = m;
           }
           if (lane < 8) sh.red[quarter][c0 + c + lane] = keep;
