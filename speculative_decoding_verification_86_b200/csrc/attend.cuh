@@ -72,17 +72,25 @@ struct AttendCut {
 };
 
 constexpr int kSegs = 8;  // ring of planned segments
-constexpr int kSharedBytes = 14336;
+constexpr int kSharedBytes = 18432;
 
 template <int D, int NP>
 struct AttendGeo {
   static constexpr int kMT = (D + 127) / 128;   // tiles of 128 channels of O^T
+  // Softmax: two sets of one warpgroup that take the tiles in turn, each with its
+  // own references and its own O (a tile's path through wait, scores, vote is longer
+  // than the other roles'), where tensor memory holds both; else one set of two
+  // warpgroups by columns.
+  static constexpr int kSets = NP <= 32 && kMT * NP <= 32 ? 2 : 1;
+  static constexpr int kSoftGroups = NP > 32 ? 2 : 1;
+  static constexpr int kCW = NP / kSoftGroups;  // query rows per softmax thread
+  static constexpr int kSoftWarps = 4 * kSoftGroups * kSets;
   // buffers in tensor memory (512 columns)
   static constexpr int kKB = D > 128 ? 1 : 2;
-  static constexpr int kOB = D > 128 && NP > 16 ? 1 : 2;
+  static constexpr int kOB = D > 128 ? 1 : 2;
   static constexpr int kKCols = D / 2;          // 32-bit columns of one K buffer
   static constexpr int kVCols = 64 * kMT;
-  static constexpr int kOCols = kMT * NP;
+  static constexpr int kOCols = kSets * kMT * NP;
   static constexpr int kTmemK = 0;
   static constexpr int kTmemV = kTmemK + kKB * kKCols;
   static constexpr int kTmemS = kTmemV + 2 * kVCols;
@@ -90,9 +98,6 @@ struct AttendGeo {
   static constexpr int kTmemUsed = kTmemO + kOB * kOCols;
   static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kTmemUsed <= 512, "tensor memory");
-  static constexpr int kCW = 16;                // query rows per softmax thread
-  static constexpr int kSoftGroups = NP / kCW;  // warpgroups of the softmax, by columns
-  static constexpr int kSoftWarps = 4 * kSoftGroups;
   static constexpr int kWarpEpi = 8;
   static constexpr int kWarpSoft = 12;
   static constexpr int kWarpLoad = kWarpSoft + kSoftWarps;
@@ -142,23 +147,24 @@ struct alignas(16) AttendShared {
   AttendSeg seg[kSegs];
   uint32_t row[kSegs][NP];  // block token << 16 | query head of the group
   int2 lim[kSegs][NP];      // visible tokens of a row, counted from the segment's first run
-  unsigned long long nan_rows[2][G::kGroups];  // rows of O[ob] that see a NaN of the value group
+  int nan_seen[kSegs];  // the value decoder took NaN scales out of the segment
   uint32_t valid[8];   // per stage: runs that were copied
   uint32_t kvalid[4];  // the same by tile, for the softmax (which lags the stages)
   alignas(16) float cs[2][NP];  // log2 units of one unit of S, per query row
-  alignas(16) float nmr[NP];    // minus the subtracted exponent: kLift - mref, 0 while nothing was seen
-  alignas(16) float fac[NP];
-  float mref[NP];       // running maximum (log2 units)
-  float red[4][NP];
-  float mout[2][NP];    // references and sums (by warp) of a finished segment
-  float lsum[2][4][NP];
-  float inv[4][NP];
+  // by softmax set
+  alignas(16) float nmr[G::kSets][NP];  // minus the subtracted exponent: kLift - mref, 0 while nothing was seen
+  alignas(16) float fac[G::kSets][NP];
+  float mref[G::kSets][NP];     // running maximum (log2 units)
+  float red[G::kSets][4][NP];
+  float mout[2][G::kSets][NP];  // references and sums (by warp) of a finished segment
+  float lsum[2][G::kSets][4][NP];
+  float weight[4][G::kSets][NP];  // epilogue, by warp: factors of the sets' O
+  float turn[4][8][32];  // epilogue, by warp: eight rows of O
   long long scan[32];
   long long units;      // this CTA's share: number of units, and where it starts
   int start_i;
   long long start_off;
   uint32_t tmem;
-  int abort;
 };
 
 // ---------------------------------------------------------------- helpers --
@@ -284,15 +290,21 @@ __device__ __forceinline__ void add_2(float& a, float& b, float x, float y) {
       : "+f"(a), "+f"(b)
       : "f"(x), "f"(y));
 }
-// Sum of v[c] over the warp's lanes, in lane c (< N = 16): the lanes trade
-// halves of the columns.
-__device__ __forceinline__ float warp_column_sums(const float (&v)[16]) {
+// Sum of v[c] over the warp's lanes, in lane c (< N): the lanes trade halves of
+// the columns.
+template <int N>
+__device__ __forceinline__ float warp_column_sums(const float (&v)[N]) {
+  constexpr int W = N > 16 ? 32 : 16;
   const int lane = threadIdx.x & 31;
-  float x[16];
+  float x[W];
 #pragma unroll
-  for (int c = 0; c < 16; ++c) x[c] = v[c] + __shfl_xor_sync(0xffffffffu, v[c], 16);
+  for (int c = 0; c < W; ++c) x[c] = c < N ? v[c] : 0.0f;
+  if constexpr (W == 16) {
 #pragma unroll
-  for (int o = 8; o; o >>= 1) {
+    for (int c = 0; c < W; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], 16);
+  }
+#pragma unroll
+  for (int o = W / 2; o; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int c = 0; c < o; ++c) {
@@ -306,6 +318,16 @@ __device__ __forceinline__ float warp_column_sums(const float (&v)[16]) {
 __device__ __forceinline__ uint32_t h2_max(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 __device__ __forceinline__ float warp_max(float x) {
@@ -338,7 +360,7 @@ __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t
   return n >= 0 && n + L <= p.c.capacity;
 }
 
-__device__ __forceinline__ void attend_rows(const AttendParams& p, int64_t n, int L, int rt, AttendSeg& s) {
+__device__ __noinline__ void attend_rows(const AttendParams& p, int64_t n, int L, int rt, AttendSeg& s) {
   s.row0 = rt * p.rp;
   s.rows = min(p.rp, L * p.group - s.row0);
   const int j0 = s.row0 / p.group, j1 = (s.row0 + s.rows - 1) / p.group;
@@ -371,57 +393,30 @@ __device__ __noinline__ long long attend_units(const AttendParams& p, int i) {
   return u;
 }
 
+__device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
 // CTA c of n takes the units [total c / n, total (c + 1) / n); the CTA of a unit.
-__device__ __forceinline__ long long share_start(long long total, int c, int n) { return total * c / n; }
+__device__ __forceinline__ long long share_start(long long total, int c, int n) { return div64(total * c, n); }
 __device__ __forceinline__ int share_of(long long total, long long unit, int n) {
-  return static_cast<int>(((unit + 1) * n - 1) / total);
+  return static_cast<int>(div64((unit + 1) * n - 1, total));
 }
 
-// Sleep on a barrier until its phase completes, or for about a millisecond.
-__device__ __forceinline__ bool mbar_sleep(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(1000000u)
-      : "memory");
-  return ok != 0;
-}
-// All lanes of a warp leave a wait together.  Most warps wait most of the time
-// and share the issue slots with the few that work, so a wait sleeps; and the
-// patient part is out of line, since six roles share the instruction caches.
-// Like mbar_wait it gives up when another role raised *abort, or after
-// kWaitCycles, raising *abort and the error word.
-constexpr long long kWaitCycles = 4000000000ll;  // 2 s: legitimate waits are microseconds
-__device__ __noinline__ bool warp_wait_long(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
-  const long long t0 = clock64();
-  bool ok = true;
+// All lanes of a warp leave a wait together; false where the phase did not complete
+// within kWaitTries tries.  A try sleeps for up to 2700 cycles (measured), so that
+// is 1.5 s at most.  Nothing more happens here, since this stands at some thirty
+// places: a role that gives up returns false, which raises the error word, and
+// the roles that wait for it give up in their turn.
+constexpr uint32_t kWaitTries = 1u << 20;
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  while (!mbar_sleep(bar, parity)) {
-    if (*static_cast<volatile int*>(abort)) {
-      ok = false;
-      break;
-    }
-    if (clock64() - t0 > kWaitCycles) {
-      *static_cast<volatile int*>(abort) = 1;
-      atomicOr(error, 1u);
-      ok = false;
-      break;
-    }
-  }
-  return __all_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, unsigned* error) {
-  if (__all_sync(0xffffffffu, mbar_sleep(bar, parity))) return true;
-  return warp_wait_long(bar, parity, abort, error);
+  for (uint32_t left = kWaitTries; left; --left)
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return false;
 }
 
 // ------------------------------------------------------------------- roles --
 // One warp.  Also leaves the cut at the start of the share for k_attend_join.
 template <int D, int NP>
-__device__ __forceinline__ void attend_plan(const AttendParams& p, AttendShared<D, NP>& sh, long long u0,
+__device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<D, NP>& sh, long long u0,
                                             long long total, int n_ctas) {
   const int lane = threadIdx.x & 31;
   long long left = sh.units, off = sh.start_off;
@@ -439,7 +434,7 @@ __device__ __forceinline__ void attend_plan(const AttendParams& p, AttendShared<
       while ((per_head = attend_units(p, i)) <= 0) ++i;  // requests without units
       attend_len(p, i, n, L);
       nrt = (L * p.group + p.rp - 1) / p.rp;
-      h = static_cast<int>(off / per_head);
+      h = static_cast<int>(div64(off, per_head));
       off -= h * per_head;
       rt = 0;
       open = true;
@@ -465,10 +460,9 @@ __device__ __forceinline__ void attend_plan(const AttendParams& p, AttendShared<
         cut.last = share_of(total, first + s.tiles - 1, n_ctas);
       }
     }
-    left -= s.t1 - s.t0;
     off = 0;
     const int slot = static_cast<int>(ns % kSegs);
-    if (!warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u, &sh.abort, p.error)) break;
+    if (!warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u)) break;
     for (int r = lane; r < NP; r += 32) {
       const int row = s.row0 + r, j = row / p.group;
       sh.row[slot][r] = static_cast<uint32_t>(j) << 16 | static_cast<uint32_t>(row - j * p.group);
@@ -480,10 +474,14 @@ __device__ __forceinline__ void attend_plan(const AttendParams& p, AttendShared<
       }
       sh.lim[slot][r] = v;
     }
-    if (lane == 0) sh.seg[slot] = s;
+    if (lane == 0) {
+      sh.seg[slot] = s;
+      sh.nan_seen[slot] = 0;
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.segfull[slot]);
     ++ns;
+    left -= s.t1 - s.t0;
     if (++rt == nrt) {
       rt = 0;
       if (++h == p.c.heads) {
@@ -493,20 +491,24 @@ __device__ __forceinline__ void attend_plan(const AttendParams& p, AttendShared<
     }
   }
   const int slot = static_cast<int>(ns % kSegs);
-  if (warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u, &sh.abort, p.error) && lane == 0) {
-    sh.seg[slot].rows = 0;
-    mbar_arrive(&sh.segfull[slot]);
+  const bool ok = left == 0 && warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u);
+  if (lane == 0) {
+    if (ok) {
+      sh.seg[slot].rows = 0;
+      mbar_arrive(&sh.segfull[slot]);
+    }
+    p.cuts[blockIdx.x] = cut;
   }
-  if (lane == 0) p.cuts[blockIdx.x] = cut;
+  return ok;
 }
 
-// The roles' view of the ring.
+// The roles' view of the ring: the segment, or nullptr at the share's end (or
+// where the wait for it ran out; the plan's own wait tells).
 template <class SH>
-__device__ __forceinline__ bool seg_wait(const AttendParams& p, SH& sh, uint32_t ns, AttendSeg& s) {
+__device__ __forceinline__ const AttendSeg* seg_wait(SH& sh, uint32_t ns) {
   const int slot = static_cast<int>(ns % kSegs);
-  if (!warp_wait(&sh.segfull[slot], (ns / kSegs) & 1u, &sh.abort, p.error)) return false;
-  s = sh.seg[slot];
-  return s.rows > 0;
+  if (!warp_wait(&sh.segfull[slot], (ns / kSegs) & 1u)) return nullptr;
+  return sh.seg[slot].rows > 0 ? &sh.seg[slot] : nullptr;
 }
 template <class SH>
 __device__ __forceinline__ void seg_done(SH& sh, uint32_t ns) {
@@ -515,31 +517,33 @@ __device__ __forceinline__ void seg_done(SH& sh, uint32_t ns) {
 }
 
 template <int D, int NP>
-__device__ __forceinline__ void attend_producer(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages) {
+__device__ __forceinline__ bool attend_producer(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages) {
   using G = AttendGeo<D, NP>;
   const int lane = threadIdx.x & 31;
-  AttendSeg s;
   uint32_t g = 0;
   bool ok = true;
-  for (uint32_t ns = 0; ok && seg_wait(p, sh, ns, s); ++ns) {
+  const AttendSeg* sp;
+  for (uint32_t ns = 0; ok && (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+    const int i = sp->i, h = sp->h, t1 = sp->t1, hi = sp->hi;
+    const int64_t run0 = sp->run0;
     // a lane looks up one run; 32 runs are four tiles
     auto look_up = [&](int t) -> const uint8_t* {
       const int run = t * kTileRuns + lane;
-      if (run * kRun >= s.hi || run >= s.t1 * kTileRuns) return nullptr;
-      const uint8_t* a = cache_run<D>(p.c, s.i, s.h, s.run0 + run);
-      if (!a && p.status) atomicOr(p.status + s.i, kDevBadPage);
+      if (run * kRun >= hi || run >= t1 * kTileRuns) return nullptr;
+      const uint8_t* a = cache_run<D>(p.c, i, h, run0 + run);
+      if (!a && p.status) atomicOr(p.status + i, kDevBadPage);
       return a;
     };
-    const uint8_t* next = look_up(s.t0);
+    const uint8_t* next = look_up(sp->t0);
 #pragma unroll 1
-    for (int t = s.t0; ok && t < s.t1; t += 4) {
+    for (int t = sp->t0; ok && t < t1; t += 4) {
       const uint8_t* src = next;
-      if (t + 4 < s.t1) next = look_up(t + 4);
+      if (t + 4 < t1) next = look_up(t + 4);
       const uint32_t have = __ballot_sync(0xffffffffu, src != nullptr);
 #pragma unroll 1
-      for (int u = 0; u < 4 && t + u < s.t1; ++u, ++g) {
+      for (int u = 0; u < 4 && t + u < t1; ++u, ++g) {
         const int st = static_cast<int>(g % G::kStages);
-        if (!warp_wait(&sh.empty[st], ((g / G::kStages) & 1u) ^ 1u, &sh.abort, p.error)) {
+        if (!warp_wait(&sh.empty[st], ((g / G::kStages) & 1u) ^ 1u)) {
           ok = false;
           break;
         }
@@ -555,16 +559,15 @@ __device__ __forceinline__ void attend_producer(const AttendParams& p, AttendSha
     }
     seg_done(sh, ns);
   }
-  if (!ok || sh.abort) {  // the copies this warp issued land before the CTA's memory goes away
-    for (uint32_t e = g > G::kStages ? g - G::kStages : 0; e < g; ++e) {
-      volatile int no_abort = 0;
-      mbar_wait(&sh.full[e % G::kStages], (e / G::kStages) & 1u, &no_abort, p.error);
-    }
-  }
+  // the copies this warp issued land before the CTA's memory goes away
+#pragma unroll 1
+  for (uint32_t e = g > G::kStages ? g - G::kStages : 0; e < g; ++e)
+    ok = warp_wait(&sh.full[e % G::kStages], (e / G::kStages) & 1u) && ok;
+  return ok;
 }
 
 template <int D, int NP>
-__device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages) {
+__device__ __forceinline__ bool attend_keys(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages) {
   using G = AttendGeo<D, NP>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tok = warp * 32 + lane;
@@ -576,12 +579,12 @@ __device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<
   for (uint32_t g = 0; g < total; ++g) {
     const int st = static_cast<int>(g % G::kStages);
     const uint32_t kb = g % G::kKB;
-    if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u, &sh.abort, p.error)) return;
+    if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u)) return false;
     const uint32_t base = stages + st * G::kStageBytes;
     // the buffer's last reader: S of tile g - kKB
     if (g >= G::kKB &&
-        !warp_wait(&sh.sdone[(g - G::kKB) & 1u], ((g - G::kKB) >> 1) & 1u, &sh.abort, p.error))
-      return;
+        !warp_wait(&sh.sdone[(g - G::kKB) & 1u], ((g - G::kKB) >> 1) & 1u))
+      return false;
     tc_fence_after();
     // K of tile g follows S of tile g - kKB, so the softmax has read S of tile
     // g - 4 and its mask
@@ -615,41 +618,53 @@ __device__ __forceinline__ void attend_keys(const AttendParams& p, AttendShared<
       mbar_arrive(&sh.empty[st]);
     }
   }
+  return true;
 }
 
-// Rows of the segment that see a token (counted from run0).
-template <int D, int NP>
-__device__ __noinline__ unsigned long long attend_rows_seeing(const AttendParams& p, const AttendSeg& s, int token) {
+// 0xff in the bytes that are NaN as e4m3.
+__device__ __noinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+
+// Rows of a segment that see a NaN value of scale group `group` in the tiles of
+// this CTA, one warp: the rare second look at scales that the decoder took out.
+template <int D>
+__device__ __noinline__ unsigned long long attend_nan_rows(const AttendParams& p, const AttendSeg& s, int group) {
+  const int lane = threadIdx.x & 31;
   unsigned long long m = 0;
-  const int64_t pos = (s.run0 << 4) + token;
-  for (int r = 0; r < s.rows; ++r) {
-    const int64_t at = s.n + (s.row0 + r) / p.group;
-    const bool see = (p.causal ? pos <= at : pos < s.n + s.L) && (!p.window || pos > at - p.window);
-    if (see) m |= 1ull << r;
+  const int64_t base = s.run0 << 4;
+  for (int t = s.t0 * kTile + lane; t < min(s.t1 * kTile, s.hi); t += 32) {
+    if (t < s.lo) continue;
+    const uint8_t* run = cache_run<D>(p.c, s.i, s.h, s.run0 + (t >> 4));
+    if (!run || (run[run_v_scales(D) + group * 16 + (t & 15)] & 0x7fu) != kScaleNaN) continue;
+    for (int r = 0; r < s.rows; ++r) {
+      const int64_t q = s.n + (s.row0 + r) / p.group, pos = base + t;
+      if ((p.causal ? pos <= q : pos < s.n + s.L) && (!p.window || pos > q - p.window)) m |= 1ull << r;
+    }
   }
+  for (int o = 16; o; o >>= 1) m |= __shfl_xor_sync(0xffffffffu, m, o);
   return m;
 }
 
 template <int D, int NP>
-__device__ __forceinline__ void attend_values(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages,
+__device__ __forceinline__ bool attend_values(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t stages,
                                               uint32_t scratch) {
   using G = AttendGeo<D, NP>;
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(warp * 32) << 16) + G::kTmemV;
   const bool mine = warp * 32 < D;  // D = 64 fills half of the tile's rows
   scratch += warp * 512 * G::kMT;
-  AttendSeg s;
   uint32_t g = 0;
-  for (uint32_t ns = 0; seg_wait(p, sh, ns, s); ++ns) {
+  const AttendSeg* sp;
+  for (uint32_t ns = 0; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+    const int t1 = sp->t1, lo = sp->lo, hi = sp->hi;
 #pragma unroll 1
-    for (int t = s.t0; t < s.t1; ++t, ++g) {
+    for (int t = sp->t0; t < t1; ++t, ++g) {
       const int st = static_cast<int>(g % G::kStages);
       const uint32_t vb = g & 1u;
-      if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u, &sh.abort, p.error)) return;
+      if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u)) return false;
       const uint32_t base = stages + st * G::kStageBytes;
       const int tb = t * kTile;
       const uint32_t valid = sh.valid[st];
-      const bool whole = valid == 0xffu && tb >= s.lo && tb + kTile <= s.hi;
+      const bool whole = valid == 0xffu && tb >= lo && tb + kTile <= hi;
       if (mine) {
         // this warp's scales (two groups of every 128 channels) to fp16, eight tokens a lane
         const int sub = lane >> 2, grp = (lane >> 1) & 1, half = lane & 1;
@@ -662,7 +677,7 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
             uint32_t keep[2] = {0, 0};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const bool in = ((valid >> sub) & 1u) && first + e >= s.lo && first + e < s.hi;
+              const bool in = ((valid >> sub) & 1u) && first + e >= lo && first + e < hi;
               if (in) keep[e >> 2] |= 0xffu << (8 * (e & 3));
             }
             w.x &= keep[0];
@@ -671,24 +686,11 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
           // scales are 0..0x7e; 0x7f (NaN) plus one, or a sign, sets a byte's top bit
           const uint32_t odd = ((w.x + 0x01010101u) | w.x | (w.y + 0x01010101u) | w.y) & 0x80808080u;
           if (__any_sync(0xffffffffu, odd != 0)) {
-            const uint32_t nan0 = __vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            const uint32_t nan1 = __vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-            // A NaN group must not meet the zeros of P (0 NaN = NaN): it is taken
-            // out here, and the epilogue gives NaN to the rows that see it.
-            const uint32_t ob = ns % G::kOB;
-            if (!warp_wait(&sh.ofree[ob], ((ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error)) return;
-            if (nan0 | nan1) {
-#pragma unroll 1
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t bad = (e < 4 ? nan0 >> (8 * e) : nan1 >> (8 * (e - 4))) & 1u;
-                if (bad)
-                  atomicOr(&sh.nan_rows[ob][group],
-                           attend_rows_seeing<D, NP>(p, s, tb + sub * 16 + half * 8 + e));
-              }
-              w.x &= ~nan0;
-              w.y &= ~nan1;
-            }
-            __syncwarp();
+            // A NaN scale must not meet the zeros of P (0 NaN = NaN): it is taken out
+            // here, and the epilogue looks for the rows that see it.
+            w.x &= ~nan_bytes(w.x);
+            w.y &= ~nan_bytes(w.y);
+            sh.nan_seen[ns % kSegs] = 1;
           }
           sts128(scratch + mt * 512 + (sub * 2 + grp) * 32 + half * 16,
                  make_uint4(e4m3x2_to_f16x2(w.x & 0xffffu), e4m3x2_to_f16x2(w.x >> 16),
@@ -697,7 +699,7 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
         __syncwarp();
       }
       // the buffer's last reader: O of tile g - 2
-      if (!warp_wait(&sh.odone[vb], ((g >> 1) & 1u) ^ 1u, &sh.abort, p.error)) return;
+      if (!warp_wait(&sh.odone[vb], ((g >> 1) & 1u) ^ 1u)) return false;
       tc_fence_after();
       if (mine) {
 #pragma unroll
@@ -705,7 +707,9 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
           const uint32_t codes = base + run_v_codes(D) + (mt * 128 + warp * 32 + lane) * 8;
           const uint32_t sc = scratch + mt * 512 + (lane >> 4) * 32;
 #pragma unroll 1
-          for (int sub = 0; sub < kTileRuns; sub += 2) {
+          for (int half = 0; half < kTileRuns; half += 4)
+#pragma unroll
+          for (int sub = half; sub < half + 4; sub += 2) {
             uint32_t v[16];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -737,6 +741,7 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
     }
     seg_done(sh, ns);
   }
+  return true;
 }
 
 // One lane issues; the warp stays together.  S of tile g goes before O of tile
@@ -744,25 +749,26 @@ __device__ __forceinline__ void attend_values(const AttendParams& p, AttendShare
 // and the products of a tile), so it waits for nothing that another wait implies:
 // P of tile g - 2 stored (awaited for its O) means that S of that tile was read.
 template <int D, int NP>
-__device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem,
+__device__ __forceinline__ bool attend_mma(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem,
                                            uint32_t p_smem) {
   using G = AttendGeo<D, NP>;
-  AttendSeg s;
   uint32_t g = 0, ns = 0;
   bool ok = true;
   const uint32_t tm = sh.tmem, el = elect_one();
   const uint64_t q_desc = sw128_desc(q_smem), p_desc = sw32_n_desc(p_smem, kTile * 32);
-  // O of the tile before: 1 there is one, 2 the first of its segment, 4 the last
+  // O of the tile before: 1 there is one, 2 the first of its segment, 4 the last,
+  // 8 the first of its set in the segment
   int pend = 0;
-  bool more = seg_wait(p, sh, ns, s);
-  int left = more ? s.t1 - s.t0 : 0;
-  bool first = true;
+  const AttendSeg* sp = seg_wait(sh, ns);
+  bool more = sp != nullptr;
+  int left = more ? sp->t1 - sp->t0 : 0;
+  int idx = 0;  // of the tile in its segment
 #pragma unroll 1
   while (more || pend) {
     const uint32_t b = g & 1u, use = (g >> 1) & 1u;
     if (more) {
-      if (first) ok = warp_wait(&sh.qready[ns & 1u], (ns >> 1) & 1u, &sh.abort, p.error);
-      ok = ok && warp_wait(&sh.kready[b], use, &sh.abort, p.error);
+      if (idx == 0) ok = warp_wait(&sh.qready[ns & 1u], (ns >> 1) & 1u);
+      ok = ok && warp_wait(&sh.kready[b], use);
       if (!ok) break;
       tc_fence_after();
       const uint64_t q = q_desc + (ns & 1u) * (G::kQBytes >> 4);
@@ -775,127 +781,144 @@ __device__ __forceinline__ void attend_mma(const AttendParams& p, AttendShared<D
     if (pend) {
       const uint32_t pb = b ^ 1u, puse = ((g - 1) >> 1) & 1u;
       // the segment whose tile it is: this one, or the one before where this tile is its first
-      const uint32_t pns = first || !more ? ns - 1 : ns, ob = pns % G::kOB;
-      ok = warp_wait(&sh.vready[pb], puse, &sh.abort, p.error) &&
-           warp_wait(&sh.pready[pb], puse, &sh.abort, p.error) &&
-           (!(pend & 2) || warp_wait(&sh.ofree[ob], ((pns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error));
+      const uint32_t pns = idx == 0 || !more ? ns - 1 : ns, ob = pns % G::kOB;
+      ok = warp_wait(&sh.vready[pb], puse) &&
+           warp_wait(&sh.pready[pb], puse) &&
+           (!(pend & 2) || warp_wait(&sh.ofree[ob], ((pns / G::kOB) & 1u) ^ 1u));
       if (!ok) break;
       tc_fence_after();
       // a step is 16 tokens: 512 bytes of P
       const uint64_t pd = p_desc + pb * (G::kPBytes >> 4);
-      const uint32_t d = tm + G::kTmemO + ob * G::kOCols, a = tm + G::kTmemV + pb * G::kVCols;
+      const uint32_t d = tm + G::kTmemO + ob * G::kOCols + (G::kSets == 2 ? pb * (G::kMT * NP) : 0);
+      const uint32_t a = tm + G::kTmemV + pb * G::kVCols;
 #pragma unroll
       for (int mt = 0; mt < G::kMT; ++mt) {
-        umma_ts64(d + mt * NP, a + mt * 64, pd, 32, G::kIdescO, (pend & 2) ? 0u : 1u, el);
+        umma_ts64(d + mt * NP, a + mt * 64, pd, 32, G::kIdescO, (pend & 8) ? 0u : 1u, el);
         umma_ts64(d + mt * NP, a + mt * 64 + 32, pd + 128, 32, G::kIdescO, 1u, el);
       }
       umma_commit_if(&sh.odone[pb], el);
       if (pend & 4) umma_commit_if(&sh.oready[ob], el);
     }
     if (!more) break;
-    pend = 1 | (first ? 2 : 0) | (left == 1 ? 4 : 0);
-    first = false;
+    pend = 1 | (idx == 0 ? 2 : 0) | (left == 1 ? 4 : 0) | (idx < G::kSets ? 8 : 0);
+    ++idx;
     ++g;
     if (--left == 0) {
       seg_done(sh, ns);
-      more = seg_wait(p, sh, ++ns, s);
-      left = s.t1 - s.t0;
-      first = true;
+      sp = seg_wait(sh, ++ns);
+      more = sp != nullptr;
+      left = more ? sp->t1 - sp->t0 : 0;
+      idx = 0;
     }
   }
-  if (!ok || sh.abort) {  // what was issued completes before tensor memory is released
-    umma_commit_if(&sh.drain, el);
-    volatile int no_abort = 0;
-    mbar_wait(&sh.drain, 0, &no_abort, p.error);
-    __syncwarp();
-  }
+  // what was issued completes before tensor memory is released
+  umma_commit_if(&sh.drain, el);
+  return warp_wait(&sh.drain, 0) && ok;
 }
 
-// Which of a thread's 16 rows see the token `at` (counted from the segment's
-// first run).
+// Which of a thread's N rows see the token `at` (counted from the segment's first run).
+template <int N>
 __device__ __noinline__ uint32_t attend_see(const int2* lim, int at, uint32_t have) {
   uint32_t m = 0;
 #pragma unroll 1
-  for (int c = 0; c < 16; ++c) {
+  for (int c = 0; c < N; ++c) {
     const int2 v = lim[c];
     if (at >= v.x && at < v.y) m |= 1u << c;
   }
   return have ? m : 0u;
 }
 
+// Eight scores of a token to P: x - reference, with x = S cs rounded (the maximum
+// is taken of the same rounded x, so P stays in range at any size of the scores),
+// its power of two, and that in fp16.
+__device__ __forceinline__ void attend_p8(uint32_t s_tmem, const float* cs, const float* nmr, float one, bool whole,
+                                          uint32_t see, float (&e)[8], uint32_t (&w)[4]) {
+  tmem_ld8(s_tmem, e);
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < 8; c += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(cs + c);
+    const float4 m = *reinterpret_cast<const float4*>(nmr + c);
+    mul_add_2(e[c], e[c + 1], f.x, f.y, m.x, m.y, one);
+    mul_add_2(e[c + 2], e[c + 3], f.z, f.w, m.z, m.w, one);
+  }
+  if (!whole) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      if (!((see >> c) & 1u)) e[c] = -INFINITY;
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    e[2 * c] = ex2(e[2 * c]);
+    e[2 * c + 1] = ex2(e[2 * c + 1]);
+    const __half2 h = __floats2half2_rn(e[2 * c], e[2 * c + 1]);
+    w[c] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
 template <int D, int NP>
-__device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t p_smem) {
+__device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t p_smem) {
   using G = AttendGeo<D, NP>;
   constexpr int CW = G::kCW;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, wg = (warp - G::kWarpSoft) >> 2;
-  const int c0 = wg * CW, id = 1 + wg;
+  const int quarter = warp & 3, wg = ((warp - G::kWarpSoft) >> 2) % G::kSoftGroups;
+  const uint32_t set = ((warp - G::kWarpSoft) >> 2) / G::kSoftGroups;
+  const int c0 = wg * CW, id = 1 + ((warp - G::kWarpSoft) >> 2);
+  float* const nmr = sh.nmr[set];
   const int tok = quarter * 32 + lane;
   const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
-  // this token's 32 bytes of the P tile (sw32_n_desc)
-  const uint32_t prow = p_smem + wg * (kTile * 32) + tok * 32, pflip = (tok & 4) << 2;
-  AttendSeg s;
+  // this token's 32 bytes of a block of the P tile (sw32_n_desc)
+  const uint32_t prow = p_smem + tok * 32, pflip = (tok & 4) << 2;
   uint32_t g = 0;
   bool ok = true;
-  for (uint32_t ns = 0; seg_wait(p, sh, ns, s); ++ns) {
+  const AttendSeg* sp;
+  for (uint32_t ns = 0; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+    const int rows = sp->rows, t1 = sp->t1, full_lo = sp->full_lo, full_hi = sp->full_hi;
     const uint32_t qb = ns & 1u, ob = ns % G::kOB;
     const int slot = static_cast<int>(ns % kSegs);
-    const int cols = min(CW, ((s.rows - c0 + 7) & ~7));  // columns with rows in them: <= 0, 8 or 16
+    const int cols = min(CW, ((rows - c0 + 7) & ~7));  // columns with rows in them, by eights (or <= 0)
     bool unset = true;  // some row has seen nothing yet (uniform over the warpgroup)
-    ok = ok && warp_wait(&sh.qready[qb], (ns >> 1) & 1u, &sh.abort, p.error);
+    ok = ok && warp_wait(&sh.qready[qb], (ns >> 1) & 1u);
     float l[CW];
 #pragma unroll
     for (int c = 0; c < CW; ++c) l[c] = 0.0f;
+    bool fresh = true;  // this set's first tile of the segment
 #pragma unroll 1
-    for (int t = s.t0; t < s.t1; ++t, ++g) {
+    for (int t = sp->t0; t < t1; ++t, ++g) {
       const uint32_t b = g & 1u;
+      if (G::kSets == 2 && b != set) continue;
       const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + b * NP + c0;
       // S of tile g was issued behind O of tile g - 2, so P's buffer is free too
-      ok = ok && warp_wait(&sh.sdone[b], (g >> 1) & 1u, &sh.abort, p.error);
+      ok = ok && warp_wait(&sh.sdone[b], (g >> 1) & 1u);
       tc_fence_after();
       const int at = t * kTile + tok;
       const uint32_t valid = sh.kvalid[g & 3];
-      const bool whole = t * kTile >= s.full_lo && t * kTile + kTile <= s.full_hi && valid == 0xffu;
-      uint32_t see = 0xffffu;  // rows that see this token
-      if (!whole) see = attend_see(&sh.lim[slot][c0], at, (valid >> (tok >> 4)) & 1u);
-      float e[CW];         // S, then x - reference, then P
+      const bool whole = t * kTile >= full_lo && t * kTile + kTile <= full_hi && valid == 0xffu;
+      uint32_t see = 0xffffffffu;  // rows that see this token
+      if (!whole) see = attend_see<CW>(&sh.lim[slot][c0], at, (valid >> (tok >> 4)) & 1u);
+      uint32_t redo = 0;   // second pass: rows whose sums lack this tile
       bool again = false;  // a second pass follows a raised reference
 #pragma unroll 1
       for (;; again = true) {
         uint32_t top = 0;
         if (!unset || again) {
-          // x - reference, with x = S cs rounded: the maximum is taken of the same
-          // rounded x, so P stays in range at any size of the scores
 #pragma unroll
-          for (int half = 0; half < CW; half += 8)
-            if (half < cols) tmem_ld8(s_tmem + half, e + half);
-          tmem_ld_wait();
-#pragma unroll
-          for (int half = 0; half < CW; half += 8) {
-            if (half < cols) {
-#pragma unroll
-              for (int c = half; c < half + 8; c += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&sh.cs[qb][c0 + c]);
-                const float4 m = *reinterpret_cast<const float4*>(&sh.nmr[c0 + c]);
-                mul_add_2(e[c], e[c + 1], f.x, f.y, m.x, m.y, p.one);
-                mul_add_2(e[c + 2], e[c + 3], f.z, f.w, m.z, m.w, p.one);
-              }
-              if (!whole) {
-#pragma unroll
-                for (int c = half; c < half + 8; ++c)
-                  if (!((see >> c) & 1u)) e[c] = -INFINITY;
-              }
+          for (int c = 0; c < CW; c += 8) {
+            if (c < cols) {
+              float e[8];
               uint32_t w[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                float &a = e[half + 2 * c], &b = e[half + 2 * c + 1];
-                a = ex2(a);
-                b = ex2(b);
-                const __half2 h = __floats2half2_rn(a, b);
-                w[c] = *reinterpret_cast<const uint32_t*>(&h);
-              }
+              attend_p8(s_tmem + c, &sh.cs[qb][c0 + c], &nmr[c0 + c], p.one, whole, see >> c, e, w);
               top = h2_max(top, h2_max(h2_max(w[0], w[1]), h2_max(w[2], w[3])));
-              sts128(prow + b * G::kPBytes + ((half * 2) ^ pflip), make_uint4(w[0], w[1], w[2], w[3]));
+              sts128(prow + b * G::kPBytes + ((c0 + c) >> 4) * (kTile * 32) + ((((c0 + c) & 8) * 2) ^ pflip),
+                     make_uint4(w[0], w[1], w[2], w[3]));
+              if (!again) {
+#pragma unroll
+                for (int x = 0; x < 8; x += 2) add_2(l[c + x], l[c + x + 1], e[x], e[x + 1]);
+              } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                  if ((redo >> (c + x)) & 1u) l[c + x] += e[x];
+              }
             }
           }
           fence_async_shared();
@@ -903,7 +926,8 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
         tc_fence_before();
         const bool raise = !again && (unset || !ok || (top & 0xffffu) > kRaise || (top >> 16) > kRaise);
         if (!group_any(id, raise)) break;
-        if (group_any(id, !ok)) return;
+        if (group_any(id, !ok)) return false;
+        const bool unset_before = unset;
         // new references: the maximum over the tile's tokens of every row
 #pragma unroll 1
         for (int c = 0; c < cols; c += 8) {
@@ -915,65 +939,73 @@ __device__ __forceinline__ void attend_softmax(const AttendParams& p, AttendShar
             const float m = warp_max(((see >> (c + u)) & 1u) ? __fmul_rn(x[u], sh.cs[qb][c0 + c + u]) : -INFINITY);
             if (lane == u) keep = m;
           }
-          if (lane < 8) sh.red[quarter][c0 + c + lane] = keep;
+          if (lane < 8) sh.red[set][quarter][c0 + c + lane] = keep;
         }
         group_sync(id);
         bool none = false;
         if (tok < cols) {
           const int c = c0 + tok;
-          const float was = t == s.t0 ? -INFINITY : sh.mref[c];
-          const float m = fmaxf(fmaxf(fmaxf(sh.red[0][c], sh.red[1][c]), fmaxf(sh.red[2][c], sh.red[3][c])), was);
+          const float was = fresh ? -INFINITY : sh.mref[set][c];
+          const float m = fmaxf(fmaxf(fmaxf(sh.red[set][0][c], sh.red[set][1][c]), fmaxf(sh.red[set][2][c], sh.red[set][3][c])), was);
           // rounded up, so that x - reference is at most kLift; +inf gives NaN
           const float mr = m == -INFINITY ? 0.0f : (m == INFINITY ? NAN : __fsub_ru(m, kLift));
-          sh.fac[c] = was == -INFINITY ? 0.0f : ex2(-sh.nmr[c] - mr);
-          sh.mref[c] = m;
-          sh.nmr[c] = -mr;
-          none = c < s.rows && m == -INFINITY;
+          sh.fac[set][c] = was == -INFINITY ? 0.0f : ex2(-nmr[c] - mr);
+          sh.mref[set][c] = m;
+          nmr[c] = -mr;
+          none = c < rows && m == -INFINITY;
         }
         unset = group_any(id, none);
-        if (t != s.t0) {
-          // O of the previous tile has to be complete before it is scaled
-          ok = warp_wait(&sh.odone[b ^ 1u], ((g - 1) >> 1) & 1u, &sh.abort, p.error);
+        if (!fresh) {
+          // O of the set's previous tile has to be complete before it is scaled;
+          // with two sets that is tile g - 2, which S of tile g came after
+          if (G::kSets == 1) ok = warp_wait(&sh.odone[b ^ 1u], ((g - 1) >> 1) & 1u);
           tc_fence_after();
           if (ok) {
 #pragma unroll 1
             for (int mt = 0; mt < G::kMT; ++mt) {
-              const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + mt * NP + c0;
+              const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + (set * G::kMT + mt) * NP + c0;
 #pragma unroll 1
               for (int c = 0; c < cols; c += 8) {
                 float v[8];
                 tmem_ld8(o + c, v);
                 tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] *= sh.fac[c0 + c + x];
+                for (int x = 0; x < 8; ++x) v[x] *= sh.fac[set][c0 + c + x];
                 tmem_st8(o + c, v);
               }
             }
             tmem_st_wait();
           }
+        }
+        // The sums to the new references.  Where they hold this tile's P already,
+        // scaling is all they need, unless they overflowed: what came before the
+        // tile is then less than 2^-100 of it, and they start anew.
+        redo = unset_before ? 0xffffffffu : 0u;
 #pragma unroll
-          for (int c = 0; c < CW; ++c)
-            if (c < cols) l[c] *= sh.fac[c0 + c];
+        for (int c = 0; c < CW; ++c) {
+          const bool over = l[c] == INFINITY;
+          l[c] = over ? 0.0f : l[c] * sh.fac[set][c0 + c];
+          redo |= static_cast<uint32_t>(over) << c;
         }
       }
       // behind the vote: every thread of the group has read S and stored P
       if (tok == 0 && ok) mbar_arrive(&sh.pready[b]);
-#pragma unroll
-      for (int c = 0; c < CW; c += 2) add_2(l[c], l[c + 1], e[c], e[c + 1]);
+      fresh = false;
     }
     // the references and sums: over the warp's tokens here, over the warps in the epilogue
-    ok = ok && warp_wait(&sh.ofree[ob], ((ns / G::kOB) & 1u) ^ 1u, &sh.abort, p.error);
-    const float sum = warp_column_sums(l);
+    ok = ok && warp_wait(&sh.ofree[ob], ((ns / G::kOB) & 1u) ^ 1u);
+    const float sum = warp_column_sums<CW>(l);
     if (ok) {
       if (lane < CW) {
-        sh.lsum[ob][quarter][c0 + lane] = sum;
-        if (quarter == 0) sh.mout[ob][c0 + lane] = -sh.nmr[c0 + lane];
+        sh.lsum[ob][set][quarter][c0 + lane] = sum;
+        if (quarter == 0) sh.mout[ob][set][c0 + lane] = -nmr[c0 + lane];
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.lready[ob]);
     }
     seg_done(sh, ns);
   }
+  return ok;
 }
 
 // Q of a segment: rows to fp16 times a power of two that brings the row's
@@ -984,7 +1016,6 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
                                               uint32_t ns, uint32_t q_smem) {
   using G = AttendGeo<D, NP>;
   constexpr int E = D / 32;  // elements of a lane
-  constexpr int RB = 4;      // rows of a warp in flight
   const int warp = (threadIdx.x >> 5) - G::kWarpEpi, lane = threadIdx.x & 31;
   const uint32_t qb = ns & 1u;
   const int ch = lane * E;
@@ -992,66 +1023,55 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
                       static_cast<int64_t>(s.h * p.group) * p.q.sh + ch;
   const float gk = p.c.k_scale ? __ldg(p.c.k_scale + s.h) : 1.0f;
   const float unit = p.scale * 1.4426950408889634f * gk;
-#pragma unroll 1
-  for (int r0 = 0; r0 < NP; r0 += 4 * RB) {
-    uint32_t raw[RB][E / 2];
-#pragma unroll
-    for (int u = 0; u < RB; ++u) {
-      const int r = r0 + 4 * u + warp;
-      if (r < s.rows) {
-        const uint32_t at = sh.row[ns % kSegs][r];
-        const uint16_t* src = q + (at >> 16) * p.q.st + (at & 0xffffu) * p.q.sh;
-        if constexpr (E == 2) {
-          raw[u][0] = __ldg(reinterpret_cast<const uint32_t*>(src));
-        } else if constexpr (E == 4) {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(src));
-          raw[u][0] = w.x, raw[u][1] = w.y;
-        } else {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
-          raw[u][0] = w.x, raw[u][1] = w.y, raw[u][2] = w.z, raw[u][3] = w.w;
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) raw[u][e] = 0;
-      }
+  struct alignas(E * 2) Raw {
+    uint32_t w[E / 2];
+  };
+  auto fetch = [&](int r) {
+    Raw x{};
+    if (r < s.rows) {
+      const uint32_t at = sh.row[ns % kSegs][r];
+      x = *reinterpret_cast<const Raw*>(q + (at >> 16) * p.q.st + (at & 0xffffu) * p.q.sh);
     }
+    return x;
+  };
+  Raw next[2] = {fetch(warp), fetch(warp + 4)};  // two rows in flight
+#pragma unroll 1
+  for (int r = warp; r < NP; r += 4) {
+    const Raw raw = next[0];
+    next[0] = next[1];
+    next[1] = fetch(r + 8);
+    float x[E];
+    uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < RB; ++u) {
-      const int r = r0 + 4 * u + warp;
-      float x[E];
-      uint32_t top = 0;
+    for (int e = 0; e < E / 2; ++e) {
+      float2 f;
+      if (p.bf16) f = make_float2(__uint_as_float(raw.w[e] << 16), __uint_as_float(raw.w[e] & 0xffff0000u));
+      else f = h2_to_f2(raw.w[e]);
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+      top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    const bool bad = top >= 0x7f800000u;  // NaN or infinity: the whole row is NaN
+    const int k = bad ? 0 : 14 + 127 - static_cast<int>(top >> 23);
+    // 2^k in two factors: k reaches 141
+    const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (k >> 1)) << 23);
+    const float f2 = __uint_as_float(static_cast<uint32_t>(127 + (k - (k >> 1))) << 23);
+    Raw w;
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        float2 f;
-        if (p.bf16) f = make_float2(__uint_as_float(raw[u][e] << 16), __uint_as_float(raw[u][e] & 0xffff0000u));
-        else f = h2_to_f2(raw[u][e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
-        top = max(top, max(__float_as_uint(f.x) & 0x7fffffffu, __float_as_uint(f.y) & 0x7fffffffu));
-      }
-      top = __reduce_max_sync(0xffffffffu, top);
-      const bool bad = top >= 0x7f800000u;  // NaN or infinity: the whole row is NaN
-      const int k = bad ? 0 : 14 + 127 - static_cast<int>(top >> 23);
-      // 2^k in two factors: k reaches 141
-      const float f1 = __uint_as_float(static_cast<uint32_t>(127 + (k >> 1)) << 23);
-      const float f2 = __uint_as_float(static_cast<uint32_t>(127 + (k - (k >> 1))) << 23);
-      uint32_t w[E / 2];
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        const __half2 h = __floats2half2_rn(bad ? 0.0f : x[2 * e] * f1 * f2, bad ? 0.0f : x[2 * e + 1] * f1 * f2);
-        w[e] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      const uint32_t a = q_smem + qb * G::kQBytes + (ch >> 6) * (NP * 128) + r * 128 +
-                         (((ch & 63) * 2) ^ ((r & 7) << 4));
-      if constexpr (E == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w[0]) : "memory");
-      else if constexpr (E == 4)
-        asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(w[0]), "r"(w[1]) : "memory");
-      else sts128(a, make_uint4(w[0], w[1], w[2], w[3]));
-      if (lane == 0) {
-        const float b1 = __uint_as_float(static_cast<uint32_t>(127 - (k >> 1)) << 23);
-        const float b2 = __uint_as_float(static_cast<uint32_t>(127 - (k - (k >> 1))) << 23);
-        sh.cs[qb][r] = r >= s.rows ? 0.0f : (bad ? NAN : unit * b1 * b2);
-      }
+    for (int e = 0; e < E / 2; ++e) {
+      const __half2 h = __floats2half2_rn(bad ? 0.0f : x[2 * e] * f1 * f2, bad ? 0.0f : x[2 * e + 1] * f1 * f2);
+      w.w[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const uint32_t a = q_smem + qb * G::kQBytes + (ch >> 6) * (NP * 128) + r * 128 + (((ch & 63) * 2) ^ ((r & 7) << 4));
+    if constexpr (E == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w.w[0]) : "memory");
+    else if constexpr (E == 4)
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(w.w[0]), "r"(w.w[1]) : "memory");
+    else sts128(a, make_uint4(w.w[0], w.w[1], w.w[2], w.w[3]));
+    if (lane == 0) {
+      const float b1 = __uint_as_float(static_cast<uint32_t>(127 - (k >> 1)) << 23);
+      const float b2 = __uint_as_float(static_cast<uint32_t>(127 - (k - (k >> 1))) << 23);
+      sh.cs[qb][r] = r >= s.rows ? 0.0f : (bad ? NAN : unit * b1 * b2);
     }
   }
   fence_async_shared();
@@ -1060,7 +1080,7 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
 }
 
 template <int D, int NP>
-__device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem) {
+__device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendShared<D, NP>& sh, uint32_t q_smem) {
   using G = AttendGeo<D, NP>;
   const int warp = (threadIdx.x >> 5) - G::kWarpEpi, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
@@ -1070,31 +1090,52 @@ __device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendSha
   // free in turn, since O of segment na - 2 was the last that used its own
 #pragma unroll 1
   for (uint32_t na = 0; more; ++na) {
-    more = seg_wait(p, sh, na, ahead);
-    if (more) attend_load_q<D, NP>(p, sh, ahead, na, q_smem);
+    const AttendSeg* sp = seg_wait(sh, na);
+    more = sp != nullptr;
+    if (more) {
+      ahead = *sp;
+      attend_load_q<D, NP>(p, sh, ahead, na, q_smem);
+    }
     if (na == 0) {
       s = ahead;
       continue;
     }
     const uint32_t ns = na - 1, ob = ns % G::kOB, par = (ns / G::kOB) & 1u;
-    if (!warp_wait(&sh.lready[ob], par, &sh.abort, p.error)) return;
-    if (!warp_wait(&sh.oready[ob], par, &sh.abort, p.error)) return;
+    if (!warp_wait(&sh.lready[ob], par)) return false;
+    if (!warp_wait(&sh.oready[ob], par)) return false;
     tc_fence_after();
     const bool cut = s.t0 > 0 || s.t1 < s.tiles;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 > 0 ? 0 : 1);
     const uint32_t* row = sh.row[ns % kSegs];
     const float gv = p.c.v_scale ? __ldg(p.c.v_scale + s.h) : 1.0f;
     for (int r = lane; r < s.rows; r += 32) {
-      const float l = (sh.lsum[ob][0][r] + sh.lsum[ob][1][r]) + (sh.lsum[ob][2][r] + sh.lsum[ob][3][r]);
-      const float mr = sh.mout[ob][r];
-      sh.inv[warp][r] = l == 0.0f ? 0.0f : __frcp_rn(l);
+      // join the sets: a set that saw nothing of the row (or had no tile) has l = 0
+      float l[G::kSets], mr = -INFINITY, sum = 0.0f;
+#pragma unroll
+      for (int u = 0; u < G::kSets; ++u) {
+        const float* x = &sh.lsum[ob][u][0][r];
+        l[u] = (x[0] + x[NP]) + (x[2 * NP] + x[3 * NP]);
+        if (l[u] != 0.0f) mr = fmaxf(mr, sh.mout[ob][u][r]);
+      }
+      if (mr == -INFINITY) mr = 0.0f;
+#pragma unroll
+      for (int u = 0; u < G::kSets; ++u) {
+        const float w = l[u] != 0.0f ? ex2(sh.mout[ob][u][r] - mr) : 0.0f;
+        sh.weight[warp][u][r] = w;
+        if (w != 0.0f) sum += w * l[u];
+      }
+      if (!cut) {
+        const float inv = sum == 0.0f ? 0.0f : rcp(sum);
+#pragma unroll
+        for (int u = 0; u < G::kSets; ++u) sh.weight[warp][u][r] *= inv;
+      }
       if (warp == 0) {
         if (cut) {
-          p.part_l[slot * NP + r] = make_float2(mr, l);
+          p.part_l[slot * NP + r] = make_float2(mr, sum);
         } else if (p.lse) {
           const uint32_t at = row[r];
           p.lse[(static_cast<int64_t>(s.i) * p.T + (at >> 16)) * p.heads_q + s.h * p.group + (at & 0xffffu)] =
-              l == 0.0f ? -INFINITY : (mr + log2f(l)) * 0.6931471805599453f;
+              sum == 0.0f ? -INFINITY : (mr + lg2(sum)) * 0.6931471805599453f;
         }
       }
     }
@@ -1105,44 +1146,58 @@ __device__ __forceinline__ void attend_epilogue(const AttendParams& p, AttendSha
       const int ch = mt * 128 + warp * 32 + lane;
       const bool mine = ch < D;
       unsigned long long nan = 0;
-      if (mine) nan = *static_cast<volatile unsigned long long*>(&sh.nan_rows[ob][ch / kGroup]);
+      if (sh.nan_seen[ns % kSegs] && mine) {  // a warp's channels are two groups
+        const unsigned long long n0 = attend_nan_rows<D>(p, sh.seg[ns % kSegs], (mt * 128 + warp * 32) / kGroup);
+        const unsigned long long n1 = attend_nan_rows<D>(p, sh.seg[ns % kSegs], (mt * 128 + warp * 32) / kGroup + 1);
+        nan = lane < 16 ? n0 : n1;
+      }
 #pragma unroll 1
       for (int c = 0; c < s.rows; c += 8) {
-        float v[8];
-        tmem_ld8(sh.tmem + lanes + G::kTmemO + ob * G::kOCols + mt * NP + c, v);
+        float v[8], u[8];
+        const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + mt * NP + c;
+        tmem_ld8(o, v);
+        if (G::kSets == 2) tmem_ld8(o + G::kMT * NP, u);
         tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {  // a set without weight may hold anything
+          const float f = sh.weight[warp][0][min(c + x, NP - 1)];
+          v[x] = f != 0.0f ? v[x] * f : 0.0f;
+          if (G::kSets == 2) {
+            const float w = sh.weight[warp][G::kSets - 1][min(c + x, NP - 1)];
+            if (w != 0.0f) v[x] = fmaf(u[x], w, v[x]);
+          }
+        }
         if (!mine) continue;
         if (nan >> c) {
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             if ((nan >> (c + x)) & 1ull) v[x] = NAN;
         }
-        if (cut) {
-          float* dst = p.part_o + (static_cast<int64_t>(slot) * NP + c) * D + ch;
+        // (a loop over rows reads them back one by one: shorter than eight copies)
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (c + x < s.rows) dst[x * D] = v[x];
-        } else {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            if (c + x < s.rows) {
-              const uint32_t at = row[c + x];
-              const int64_t to = out + (at >> 16) * p.out.st + (at & 0xffffu) * p.out.sh + ch;
-              const float f = v[x] * sh.inv[warp][c + x] * gv;
-              if (p.bf16) static_cast<__nv_bfloat16*>(p.out.data)[to] = __float2bfloat16_rn(f);
-              else static_cast<__half*>(p.out.data)[to] = __float2half_rn(f);
-            }
+        for (int x = 0; x < 8; ++x) sh.turn[warp][x][lane] = v[x];
+#pragma unroll 1
+        for (int r = c; r < min(c + 8, s.rows); ++r) {
+          const float o = sh.turn[warp][r - c][lane];
+          if (cut) {
+            p.part_o[(static_cast<int64_t>(slot) * NP + r) * D + ch] = o;
+          } else {
+            const uint32_t at = row[r];
+            const int64_t to = out + (at >> 16) * p.out.st + (at & 0xffffu) * p.out.sh + ch;
+            const float f = o * gv;
+            static_cast<uint16_t*>(p.out.data)[to] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f))
+                                                            : __half_as_ushort(__float2half_rn(f));
           }
         }
       }
       __syncwarp();
-      if (mine && nan && (lane & 15) == 0) sh.nan_rows[ob][ch / kGroup] = 0;
     }
     tc_fence_before();
     seg_done(sh, ns);
     if (lane == 0) mbar_arrive(&sh.ofree[ob]);
     s = ahead;
   }
+  return true;
 }
 
 // Exclusive prefix of v over the CTA, and the total.
@@ -1203,12 +1258,11 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
       mbar_init(&sh.segfree[u], G::kSegReaders);
     }
     mbar_init(&sh.drain, 1);
-    sh.abort = 0;
     sh.start_i = 0;
     sh.start_off = 0;
     mbar_init_fence();
   }
-  if (threadIdx.x < 2 * G::kGroups) (&sh.nan_rows[0][0])[threadIdx.x] = 0;
+  if (threadIdx.x < kSegs) sh.nan_seen[threadIdx.x] = 0;
   if (warp == G::kWarpMma) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
                  "r"(G::kTmemCols)
@@ -1257,21 +1311,23 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   __syncthreads();
   tc_fence_after();
 
+  bool ok;
   if (warp == G::kWarpLoad) {
-    attend_producer<D, NP>(p, sh, stages);
+    ok = attend_producer<D, NP>(p, sh, stages);
   } else if (warp == G::kWarpMma) {
-    attend_mma<D, NP>(p, sh, q_smem, p_smem);
+    ok = attend_mma<D, NP>(p, sh, q_smem, p_smem);
   } else if (warp == G::kWarpPlan) {
-    attend_plan<D, NP>(p, sh, u0, total, n);
+    ok = attend_plan<D, NP>(p, sh, u0, total, n);
   } else if (warp < 4) {
-    attend_keys<D, NP>(p, sh, stages);
+    ok = attend_keys<D, NP>(p, sh, stages);
   } else if (warp < 8) {
-    attend_values<D, NP>(p, sh, stages, scratch);
+    ok = attend_values<D, NP>(p, sh, stages, scratch);
   } else if (warp < G::kWarpSoft) {
-    attend_epilogue<D, NP>(p, sh, q_smem);
+    ok = attend_epilogue<D, NP>(p, sh, q_smem);
   } else {
-    attend_softmax<D, NP>(p, sh, p_smem);
+    ok = attend_softmax<D, NP>(p, sh, p_smem);
   }
+  if (!ok) atomicOr(p.error, 1u);
   tc_fence_before();
   __syncthreads();
   if (warp == G::kWarpMma) {
