@@ -7,6 +7,7 @@ the library is missing or fails to load, :func:`lib` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -197,6 +198,16 @@ def _dev_ptr(t, dtype=None, device=None, name="tensor"):
 def _stream_handle(stream, device):
     s = stream if stream is not None else torch.cuda.current_stream(device)
     return s.cuda_stream
+
+
+# The current stream's handle by device number: a tenth of current_stream's time.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_number(stream, device):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(device.index)
+    return _stream_handle(stream, device)
 
 
 class SpecVerifier:
@@ -848,6 +859,7 @@ class BlockCache:
         self.device = dev
         self.heads_q, self.heads_kv, self.head_dim = int(heads_q), int(heads_kv), int(head_dim)
         self.page_size, self.max_batch = int(page_size), int(max_batch)
+        self._page_shape = torch.Size((self.heads_kv, self.page_size // 16, 18 * self.head_dim))
         h = _vp()
         _check(lib().spec_cache_init(ctypes.byref(h), dev.index, self.max_batch, self.heads_q,
                                      self.heads_kv, self.head_dim, self.page_size), "spec_cache_init")
@@ -890,54 +902,75 @@ class BlockCache:
         return int(out.value)
 
     # -- helpers --------------------------------------------------------------
+    # A call is a few microseconds on the GPU, so the checks are plain ones: one
+    # look at a tensor's shape, strides, device number and type each.
+    def _dev(self, t, dtype, name):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s must be a torch.Tensor" % name)
+        if t.get_device() != self.device.index:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, self.device))
+        if t.dtype is not dtype:
+            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+
     def _pages(self, pages, table, B, k_scale, v_scale):
-        shape = (self.heads_kv, self.page_size // 16, 18 * self.head_dim)
-        if pages.dim() != 4 or tuple(pages.shape[1:]) != shape:
-            raise ValueError("pages must be [num_pages, %d, %d, %d]" % shape)
-        if table.dim() != 2 or table.shape[0] != B:
+        self._dev(pages, torch.uint8, "pages")
+        n = pages.shape
+        if len(n) != 4 or n[1:] != self._page_shape:
+            raise ValueError("pages must be [num_pages, %d, %d, %d]" % tuple(self._page_shape))
+        if not pages.is_contiguous():
+            raise ValueError("pages must be contiguous")
+        self._dev(table, torch.int32, "table")
+        w = table.shape
+        if len(w) != 2 or w[0] != B:
             raise ValueError("table must be [B, width] with B = %d" % B)
-        if not table.is_cuda or table.device != self.device:
-            raise ValueError("table must be on %s" % self.device)
-        if table.dtype != torch.int32:
-            raise TypeError("table must be torch.int32, got %s" % table.dtype)
-        if table.shape[1] > 1 and table.stride(1) != 1:
+        stride = table.stride()
+        if w[1] > 1 and stride[1] != 1:
             raise ValueError("a row of the table must be contiguous")
-        for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-            if s is not None and tuple(s.shape) != (self.heads_kv,):
-                raise ValueError("%s must be [%d]" % (name, self.heads_kv))
-        stride = table.stride(0) if B > 1 else table.shape[1]
-        return CachePages(_dev_ptr(pages, torch.uint8, self.device, "pages"), pages.shape[0],
-                          table.data_ptr(), stride, table.shape[1],
-                          _dev_ptr(k_scale, torch.float32, self.device, "k_scale"),
-                          _dev_ptr(v_scale, torch.float32, self.device, "v_scale"))
+        return CachePages(pages.data_ptr(), n[0], table.data_ptr(), stride[0] if B > 1 else w[1], w[1],
+                          self._vector(k_scale, torch.float32, self.heads_kv, "k_scale"),
+                          self._vector(v_scale, torch.float32, self.heads_kv, "v_scale"))
 
     def _rows(self, t, heads, name, shape=None, dtype=None):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s must be a torch.Tensor" % name)
-        if not t.is_cuda or t.device != self.device:
+        if t.get_device() != self.device.index:
             raise ValueError("%s must be on %s" % (name, self.device))
-        if t.dtype not in _CACHE_DTYPES or (dtype is not None and t.dtype != dtype):
-            raise TypeError("%s has dtype %s" % (name, t.dtype))
-        if t.dim() != 4 or tuple(t.shape[2:]) != (heads, self.head_dim) or \
-                (shape is not None and tuple(t.shape[:2]) != tuple(shape)):
-            raise ValueError("%s must be [B, T, %d, %d], got %s" % (name, heads, self.head_dim, tuple(t.shape)))
-        if t.stride(3) != 1:
+        dt = t.dtype
+        if dt not in _CACHE_DTYPES or (dtype is not None and dt is not dtype):
+            raise TypeError("%s has dtype %s" % (name, dt))
+        n = t.shape
+        if len(n) != 4 or n[2] != heads or n[3] != self.head_dim or (shape is not None and n[:2] != shape):
+            raise ValueError("%s must be [B, T, %d, %d], got %s" % (name, heads, self.head_dim, tuple(n)))
+        b, r, h, c = t.stride()
+        if c != 1:
             raise ValueError("the channels of %s must be contiguous" % name)
         # the stride of a dimension of one element says nothing
-        st = [t.stride(d) if t.shape[d] > 1 else 0 for d in range(3)]
-        return CacheRows(t.data_ptr(), *st)
+        return CacheRows(t.data_ptr(), b if n[0] > 1 else 0, r if n[1] > 1 else 0, h if heads > 1 else 0)
+
+    def _vector(self, t, dtype, n, name):
+        if t is None:
+            return None
+        self._dev(t, dtype, name)
+        if t.shape != (n,):
+            raise ValueError("%s must be [%d]" % (name, n))
+        if n > 1 and t.stride()[0] != 1:
+            raise ValueError("%s must be contiguous" % name)
+        return t.data_ptr()
 
     def _ints(self, t, B, name):
-        if t is not None and tuple(t.shape) != (B,):
-            raise ValueError("%s must be [B] = [%d]" % (name, B))
-        return _dev_ptr(t, torch.int32, self.device, name)
+        return self._vector(t, torch.int32, B, name)
 
     @staticmethod
-    def _one_place(t, name):
+    def _on(stream):
+        """Outputs that a call makes are filled on the stream that it runs on."""
+        return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+    @staticmethod
+    def _one_place(rows, shape, name):
         """Rows that are written must not share memory (an expanded dimension)."""
-        for d in range(t.dim()):
-            if t.shape[d] > 1 and t.stride(d) == 0:
-                raise ValueError("%s must not be an expanded tensor" % name)
+        if (shape[0] > 1 and rows.stride_b == 0) or (shape[1] > 1 and rows.stride_t == 0) or \
+                (shape[2] > 1 and rows.stride_h == 0):
+            raise ValueError("%s must not be an expanded tensor" % name)
 
     # -- entry points ---------------------------------------------------------
     def write(self, k, v, pages, table, cache_len, block_len=None, k_scale=None, v_scale=None,
@@ -956,7 +989,7 @@ class BlockCache:
         st = lib().spec_cache_write(
             self._h, ctypes.byref(pg), ctypes.byref(kr), ctypes.byref(vr), _CACHE_DTYPES[k.dtype],
             self._ints(cache_len, B, "cache_len"), self._ints(block_len, B, "block_len"), B, T,
-            self._ints(status, B, "status"), _stream_handle(stream, self.device))
+            self._ints(status, B, "status"), _stream_number(stream, self.device))
         _check(st, "spec_cache_write")
 
     def read(self, pages, table, start=None, count=None, rows=None, dtype=torch.bfloat16, k_scale=None,
@@ -969,21 +1002,22 @@ class BlockCache:
             if rows is None:
                 raise ValueError("rows is needed where out is not given")
             shape = (B, int(rows), self.heads_kv, self.head_dim)
-            out = (torch.zeros(shape, dtype=dtype, device=self.device),
-                   torch.zeros(shape, dtype=dtype, device=self.device))
+            with self._on(stream):
+                out = (torch.zeros(shape, dtype=dtype, device=self.device),
+                       torch.zeros(shape, dtype=dtype, device=self.device))
         k, v = out
         if k.dim() != 4 or (rows is not None and k.shape[1] != rows):
             raise ValueError("out must be two [B, rows, %d, %d] tensors" % (self.heads_kv, self.head_dim))
         T = k.shape[1]
         kr = self._rows(k, self.heads_kv, "out[0]", (B, T))
         vr = self._rows(v, self.heads_kv, "out[1]", (B, T), k.dtype)
-        self._one_place(k, "out[0]")
-        self._one_place(v, "out[1]")
+        self._one_place(kr, k.shape, "out[0]")
+        self._one_place(vr, v.shape, "out[1]")
         pg = self._pages(pages, table, B, k_scale, v_scale)
         st = lib().spec_cache_read(
             self._h, ctypes.byref(pg), self._ints(start, B, "start"), self._ints(count, B, "count"), B, T,
             _CACHE_DTYPES[k.dtype], ctypes.byref(kr), ctypes.byref(vr), self._ints(status, B, "status"),
-            _stream_handle(stream, self.device))
+            _stream_number(stream, self.device))
         _check(st, "spec_cache_read")
         return out
 
@@ -1004,21 +1038,27 @@ class BlockCache:
         if cache_len is None:
             raise ValueError("cache_len is needed")
         if out is None:
-            out = torch.zeros((B, T, self.heads_q, self.head_dim), dtype=q.dtype, device=self.device)
+            with self._on(stream):
+                out = torch.zeros((B, T, self.heads_q, self.head_dim), dtype=q.dtype, device=self.device)
         outr = self._rows(out, self.heads_q, "out", (B, T), q.dtype)
-        self._one_place(out, "out")
+        self._one_place(outr, out.shape, "out")
         if lse is None or lse is True:
-            lse = torch.full((B, T, self.heads_q), float("-inf"), device=self.device)
+            with self._on(stream):
+                lse = torch.full((B, T, self.heads_q), float("-inf"), device=self.device)
         elif lse is False:
             lse = None
-        elif tuple(lse.shape) != (B, T, self.heads_q):
-            raise ValueError("lse must be [B, T, %d]" % self.heads_q)
+        lse_ptr = None
+        if lse is not None:
+            self._dev(lse, torch.float32, "lse")
+            if lse.shape != (B, T, self.heads_q) or not lse.is_contiguous():
+                raise ValueError("lse must be a contiguous [B, T, %d]" % self.heads_q)
+            lse_ptr = lse.data_ptr()
         pg = self._pages(pages, table, B, k_scale, v_scale)
         st = lib().spec_cache_attend(
             self._h, ctypes.byref(pg), ctypes.byref(qr), _CACHE_DTYPES[q.dtype],
             self._ints(cache_len, B, "cache_len"), self._ints(block_len, B, "block_len"), B, T,
             float(self.head_dim ** -0.5 if scale is None else scale), int(bool(causal)), int(window),
-            ctypes.byref(outr), _dev_ptr(lse, torch.float32, self.device, "lse"),
-            self._ints(status, B, "status"), _stream_handle(stream, self.device))
+            ctypes.byref(outr), lse_ptr,
+            self._ints(status, B, "status"), _stream_number(stream, self.device))
         _check(st, "spec_cache_attend")
         return out, lse

@@ -71,10 +71,11 @@ spec_status check_rows(const spec_cache_rows* r, spec_dtype dtype, sv::CacheRows
   return SPEC_OK;
 }
 
-// Launch the write or the read with one warp per 64 channels of a run.
+// Launch the write (a warp per 64 channels of a run, keys or values) or the read
+// (a warp per run).
 template <bool WRITE, int D>
 spec_status launch_move(const sv::CacheMove& p, spec_dtype dtype, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(p.B) * p.runs * p.c.heads * 2 * (D / 64);
+  const int64_t warps = static_cast<int64_t>(p.B) * p.runs * p.c.heads * 2 * (WRITE ? D / 64 : 1);
   const int64_t blocks = (warps * 32 + sv::kMoveThreads - 1) / sv::kMoveThreads;
   if (blocks > 0x7fffffff) return SPEC_ERR_INVALID_ARG;
   const dim3 g(static_cast<unsigned>(blocks)), b(sv::kMoveThreads);

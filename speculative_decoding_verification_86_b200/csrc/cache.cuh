@@ -73,15 +73,35 @@ __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&r)[4]) {
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
       : "r"(w));
 }
-// Two values -> two e2m1 codes in a byte (lo in the low four bits), to nearest,
+// Eight values -> eight e2m1 codes, the first in the low four bits: to nearest,
 // ties to even, saturating.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float (&q)[8]) {
   uint32_t r;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}\n"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}\n"
       : "=r"(r)
-      : "f"(lo), "f"(hi));
+      : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]), "f"(q[7]));
+  return r;
+}
+// (a, b) * (c, c) and (a, b) * (c, c) + (d, e), two at a time.
+__device__ __forceinline__ float2 mul_pair(float2 a, float c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float2 fma_pair(float2 a, float c, float2 d) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %6};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(c), "f"(d.x), "f"(d.y));
   return r;
 }
 // e4m3 of a value in [0, 448], to nearest, ties to even.
@@ -99,32 +119,44 @@ __device__ __forceinline__ float2 h2_to_f2(uint32_t a) {
   return __half22float2(*reinterpret_cast<const __half2*>(&a));
 }
 
-// 16 neighbouring channels of a row, as fp32 (32 or 64 aligned bytes).
+// 16 neighbouring channels of a row, as fp32 (32 or 64 aligned bytes); returns the
+// largest magnitude, NaN where there is a NaN.
 template <typename T>
-__device__ __forceinline__ void load_group(const T* p, float (&x)[16]) {
+__device__ __forceinline__ float load_group(const T* p, float (&x)[16]) {
   if constexpr (sizeof(T) == 4) {
+    uint32_t top = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float4 f = __ldg(reinterpret_cast<const float4*>(p) + u);
       x[4 * u] = f.x, x[4 * u + 1] = f.y, x[4 * u + 2] = f.z, x[4 * u + 3] = f.w;
     }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);  // NaN above all
+    return __uint_as_float(top);
   } else {
+    uint4 w[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + u);
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    for (int u = 0; u < 2; ++u) w[u] = __ldg(reinterpret_cast<const uint4*>(p) + u);
+    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    uint32_t top = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float2 f;
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          f = make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
-        } else {
-          f = h2_to_f2(v[e]);
-        }
-        x[8 * u + 2 * e] = f.x;
-        x[8 * u + 2 * e + 1] = f.y;
+    for (int e = 0; e < 8; ++e) {
+      float2 f;
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        f = make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(v[e] & 0x7fff7fffu));
+      } else {
+        f = h2_to_f2(v[e]);
+        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(top) : "r"(v[e] & 0x7fff7fffu));
       }
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
     }
+    float2 t;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      t = make_float2(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
+    else t = h2_to_f2(top);
+    return t.x != t.x || t.x > t.y ? t.x : t.y;
   }
 }
 template <typename T>
@@ -154,40 +186,35 @@ __device__ __forceinline__ void store_group(T* p, const float (&x)[16]) {
 }
 
 // Quantise one group.  `code` gets the sixteen codes, channel c in bits 4c;
-// returns the scale's byte.  rg = RN(1/g).
-// The quotient y / s is formed as q0 = y r, q = fma(fma(-q0, s, y), r, q0) with
-// r = RN(1/s): the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34,
-// 1990).  A correctly rounded quotient lies on a midpoint of two codes only if
+// returns the scale's byte.  rg = RN(1/g); `top` is max |x|, NaN or infinite where
+// an element is: |y| <= RN(top rg), since rounding is monotone.
+// The quotient y / s is formed as q0 = y r, q = q0 - (q0 s - y) r with r = RN(1/s):
+// the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990), and -0
+// for y = -0.  A correctly rounded quotient lies on a midpoint of two codes only if
 // the exact one does (the midpoints have three significant bits), so the
 // conversion's ties-to-even decides exactly the ties of y / s.
-__device__ __forceinline__ uint32_t quantise_group(const float (&x)[16], float rg, uint64_t& code) {
-  float y[16];
-  float top = 0.0f;
-  bool bad = false;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    y[e] = __fmul_rn(x[e], rg);
-    top = fmaxf(top, fabsf(y[e]));
-    bad |= !(fabsf(y[e]) < INFINITY);
-  }
+__device__ __forceinline__ uint32_t quantise_group(const float (&x)[16], float top, float rg, uint64_t& code) {
+  top = __fmul_rn(top, rg);
+  const bool bad = !(top < INFINITY);
   uint32_t sb = f32_to_e4m3(fminf(__fdiv_rn(top, 6.0f), 448.0f));
   sb = sb ? sb : 1u;  // 2^-9, the smallest scale
   const float s = h2_to_f2(e4m3x2_to_f16x2(sb)).x;
   const float r = __frcp_rn(s);
-  uint32_t lo = 0, hi = 0;
+  uint32_t w[2];
 #pragma unroll
-  for (int e = 0; e < 16; e += 2) {
-    float q[2];
+  for (int u = 0; u < 2; ++u) {
+    float q[8];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float q0 = __fmul_rn(y[e + u], r);
-      q[u] = copysignf(__fmaf_rn(__fmaf_rn(-q0, s, y[e + u]), r, q0), y[e + u]);  // -0 stays -0
+    for (int e = 0; e < 8; e += 2) {
+      const float2 yn = mul_pair(make_float2(x[8 * u + e], x[8 * u + e + 1]), -rg);  // -y
+      const float2 q0 = mul_pair(yn, -r);
+      const float2 v = fma_pair(fma_pair(q0, s, yn), -r, q0);
+      q[e] = v.x;
+      q[e + 1] = v.y;
     }
-    const uint32_t b = f32x2_to_e2m1x2(q[0], q[1]);
-    if (e < 8) lo |= b << (4 * e);
-    else hi |= b << (4 * (e - 8));
+    w[u] = f32x8_to_e2m1(q);
   }
-  code = bad ? 0ull : (static_cast<uint64_t>(hi) << 32) | lo;
+  code = bad ? 0ull : (static_cast<uint64_t>(w[1]) << 32) | w[0];
   return bad ? kScaleNaN : sb;
 }
 
@@ -234,21 +261,17 @@ __device__ __forceinline__ bool cache_span(const CacheMove& p, int i, int64_t& n
   return n >= 0 && n + L <= p.c.capacity;
 }
 
-// One warp moves 64 channels of one run of one (request, head), keys or values:
-// lane = token pair b (tokens 2b, 2b+1) + 8 * scale group.  A pair of tokens
-// fills one byte of a value's row, so a warp holds whole rows of codes, and no
-// two warps touch the same bytes.  The work is a streaming pass: 128-byte rows
-// in, 256-byte runs of codes out, so it is bound by memory; a lane keeps its 64
-// input bytes in flight, and there are enough warps (a prompt of 8191 tokens
-// has 16 K) to cover the table look-up before the store.
+// One warp moves a run of one (request, head), keys or values (the write: 64
+// channels of it): lane = token pair b (tokens 2b, 2b+1) + 8 * scale group.  A pair
+// of tokens fills one byte of a value's row, so a warp holds whole rows of codes, and
+// no two warps touch the same bytes.
 struct CacheTask {
   int i, h, chunk, is_v;
   int64_t run;
 };
-template <int D>
+template <int C>
 __device__ __forceinline__ bool cache_task(const CacheMove& p, CacheTask& t) {
   int64_t w = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
-  constexpr int C = D / 64;
   t.chunk = static_cast<int>(w % C);
   w /= C;
   t.is_v = static_cast<int>(w & 1);
@@ -266,7 +289,7 @@ constexpr int kMoveThreads = 128;
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   CacheTask t;
-  if (!cache_task<D>(p, t)) return;
+  if (!cache_task<D / 64>(p, t)) return;
   const int lane = threadIdx.x & 31;
   int64_t n;
   int L;
@@ -287,14 +310,14 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   const float* gs = t.is_v ? p.c.v_scale : p.c.k_scale;
   const float rg = gs ? __frcp_rn(__ldg(gs + t.h)) : 1.0f;
   const T* src = static_cast<const T*>(rows.data) + t.i * rows.sb + t.h * rows.sh + g * kGroup;
-  float x[2][16];
+  float x[2][16], top[2] = {0.0f, 0.0f};
   bool in[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int tok = 2 * b + u;
     in[u] = tok >= lo && tok < hi;
     if (in[u]) {
-      load_group(src + (run * kRun + tok - n) * rows.st, x[u]);
+      top[u] = load_group(src + (run * kRun + tok - n) * rows.st, x[u]);
     } else {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[u][e] = 0.0f;
@@ -308,7 +331,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   uint64_t code[2];
   uint32_t sc[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) sc[u] = quantise_group(x[u], rg, code[u]);
+  for (int u = 0; u < 2; ++u) sc[u] = quantise_group(x[u], top[u], rg, code[u]);
   if (!t.is_v) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -361,7 +384,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
   CacheTask t;
-  if (!cache_task<D>(p, t)) return;
+  if (!cache_task<1>(p, t)) return;  // the whole run: all its bytes in flight
   const int lane = threadIdx.x & 31;
   int64_t n;
   int L;
@@ -380,55 +403,66 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
       atomicOr(p.status + t.i, kDevBadPage);
     return;
   }
-  const int b = lane & 7, g = t.chunk * 4 + (lane >> 3);
+  const int b = lane & 7;
   const float* gs = t.is_v ? p.c.v_scale : p.c.k_scale;
   const float gv = gs ? __ldg(gs + t.h) : 1.0f;
-  uint64_t code[2];
-  uint32_t sc[2];
-  if (!t.is_v) {
+  constexpr int C = D / 64;
+  uint4 raw[C];  // keys: token 2b's codes, token 2b + 1's; values: channel 2b's, channel 2b + 1's
+  uint32_t sc[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int g = c * 4 + (lane >> 3);
+    if (!t.is_v) {
+      const uint8_t* at = src + (g >> 1) * 256 + 2 * b * 16 + (g & 1) * 8;
+      const uint2 k0 = *reinterpret_cast<const uint2*>(at), k1 = *reinterpret_cast<const uint2*>(at + 16);
+      raw[c] = make_uint4(k0.x, k0.y, k1.x, k1.y);
+      const uint8_t* s = src + run_k_scales(D) + 2 * b * (D / kGroup) + g;
+      sc[c] = s[0] | (static_cast<uint32_t>(s[D / kGroup]) << 8);
+    } else {
+      raw[c] = *reinterpret_cast<const uint4*>(src + run_v_codes(D) + (g * kGroup + 2 * b) * 8);
+      sc[c] = *reinterpret_cast<const uint16_t*>(src + run_v_scales(D) + g * kRun + 2 * b);
+    }
+  }
+  const CacheRows& rows = t.is_v ? p.v : p.k;
+  T* out = static_cast<T*>(rows.data) + t.i * rows.sb + t.h * rows.sh;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int g = c * 4 + (lane >> 3);
+    uint32_t code[2][2] = {{raw[c].x, raw[c].y}, {raw[c].z, raw[c].w}};
+    if (t.is_v) {
+      const uint4 o = raw[c];
+      uint32_t w[4] = {__byte_perm(o.x, o.z, 0x5140), __byte_perm(o.x, o.z, 0x7362),
+                       __byte_perm(o.y, o.w, 0x5140), __byte_perm(o.y, o.w, 0x7362)};
+      transpose_lanes8(w, b);  // byte: a channel of the tokens 2b (low four bits), 2b + 1
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        // eight channels' bytes to the eight codes of each token
+        const uint32_t l0 = w[2 * q] & 0x0f0f0f0fu, l1 = w[2 * q + 1] & 0x0f0f0f0fu;
+        const uint32_t h0 = (w[2 * q] >> 4) & 0x0f0f0f0fu, h1 = (w[2 * q + 1] >> 4) & 0x0f0f0f0fu;
+        code[0][q] = __byte_perm(l0 | (l0 >> 4), l1 | (l1 >> 4), 0x6420);
+        code[1][q] = __byte_perm(h0 | (h0 >> 4), h1 | (h1 >> 4), 0x6420);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int tok = 2 * b + u;
-      code[u] = *reinterpret_cast<const uint64_t*>(src + (g >> 1) * 256 + tok * 16 + (g & 1) * 8);
-      sc[u] = src[run_k_scales(D) + tok * (D / kGroup) + g];
-    }
-  } else {
-    const uint4 o = *reinterpret_cast<const uint4*>(src + run_v_codes(D) + (g * kGroup + 2 * b) * 8);
-    uint32_t w[4] = {__byte_perm(o.x, o.z, 0x5140), __byte_perm(o.x, o.z, 0x7362),
-                     __byte_perm(o.y, o.w, 0x5140), __byte_perm(o.y, o.w, 0x7362)};
-    transpose_lanes8(w, b);  // byte c: channel c of the tokens 2b (low four bits), 2b+1
-    code[0] = code[1] = 0;
+      if (tok < lo || tok >= hi) continue;
+      const uint32_t one = u ? sc[c] >> 8 : sc[c] & 0xffu;
+      const uint32_t s2 = e4m3x2_to_f16x2(one | (one << 8));
+      float x[16];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t a = w[q] & 0x0f0f0f0fu, c = (w[q] >> 4) & 0x0f0f0f0fu;
-      a = (a | (a >> 4)) & 0x00ff00ffu, c = (c | (c >> 4)) & 0x00ff00ffu;
-      a = (a | (a >> 8)) & 0xffffu, c = (c | (c >> 8)) & 0xffffu;
-      code[0] |= static_cast<uint64_t>(a) << (16 * q);
-      code[1] |= static_cast<uint64_t>(c) << (16 * q);
-    }
-    const uint32_t two = *reinterpret_cast<const uint16_t*>(src + run_v_scales(D) + g * kRun + 2 * b);
-    sc[0] = two & 0xffu, sc[1] = two >> 8;
-  }
-  const CacheRows& rows = t.is_v ? p.v : p.k;
-  T* out = static_cast<T*>(rows.data) + t.i * rows.sb + t.h * rows.sh + g * kGroup;
+      for (int q = 0; q < 2; ++q) {
+        uint32_t h[4];
+        e2m1x8_to_f16(code[u][q], h);
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int tok = 2 * b + u;
-    if (tok < lo || tok >= hi) continue;
-    const uint32_t s2 = e4m3x2_to_f16x2(sc[u] | (sc[u] << 8));
-    float x[16];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t h[4];
-      e2m1x8_to_f16(static_cast<uint32_t>(code[u] >> (32 * q)), h);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = h2_to_f2(h2_mul(h[e], s2));
-        x[8 * q + 2 * e] = __fmul_rn(f.x, gv);
-        x[8 * q + 2 * e + 1] = __fmul_rn(f.y, gv);
+        for (int e = 0; e < 4; ++e) {
+          const float2 f = mul_pair(h2_to_f2(h2_mul(h[e], s2)), gv);
+          x[8 * q + 2 * e] = f.x;
+          x[8 * q + 2 * e + 1] = f.y;
+        }
       }
+      store_group(out + (run * kRun + tok - n) * rows.st + g * kGroup, x);
     }
-    store_group(out + (run * kRun + tok - n) * rows.st, x);
   }
 }
 
