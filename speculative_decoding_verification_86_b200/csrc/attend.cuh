@@ -104,7 +104,7 @@ struct AttendGeo {
   static constexpr int kWarpMma = kWarpLoad + 1;
   static constexpr int kWarpPlan = kWarpMma + 1;
   static constexpr int kThreads = 32 * (kWarpPlan + 1);
-  static constexpr int kSegReaders = 1 + 1 + 4 + kSoftWarps + 4;  // warps that read a segment
+  static constexpr int kSegReaders = 1 + 1 + 4 + 4 + kSoftWarps + 4;  // warps that read a segment
   static constexpr int kGroups = D / kGroup;
   static constexpr uint32_t kStageBytes = kTileRuns * run_bytes(D);
   static constexpr uint32_t kQBytes = NP * D * 2;
@@ -159,7 +159,7 @@ struct alignas(16) AttendShared {
   float mout[2][G::kSets][NP];  // references and sums (by warp) of a finished segment
   float lsum[2][G::kSets][4][NP];
   float weight[4][G::kSets][NP];  // epilogue, by warp: factors of the sets' O
-  float turn[4][8][32];  // epilogue, by warp: eight rows of O
+  long long to[4][NP];    // and where its rows go
   long long scan[32];
   long long units;      // this CTA's share: number of units, and where it starts
   int start_i;
@@ -353,7 +353,10 @@ __device__ __forceinline__ void group_sync(int id) {
 }
 
 // ------------------------------------------------------------- work shares --
-// A request's units, in order: head, row tile, token tile.
+// A request's units, in order: head, row tile, token tile.  A segment (one row
+// tile of one head) counts kSegUnits more than its tiles: that is what its first
+// references, its Q and its output cost beside them.
+constexpr int kSegUnits = 6;
 __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t& n, int& L) {
   n = __ldg(p.cache_len + i);
   L = p.block_len ? min(max(__ldg(p.block_len + i), 0), p.T) : p.T;
@@ -388,7 +391,7 @@ __device__ __noinline__ long long attend_units(const AttendParams& p, int i) {
 #pragma unroll 1
   for (int rt = 0; rt < nrt; ++rt) {
     attend_rows(p, n, L, rt, s);
-    u += s.tiles;
+    u += s.tiles + kSegUnits;
   }
   return u;
 }
@@ -440,17 +443,18 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
       open = true;
     }
     attend_rows(p, n, L, rt, s);
-    if (off >= s.tiles) {  // only where the share starts behind a row tile
-      off -= s.tiles;
+    const int all = s.tiles + kSegUnits;
+    if (off >= all) {  // only where the share starts behind a row tile
+      off -= all;
       ++rt;
       continue;
     }
     s.i = i;
     s.h = h;
-    s.t0 = static_cast<int>(off);
-    s.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), off + left));
+    s.t0 = static_cast<int>(max(off - kSegUnits, 0ll));
+    s.t1 = static_cast<int>(max(min(static_cast<long long>(all), off + left) - kSegUnits, 0ll));
     if (ns == 0 && s.t0 > 0) {
-      const long long first = u0 - s.t0;
+      const long long first = u0 - s.t0;  // the segment's first tile
       if (share_of(total, first, n_ctas) == static_cast<int>(blockIdx.x) - 1) {
         cut.i = s.i;
         cut.h = s.h;
@@ -460,28 +464,31 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
         cut.last = share_of(total, first + s.tiles - 1, n_ctas);
       }
     }
+    const long long here = min(static_cast<long long>(all) - off, left);
     off = 0;
-    const int slot = static_cast<int>(ns % kSegs);
-    if (!warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u)) break;
-    for (int r = lane; r < NP; r += 32) {
-      const int row = s.row0 + r, j = row / p.group;
-      sh.row[slot][r] = static_cast<uint32_t>(j) << 16 | static_cast<uint32_t>(row - j * p.group);
-      int2 v = make_int2(0, INT_MAX);
-      if (r < s.rows) {
-        const int64_t base = s.run0 << 4, pos = n + j;
-        v.x = p.window ? static_cast<int>(max(pos + 1 - p.window - base, int64_t(0))) : 0;
-        v.y = static_cast<int>((p.causal ? pos + 1 : n + L) - base);
+    if (s.t1 > s.t0) {
+      const int slot = static_cast<int>(ns % kSegs);
+      if (!warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u)) break;
+      for (int r = lane; r < NP; r += 32) {
+        const int row = s.row0 + r, j = row / p.group;
+        sh.row[slot][r] = static_cast<uint32_t>(j) << 16 | static_cast<uint32_t>(row - j * p.group);
+        int2 v = make_int2(0, INT_MAX);
+        if (r < s.rows) {
+          const int64_t base = s.run0 << 4, pos = n + j;
+          v.x = p.window ? static_cast<int>(max(pos + 1 - p.window - base, int64_t(0))) : 0;
+          v.y = static_cast<int>((p.causal ? pos + 1 : n + L) - base);
+        }
+        sh.lim[slot][r] = v;
       }
-      sh.lim[slot][r] = v;
+      if (lane == 0) {
+        sh.seg[slot] = s;
+        sh.nan_seen[slot] = 0;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.segfull[slot]);
+  ++ns;
     }
-    if (lane == 0) {
-      sh.seg[slot] = s;
-      sh.nan_seen[slot] = 0;
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.segfull[slot]);
-    ++ns;
-    left -= s.t1 - s.t0;
+    left -= here;
     if (++rt == nrt) {
       rt = 0;
       if (++h == p.c.heads) {
@@ -574,49 +581,54 @@ __device__ __forceinline__ bool attend_keys(const AttendParams& p, AttendShared<
   const uint32_t row = (tok >> 4) * run_bytes(D) + (tok & 15) * 16;
   const uint32_t scales = (tok >> 4) * run_bytes(D) + run_k_scales(D) + (tok & 15) * G::kGroups;
   const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(warp * 32) << 16) + G::kTmemK;
-  const uint32_t total = static_cast<uint32_t>(sh.units);
+  uint32_t g = 0;
+  const AttendSeg* sp;
+  for (uint32_t ns = 0; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+    const uint32_t end = g + static_cast<uint32_t>(sp->t1 - sp->t0);
 #pragma unroll 1
-  for (uint32_t g = 0; g < total; ++g) {
-    const int st = static_cast<int>(g % G::kStages);
-    const uint32_t kb = g % G::kKB;
-    if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u)) return false;
-    const uint32_t base = stages + st * G::kStageBytes;
-    // the buffer's last reader: S of tile g - kKB
-    if (g >= G::kKB &&
-        !warp_wait(&sh.sdone[(g - G::kKB) & 1u], ((g - G::kKB) >> 1) & 1u))
-      return false;
-    tc_fence_after();
-    // K of tile g follows S of tile g - kKB, so the softmax has read S of tile
-    // g - 4 and its mask
-    if (tok == 0) sh.kvalid[g & 3] = sh.valid[st];
+    for (; g != end; ++g) {
+      const int st = static_cast<int>(g % G::kStages);
+      const uint32_t kb = g % G::kKB;
+      if (!warp_wait(&sh.full[st], (g / G::kStages) & 1u)) return false;
+      const uint32_t base = stages + st * G::kStageBytes;
+      // the buffer's last reader: S of tile g - kKB
+      if (g >= G::kKB &&
+          !warp_wait(&sh.sdone[(g - G::kKB) & 1u], ((g - G::kKB) >> 1) & 1u))
+        return false;
+      tc_fence_after();
+      // K of tile g follows S of tile g - kKB, so the softmax has read S of tile
+      // g - 4 and its mask
+      if (tok == 0) sh.kvalid[g & 3] = sh.valid[st];
 #pragma unroll 1
-    for (int c = 0; c < D / 32; c += 2) {
-      uint32_t four;  // the scales of two chunks' groups
-      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(four) : "r"(base + scales + 2 * c));
+      for (int c = 0; c < D / 32; c += 2) {
+        uint32_t four;  // the scales of two chunks' groups
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(four) : "r"(base + scales + 2 * c));
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const uint4 w = lds128(base + row + (c + u) * 256);
-        const uint32_t sc = e4m3x2_to_f16x2(u ? four >> 16 : four & 0xffffu);
-        const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        uint32_t v[16];
+        for (int u = 0; u < 2; ++u) {
+          const uint4 w = lds128(base + row + (c + u) * 256);
+          const uint32_t sc = e4m3x2_to_f16x2(u ? four >> 16 : four & 0xffffu);
+          const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+          uint32_t v[16];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          uint32_t h[4];
-          e2m1x8_to_f16(ww[x], h);
+          for (int x = 0; x < 4; ++x) {
+            uint32_t h[4];
+            e2m1x8_to_f16(ww[x], h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[4 * x + e] = h2_mul(h[e], x < 2 ? s0 : s1);
+            for (int e = 0; e < 4; ++e) v[4 * x + e] = h2_mul(h[e], x < 2 ? s0 : s1);
+          }
+          tmem_st16(tmem + kb * G::kKCols + (c + u) * 16, v);
         }
-        tmem_st16(tmem + kb * G::kKCols + (c + u) * 16, v);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.kready[g & 1u]);
+        mbar_arrive(&sh.empty[st]);
       }
     }
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&sh.kready[g & 1u]);
-      mbar_arrive(&sh.empty[st]);
-    }
+    seg_done(sh, ns);
   }
   return true;
 }
@@ -1020,26 +1032,41 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
   const uint32_t qb = ns & 1u;
   const int ch = lane * E;
   const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + s.i * p.q.sb +
-                      static_cast<int64_t>(s.h * p.group) * p.q.sh + ch;
+                      static_cast<int64_t>(s.h * p.group) * p.q.sh;
   const float gk = p.c.k_scale ? __ldg(p.c.k_scale + s.h) : 1.0f;
   const float unit = p.scale * 1.4426950408889634f * gk;
   struct alignas(E * 2) Raw {
     uint32_t w[E / 2];
   };
-  auto fetch = [&](int r) {
-    Raw x{};
-    if (r < s.rows) {
-      const uint32_t at = sh.row[ns % kSegs][r];
-      x = *reinterpret_cast<const Raw*>(q + (at >> 16) * p.q.st + (at & 0xffffu) * p.q.sh);
-    }
-    return x;
-  };
-  Raw next[2] = {fetch(warp), fetch(warp + 4)};  // two rows in flight
+  // A warp's rows (every fourth, up to the last eight with rows in them) come into
+  // the tile as they are, all in flight, and are converted where they lie.
+  const int rows = (s.rows + 7) & ~7;
+  const uint32_t tile = q_smem + qb * G::kQBytes;
 #pragma unroll 1
-  for (int r = warp; r < NP; r += 4) {
-    const Raw raw = next[0];
-    next[0] = next[1];
-    next[1] = fetch(r + 8);
+  for (int e = lane; e < (rows >> 2) * (D / 8); e += 32) {
+    const int r = 4 * (e / (D / 8)) + warp, c = e % (D / 8);
+    const uint32_t at = sh.row[ns % kSegs][r];
+    const uint16_t* src = q + (at >> 16) * p.q.st + (at & 0xffffu) * p.q.sh + 8 * c;
+    const uint32_t dst = tile + (c >> 3) * (NP * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(r < s.rows ? src : q),
+                 "r"(r < s.rows ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+#pragma unroll 1
+  for (int r = warp; r < rows; r += 4) {
+    const uint32_t a = tile + (ch >> 6) * (NP * 128) + r * 128 + (((ch & 63) * 2) ^ ((r & 7) << 4));
+    Raw raw;
+    if constexpr (E == 2) {
+      asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw.w[0]) : "r"(a) : "memory");
+    } else if constexpr (E == 4) {
+      const uint2 v = lds64(a);
+      raw.w[0] = v.x, raw.w[1] = v.y;
+    } else {
+      const uint4 v = lds128(a);
+      raw.w[0] = v.x, raw.w[1] = v.y, raw.w[2] = v.z, raw.w[3] = v.w;
+    }
     float x[E];
     uint32_t top = 0;
 #pragma unroll
@@ -1063,7 +1090,6 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
       const __half2 h = __floats2half2_rn(bad ? 0.0f : x[2 * e] * f1 * f2, bad ? 0.0f : x[2 * e + 1] * f1 * f2);
       w.w[e] = *reinterpret_cast<const uint32_t*>(&h);
     }
-    const uint32_t a = q_smem + qb * G::kQBytes + (ch >> 6) * (NP * 128) + r * 128 + (((ch & 63) * 2) ^ ((r & 7) << 4));
     if constexpr (E == 2) asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(w.w[0]) : "memory");
     else if constexpr (E == 4)
       asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(w.w[0]), "r"(w.w[1]) : "memory");
@@ -1129,18 +1155,20 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
 #pragma unroll
         for (int u = 0; u < G::kSets; ++u) sh.weight[warp][u][r] *= inv;
       }
+      const uint32_t at = row[r];
+      const int hq = s.h * p.group + static_cast<int>(at & 0xffffu), j = static_cast<int>(at >> 16);
+      sh.to[warp][r] = cut ? (static_cast<long long>(slot) * NP + r) * D
+                           : s.i * p.out.sb + j * p.out.st + hq * p.out.sh;
       if (warp == 0) {
         if (cut) {
           p.part_l[slot * NP + r] = make_float2(mr, sum);
         } else if (p.lse) {
-          const uint32_t at = row[r];
-          p.lse[(static_cast<int64_t>(s.i) * p.T + (at >> 16)) * p.heads_q + s.h * p.group + (at & 0xffffu)] =
+          p.lse[(static_cast<int64_t>(s.i) * p.T + j) * p.heads_q + hq] =
               sum == 0.0f ? -INFINITY : (mr + lg2(sum)) * 0.6931471805599453f;
         }
       }
     }
     __syncwarp();
-    const int64_t out = s.i * p.out.sb + static_cast<int64_t>(s.h * p.group) * p.out.sh;
 #pragma unroll 1
     for (int mt = 0; mt < G::kMT; ++mt) {
       const int ch = mt * 128 + warp * 32 + lane;
@@ -1173,20 +1201,17 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
           for (int x = 0; x < 8; ++x)
             if ((nan >> (c + x)) & 1ull) v[x] = NAN;
         }
-        // (a loop over rows reads them back one by one: shorter than eight copies)
 #pragma unroll
-        for (int x = 0; x < 8; ++x) sh.turn[warp][x][lane] = v[x];
-#pragma unroll 1
-        for (int r = c; r < min(c + 8, s.rows); ++r) {
-          const float o = sh.turn[warp][r - c][lane];
-          if (cut) {
-            p.part_o[(static_cast<int64_t>(slot) * NP + r) * D + ch] = o;
-          } else {
-            const uint32_t at = row[r];
-            const int64_t to = out + (at >> 16) * p.out.st + (at & 0xffffu) * p.out.sh + ch;
-            const float f = o * gv;
-            static_cast<uint16_t*>(p.out.data)[to] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f))
-                                                            : __half_as_ushort(__float2half_rn(f));
+        for (int x = 0; x < 8; ++x) {
+          if (c + x < s.rows) {
+            const long long to = sh.to[warp][c + x] + ch;
+            if (cut) {
+              p.part_o[to] = v[x];
+            } else {
+              const float f = v[x] * gv;
+              static_cast<uint16_t*>(p.out.data)[to] = p.bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(f))
+                                                              : __half_as_ushort(__float2half_rn(f));
+            }
           }
         }
       }
