@@ -74,14 +74,16 @@ struct AttendCut {
 constexpr int kSegs = 8;  // ring of planned segments
 constexpr int kSharedBytes = 18432;
 
+// NP: rows a row tile may have, a multiple of 8.
 template <int D, int NP>
 struct AttendGeo {
+  static constexpr int kN = (NP + 15) / 16 * 16;  // N of the products: columns of S, O, P
   static constexpr int kMT = (D + 127) / 128;   // tiles of 128 channels of O^T
   // Softmax: two sets of one warpgroup that take the tiles in turn, each with its
   // own references and its own O (a tile's path through wait, scores, vote is longer
   // than the other roles'), where tensor memory holds both; else one set of two
   // warpgroups by columns.
-  static constexpr int kSets = NP <= 32 && kMT * NP <= 32 ? 2 : 1;
+  static constexpr int kSets = NP <= 32 && kMT * kN <= 32 ? 2 : 1;
   static constexpr int kSoftGroups = NP > 32 ? 2 : 1;
   static constexpr int kCW = NP / kSoftGroups;  // query rows per softmax thread
   static constexpr int kSoftWarps = 4 * kSoftGroups * kSets;
@@ -90,11 +92,11 @@ struct AttendGeo {
   static constexpr int kOB = D > 128 ? 1 : 2;
   static constexpr int kKCols = D / 2;          // 32-bit columns of one K buffer
   static constexpr int kVCols = 64 * kMT;
-  static constexpr int kOCols = kSets * kMT * NP;
+  static constexpr int kOCols = kSets * kMT * kN;
   static constexpr int kTmemK = 0;
   static constexpr int kTmemV = kTmemK + kKB * kKCols;
   static constexpr int kTmemS = kTmemV + 2 * kVCols;
-  static constexpr int kTmemO = kTmemS + 2 * NP;
+  static constexpr int kTmemO = kTmemS + 2 * kN;
   static constexpr int kTmemUsed = kTmemO + kOB * kOCols;
   static constexpr int kTmemCols = kTmemUsed <= 256 ? 256 : 512;
   static_assert(kTmemUsed <= 512, "tensor memory");
@@ -107,16 +109,16 @@ struct AttendGeo {
   static constexpr int kSegReaders = 1 + 1 + 4 + 4 + kSoftWarps + 4;  // warps that read a segment
   static constexpr int kGroups = D / kGroup;
   static constexpr uint32_t kStageBytes = kTileRuns * run_bytes(D);
-  static constexpr uint32_t kQBytes = NP * D * 2;
-  static constexpr uint32_t kPBytes = NP * kTile * 2;
+  static constexpr uint32_t kQBytes = kN * D * 2;
+  static constexpr uint32_t kPBytes = kN * kTile * 2;
   static constexpr uint32_t kFixed = 2 * kQBytes + 2 * kPBytes + 4 * 512 * kMT + kSharedBytes;
   static constexpr int kStages = static_cast<int>((227 * 1024 - 1024 - kFixed) / kStageBytes) < 8
                                      ? static_cast<int>((227 * 1024 - 1024 - kFixed) / kStageBytes)
                                      : 8;
   static_assert(kStages >= 3, "stages");
   static constexpr size_t kSmemBytes = 1024 + kFixed + kStages * kStageBytes;
-  // fp32 accumulator, fp16 operands, M = 128, N = NP; B of O is N-major
-  static constexpr uint32_t kIdescS = (1u << 4) | (static_cast<uint32_t>(NP >> 3) << 17) | (8u << 24);
+  // fp32 accumulator, fp16 operands, M = 128, N = kN; B of O is N-major
+  static constexpr uint32_t kIdescS = (1u << 4) | (static_cast<uint32_t>(kN >> 3) << 17) | (8u << 24);
   static constexpr uint32_t kIdescO = kIdescS | (1u << 16);
 };
 
@@ -189,15 +191,33 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
 }
+// (without the compiler's memory barrier: a fence follows before anyone reads)
+__device__ __forceinline__ void sts128_free(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+}
 __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
-__device__ __forceinline__ void tmem_ld8(uint32_t t, float* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
-                 "=f"(r[7])
-               : "r"(t));
+// 8 or 16 columns of this thread's lane, and the wait for them: one statement, so
+// that nothing uses the registers in between.
+template <int N>
+__device__ __forceinline__ void tmem_get(uint32_t t, float* r) {
+  if constexpr (N == 8) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7])
+        : "r"(t));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+          "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+        : "r"(t));
+  }
 }
 __device__ __forceinline__ void tmem_st8(uint32_t t, const float* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t),
@@ -294,14 +314,15 @@ __device__ __forceinline__ void add_2(float& a, float& b, float x, float y) {
 // the columns.
 template <int N>
 __device__ __forceinline__ float warp_column_sums(const float (&v)[N]) {
-  constexpr int W = N > 16 ? 32 : 16;
+  constexpr int W = N > 16 ? 32 : (N > 8 ? 16 : 8);
   const int lane = threadIdx.x & 31;
   float x[W];
 #pragma unroll
   for (int c = 0; c < W; ++c) x[c] = c < N ? v[c] : 0.0f;
-  if constexpr (W == 16) {
 #pragma unroll
-    for (int c = 0; c < W; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], 16);
+  for (int o = 16; o >= W; o >>= 1) {
+#pragma unroll
+    for (int c = 0; c < W; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], o);
   }
 #pragma unroll
   for (int o = W / 2; o; o >>= 1) {
@@ -363,7 +384,7 @@ __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t
   return n >= 0 && n + L <= p.c.capacity;
 }
 
-__device__ __noinline__ void attend_rows(const AttendParams& p, int64_t n, int L, int rt, AttendSeg& s) {
+static __device__ __noinline__ void attend_rows(const AttendParams& p, int64_t n, int L, int rt, AttendSeg& s) {
   s.row0 = rt * p.rp;
   s.rows = min(p.rp, L * p.group - s.row0);
   const int j0 = s.row0 / p.group, j1 = (s.row0 + s.rows - 1) / p.group;
@@ -381,7 +402,7 @@ __device__ __noinline__ void attend_rows(const AttendParams& p, int64_t n, int L
 }
 
 // Units of one head of request i; -1 where the request is skipped.
-__device__ __noinline__ long long attend_units(const AttendParams& p, int i) {
+static __device__ __noinline__ long long attend_units(const AttendParams& p, int i) {
   int64_t n;
   int L;
   if (!attend_len(p, i, n, L)) return -1;
@@ -396,7 +417,7 @@ __device__ __noinline__ long long attend_units(const AttendParams& p, int i) {
   return u;
 }
 
-__device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
+static __device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
 // CTA c of n takes the units [total c / n, total (c + 1) / n); the CTA of a unit.
 __device__ __forceinline__ long long share_start(long long total, int c, int n) { return div64(total * c, n); }
 __device__ __forceinline__ int share_of(long long total, long long unit, int n) {
@@ -634,12 +655,12 @@ __device__ __forceinline__ bool attend_keys(const AttendParams& p, AttendShared<
 }
 
 // 0xff in the bytes that are NaN as e4m3.
-__device__ __noinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+static __device__ __noinline__ uint32_t nan_bytes(uint32_t w) { return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 
 // Rows of a segment that see a NaN value of scale group `group` in the tiles of
 // this CTA, one warp: the rare second look at scales that the decoder took out.
 template <int D>
-__device__ __noinline__ unsigned long long attend_nan_rows(const AttendParams& p, const AttendSeg& s, int group) {
+static __device__ __noinline__ unsigned long long attend_nan_rows(const AttendParams& p, const AttendSeg& s, int group) {
   const int lane = threadIdx.x & 31;
   unsigned long long m = 0;
   const int64_t base = s.run0 << 4;
@@ -786,8 +807,8 @@ __device__ __forceinline__ bool attend_mma(const AttendParams& p, AttendShared<D
       const uint64_t q = q_desc + (ns & 1u) * (G::kQBytes >> 4);
 #pragma unroll
       for (int kk = 0; kk < D / 64; ++kk)
-        umma_ts64(tm + G::kTmemS + b * NP, tm + G::kTmemK + (G::kKB == 2 ? b * G::kKCols : 0) + 32 * kk,
-                  q + kk * (NP * 128 >> 4), 2, G::kIdescS, kk > 0 ? 1u : 0u, el);
+        umma_ts64(tm + G::kTmemS + b * G::kN, tm + G::kTmemK + (G::kKB == 2 ? b * G::kKCols : 0) + 32 * kk,
+                  q + kk * (G::kN * 128 >> 4), 2, G::kIdescS, kk > 0 ? 1u : 0u, el);
       umma_commit_if(&sh.sdone[b], el);
     }
     if (pend) {
@@ -801,12 +822,12 @@ __device__ __forceinline__ bool attend_mma(const AttendParams& p, AttendShared<D
       tc_fence_after();
       // a step is 16 tokens: 512 bytes of P
       const uint64_t pd = p_desc + pb * (G::kPBytes >> 4);
-      const uint32_t d = tm + G::kTmemO + ob * G::kOCols + (G::kSets == 2 ? pb * (G::kMT * NP) : 0);
+      const uint32_t d = tm + G::kTmemO + ob * G::kOCols + (G::kSets == 2 ? pb * (G::kMT * G::kN) : 0);
       const uint32_t a = tm + G::kTmemV + pb * G::kVCols;
 #pragma unroll
       for (int mt = 0; mt < G::kMT; ++mt) {
-        umma_ts64(d + mt * NP, a + mt * 64, pd, 32, G::kIdescO, (pend & 8) ? 0u : 1u, el);
-        umma_ts64(d + mt * NP, a + mt * 64 + 32, pd + 128, 32, G::kIdescO, 1u, el);
+        umma_ts64(d + mt * G::kN, a + mt * 64, pd, 32, G::kIdescO, (pend & 8) ? 0u : 1u, el);
+        umma_ts64(d + mt * G::kN, a + mt * 64 + 32, pd + 128, 32, G::kIdescO, 1u, el);
       }
       umma_commit_if(&sh.odone[pb], el);
       if (pend & 4) umma_commit_if(&sh.oready[ob], el);
@@ -830,7 +851,7 @@ __device__ __forceinline__ bool attend_mma(const AttendParams& p, AttendShared<D
 
 // Which of a thread's N rows see the token `at` (counted from the segment's first run).
 template <int N>
-__device__ __noinline__ uint32_t attend_see(const int2* lim, int at, uint32_t have) {
+static __device__ __noinline__ uint32_t attend_see(const int2* lim, int at, uint32_t have) {
   uint32_t m = 0;
 #pragma unroll 1
   for (int c = 0; c < N; ++c) {
@@ -840,15 +861,15 @@ __device__ __noinline__ uint32_t attend_see(const int2* lim, int at, uint32_t ha
   return have ? m : 0u;
 }
 
-// Eight scores of a token to P: x - reference, with x = S cs rounded (the maximum
-// is taken of the same rounded x, so P stays in range at any size of the scores),
-// its power of two, and that in fp16.
-__device__ __forceinline__ void attend_p8(uint32_t s_tmem, const float* cs, const float* nmr, float one, bool whole,
-                                          uint32_t see, float (&e)[8], uint32_t (&w)[4]) {
-  tmem_ld8(s_tmem, e);
-  tmem_ld_wait();
+// W (8 or 16) scores of a token to P: x - reference, with x = S cs rounded (the
+// maximum is taken of the same rounded x, so P stays in range at any size of the
+// scores), its power of two, and that in fp16.
+template <int W>
+__device__ __forceinline__ void attend_p(uint32_t s_tmem, const float* cs, const float* nmr, float one, bool whole,
+                                         uint32_t see, float (&e)[W], uint32_t (&w)[W / 2]) {
+  tmem_get<W>(s_tmem, e);
 #pragma unroll
-  for (int c = 0; c < 8; c += 4) {
+  for (int c = 0; c < W; c += 4) {
     const float4 f = *reinterpret_cast<const float4*>(cs + c);
     const float4 m = *reinterpret_cast<const float4*>(nmr + c);
     mul_add_2(e[c], e[c + 1], f.x, f.y, m.x, m.y, one);
@@ -856,15 +877,41 @@ __device__ __forceinline__ void attend_p8(uint32_t s_tmem, const float* cs, cons
   }
   if (!whole) {
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
+    for (int c = 0; c < W; ++c)
       if (!((see >> c) & 1u)) e[c] = -INFINITY;
   }
 #pragma unroll
-  for (int c = 0; c < 4; ++c) {
+  for (int c = 0; c < W / 2; ++c) {
     e[2 * c] = ex2(e[2 * c]);
     e[2 * c + 1] = ex2(e[2 * c + 1]);
     const __half2 h = __floats2half2_rn(e[2 * c], e[2 * c + 1]);
     w[c] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// The same for columns [C, C + W) of a softmax thread: P to shared memory, its
+// largest value, and the sums.
+template <int C, int W, int CW>
+__device__ __forceinline__ void attend_columns(uint32_t s_tmem, const float* cs, const float* nmr, float one,
+                                               bool whole, uint32_t see, uint32_t p_tile, int c0, uint32_t pflip,
+                                               bool again, uint32_t redo, float (&l)[CW], uint32_t& top) {
+  float e[W];
+  uint32_t w[W / 2];
+  attend_p<W>(s_tmem + C, cs + C, nmr + C, one, whole, see >> C, e, w);
+#pragma unroll
+  for (int x = 0; x < W / 2; x += 4) {
+    const int col = c0 + C + 2 * x;
+    top = h2_max(top, h2_max(h2_max(w[x], w[x + 1]), h2_max(w[x + 2], w[x + 3])));
+    sts128_free(p_tile + (col >> 4) * (kTile * 32) + (((col & 8) * 2) ^ pflip),
+                make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]));
+  }
+  if (!again) {
+#pragma unroll
+    for (int x = 0; x < W; x += 2) add_2(l[C + x], l[C + x + 1], e[x], e[x + 1]);
+  } else {
+#pragma unroll
+    for (int x = 0; x < W; ++x)
+      if ((redo >> (C + x)) & 1u) l[C + x] += e[x];
   }
 }
 
@@ -888,7 +935,6 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
     const int rows = sp->rows, t1 = sp->t1, full_lo = sp->full_lo, full_hi = sp->full_hi;
     const uint32_t qb = ns & 1u, ob = ns % G::kOB;
     const int slot = static_cast<int>(ns % kSegs);
-    const int cols = min(CW, ((rows - c0 + 7) & ~7));  // columns with rows in them, by eights (or <= 0)
     bool unset = true;  // some row has seen nothing yet (uniform over the warpgroup)
     ok = ok && warp_wait(&sh.qready[qb], (ns >> 1) & 1u);
     float l[CW];
@@ -899,7 +945,7 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
     for (int t = sp->t0; t < t1; ++t, ++g) {
       const uint32_t b = g & 1u;
       if (G::kSets == 2 && b != set) continue;
-      const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + b * NP + c0;
+      const uint32_t s_tmem = sh.tmem + lanes + G::kTmemS + b * G::kN + c0;
       // S of tile g was issued behind O of tile g - 2, so P's buffer is free too
       ok = ok && warp_wait(&sh.sdone[b], (g >> 1) & 1u);
       tc_fence_after();
@@ -914,24 +960,17 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
       for (;; again = true) {
         uint32_t top = 0;
         if (!unset || again) {
-#pragma unroll
-          for (int c = 0; c < CW; c += 8) {
-            if (c < cols) {
-              float e[8];
-              uint32_t w[4];
-              attend_p8(s_tmem + c, &sh.cs[qb][c0 + c], &nmr[c0 + c], p.one, whole, see >> c, e, w);
-              top = h2_max(top, h2_max(h2_max(w[0], w[1]), h2_max(w[2], w[3])));
-              sts128(prow + b * G::kPBytes + ((c0 + c) >> 4) * (kTile * 32) + ((((c0 + c) & 8) * 2) ^ pflip),
-                     make_uint4(w[0], w[1], w[2], w[3]));
-              if (!again) {
-#pragma unroll
-                for (int x = 0; x < 8; x += 2) add_2(l[c + x], l[c + x + 1], e[x], e[x + 1]);
-              } else {
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                  if ((redo >> (c + x)) & 1u) l[c + x] += e[x];
-              }
-            }
+          const uint32_t pt = prow + b * G::kPBytes;
+          const float* cs = &sh.cs[qb][c0];
+          const float* nm = &nmr[c0];
+          if constexpr (CW == 8) {
+            attend_columns<0, 8>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
+          } else {
+            attend_columns<0, 16>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
+            if constexpr (CW == 24)
+              attend_columns<16, 8>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
+            if constexpr (CW == 32)
+              attend_columns<16, 16>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
           }
           fence_async_shared();
         }
@@ -942,10 +981,9 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
         const bool unset_before = unset;
         // new references: the maximum over the tile's tokens of every row
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 8) {
+        for (int c = 0; c < CW; c += 8) {
           float x[8], keep = 0.0f;
-          tmem_ld8(s_tmem + c, x);
-          tmem_ld_wait();
+          tmem_get<8>(s_tmem + c, x);
 #pragma unroll
           for (int u = 0; u < 8; ++u) {
             const float m = warp_max(((see >> (c + u)) & 1u) ? __fmul_rn(x[u], sh.cs[qb][c0 + c + u]) : -INFINITY);
@@ -955,7 +993,7 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
         }
         group_sync(id);
         bool none = false;
-        if (tok < cols) {
+        if (tok < CW) {
           const int c = c0 + tok;
           const float was = fresh ? -INFINITY : sh.mref[set][c];
           const float m = fmaxf(fmaxf(fmaxf(sh.red[set][0][c], sh.red[set][1][c]), fmaxf(sh.red[set][2][c], sh.red[set][3][c])), was);
@@ -975,12 +1013,11 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
           if (ok) {
 #pragma unroll 1
             for (int mt = 0; mt < G::kMT; ++mt) {
-              const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + (set * G::kMT + mt) * NP + c0;
+              const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + (set * G::kMT + mt) * G::kN + c0;
 #pragma unroll 1
-              for (int c = 0; c < cols; c += 8) {
+              for (int c = 0; c < CW; c += 8) {
                 float v[8];
-                tmem_ld8(o + c, v);
-                tmem_ld_wait();
+                tmem_get<8>(o + c, v);
 #pragma unroll
                 for (int x = 0; x < 8; ++x) v[x] *= sh.fac[set][c0 + c + x];
                 tmem_st8(o + c, v);
@@ -1038,16 +1075,15 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
   struct alignas(E * 2) Raw {
     uint32_t w[E / 2];
   };
-  // A warp's rows (every fourth, up to the last eight with rows in them) come into
-  // the tile as they are, all in flight, and are converted where they lie.
-  const int rows = (s.rows + 7) & ~7;
+  // A warp's rows (every fourth; zeros behind the last) come into the tile as they
+  // are, all in flight, and are converted where they lie.
   const uint32_t tile = q_smem + qb * G::kQBytes;
 #pragma unroll 1
-  for (int e = lane; e < (rows >> 2) * (D / 8); e += 32) {
+  for (int e = lane; e < NP / 4 * (D / 8); e += 32) {
     const int r = 4 * (e / (D / 8)) + warp, c = e % (D / 8);
     const uint32_t at = sh.row[ns % kSegs][r];
     const uint16_t* src = q + (at >> 16) * p.q.st + (at & 0xffffu) * p.q.sh + 8 * c;
-    const uint32_t dst = tile + (c >> 3) * (NP * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    const uint32_t dst = tile + (c >> 3) * (G::kN * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(r < s.rows ? src : q),
                  "r"(r < s.rows ? 16 : 0)
                  : "memory");
@@ -1055,8 +1091,8 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
 #pragma unroll 1
-  for (int r = warp; r < rows; r += 4) {
-    const uint32_t a = tile + (ch >> 6) * (NP * 128) + r * 128 + (((ch & 63) * 2) ^ ((r & 7) << 4));
+  for (int r = warp; r < NP; r += 4) {
+    const uint32_t a = tile + (ch >> 6) * (G::kN * 128) + r * 128 + (((ch & 63) * 2) ^ ((r & 7) << 4));
     Raw raw;
     if constexpr (E == 2) {
       asm volatile("ld.shared.u32 %0, [%1];" : "=r"(raw.w[0]) : "r"(a) : "memory");
@@ -1182,10 +1218,9 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
 #pragma unroll 1
       for (int c = 0; c < s.rows; c += 8) {
         float v[8], u[8];
-        const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + mt * NP + c;
-        tmem_ld8(o, v);
-        if (G::kSets == 2) tmem_ld8(o + G::kMT * NP, u);
-        tmem_ld_wait();
+        const uint32_t o = sh.tmem + lanes + G::kTmemO + ob * G::kOCols + mt * G::kN + c;
+        tmem_get<8>(o, v);
+        if (G::kSets == 2) tmem_get<8>(o + G::kMT * G::kN, u);
 #pragma unroll
         for (int x = 0; x < 8; ++x) {  // a set without weight may hold anything
           const float f = sh.weight[warp][0][min(c + x, NP - 1)];
@@ -1362,21 +1397,24 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   }
 }
 
-constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 4;      // rows of a CTA
-constexpr int kJoinMaxParts = 1024;
+// Joins: a block small enough to be resident beside the attention's, whose end it
+// waits for, and two rows a block.
+__host__ __device__ constexpr int join_threads(int D) { return D > 128 ? D : 128; }
+constexpr int kJoinRows = 2;
+constexpr int kJoinMaxParts = 256;
 
 // Join the parts of the segments that were cut: block (x, y) takes the rows
-// [4 y, 4 y + 4) of the segment that CTA x + 1's share starts inside of, where
-// that is the segment's first cut.  Parts are added in the order of the CTAs
-// (in D == 128: two interleaved halves, then their sum), so the result does not
-// depend on timing.
+// [2 y, 2 y + 2) of the segment that CTA x + 1's share starts inside of, where
+// that is the segment's first cut.  Parts are added in the order of the CTAs (at
+// D = 64 in two interleaved halves, then their sum), so the result does not depend
+// on timing.
 template <int D, int NP>
-__global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_constant__ AttendParams p) {
-  constexpr int S = kJoinThreads / D;  // threads of a channel
+__global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_constant__ AttendParams p) {
+  constexpr int kThreads = join_threads(D);
+  constexpr int S = kThreads / D;  // threads of a channel
   __shared__ float weight[kJoinRows][kJoinMaxParts];
   __shared__ float inv[kJoinRows];
-  __shared__ float sum[kJoinRows][kJoinThreads];
+  __shared__ float sum[kJoinRows][kThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const AttendCut& cut = p.cuts[blockIdx.x + 1];
   const int last = __ldcg(&cut.last);
@@ -1389,27 +1427,35 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto slot = [&](int e) { return 2 * (first + e) + (e == 0 ? 1 : 0); };
   const int nr = min(kJoinRows, rows - r0);
+  const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f;
   if (warp < nr) {
     const int r = r0 + warp;
+    constexpr int kPer = kJoinMaxParts / 32;
+    float2 v[kPer];
     float m = -INFINITY;
-    for (int e = lane; e < parts; e += 32) {
-      const float2 v = __ldcg(p.part_l + slot(e) * NP + r);
-      if (v.y != 0.0f) m = fmaxf(m, v.x);
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int e = lane + 32 * u;
+      v[u] = e < parts ? __ldcg(p.part_l + slot(e) * NP + r) : make_float2(0.0f, 0.0f);
     }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u)
+      if (v[u].y != 0.0f) m = fmaxf(m, v[u].x);
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     float l = 0.0f;
-    for (int e = lane; e < parts; e += 32) {
-      const float2 v = __ldcg(p.part_l + slot(e) * NP + r);
-      const float w = v.y == 0.0f ? 0.0f : ex2(v.x - m);
-      weight[warp][e] = w;
-      l += w * v.y;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int e = lane + 32 * u;
+      const float w = v[u].y == 0.0f ? 0.0f : ex2(v[u].x - m);
+      if (e < parts) weight[warp][e] = w;
+      l += w * v[u].y;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
       inv[warp] = l == 0.0f ? 0.0f : __frcp_rn(l);
-      if (p.lse && blockIdx.y * kJoinRows + warp < rows) {
+      if (p.lse) {
         const int row = row0 + r, j = row / p.group, hq = h * p.group + row % p.group;
         p.lse[(static_cast<int64_t>(i) * p.T + j) * p.heads_q + hq] =
             l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
@@ -1419,7 +1465,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
   __syncthreads();
   const int ch = threadIdx.x % D, part = threadIdx.x / D;
   float acc[kJoinRows] = {};
-#pragma unroll 4
+#pragma unroll 8
   for (int e = part; e < parts; e += S) {
     const float* src = p.part_o + (static_cast<int64_t>(slot(e)) * NP + r0) * D + ch;
 #pragma unroll
@@ -1429,8 +1475,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attend_join(const __grid_const
 #pragma unroll
   for (int r = 0; r < kJoinRows; ++r) sum[r][threadIdx.x] = acc[r];
   __syncthreads();
-  const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f;
-  for (int e = threadIdx.x; e < nr * D; e += kJoinThreads) {
+  for (int e = threadIdx.x; e < nr * D; e += kThreads) {
     const int r = e / D, cc = e % D;
     float o = 0.0f;
 #pragma unroll

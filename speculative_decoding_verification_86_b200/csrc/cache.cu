@@ -7,7 +7,7 @@
 #include <cstdint>
 #include <new>
 
-#include "attend.cuh"
+#include "attend_launch.cuh"
 #include "cache.cuh"
 #include "host.cuh"
 
@@ -124,46 +124,10 @@ spec_status move(spec_cache_ctx* c, const spec_cache_pages* cache, const spec_ca
 // share 512 columns of tensor memory with the decoded tiles.
 int max_rows(int head_dim) { return head_dim == 256 ? 32 : 64; }
 
-template <int D, int NP>
-spec_status launch_attend(const spec_cache_ctx* c, const sv::AttendParams& p, cudaStream_t stream) {
-  using G = sv::AttendGeo<D, NP>;
-  sv::k_attend<D, NP><<<c->num_sms, G::kThreads, G::kSmemBytes, stream>>>(p);
-  // the join starts while the attention drains, and waits for its end by itself
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(c->num_sms - 1, (p.rp + sv::kJoinRows - 1) / sv::kJoinRows);
-  cfg.blockDim = dim3(sv::kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (c->num_sms > 1 && cudaLaunchKernelEx(&cfg, sv::k_attend_join<D, NP>, p) != cudaSuccess) return SPEC_ERR_CUDA;
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
-}
-
-template <int D>
-spec_status launch_attend(const spec_cache_ctx* c, const sv::AttendParams& p, cudaStream_t stream) {
-  if (p.rp <= 16) return launch_attend<D, 16>(c, p, stream);
-  if (p.rp <= 32) return launch_attend<D, 32>(c, p, stream);
-  if constexpr (D < 256) {
-    if (p.rp <= 48) return launch_attend<D, 48>(c, p, stream);
-    return launch_attend<D, 64>(c, p, stream);
-  }
-  return SPEC_ERR_INVALID_ARG;
-}
-
-template <int D, int NP>
-bool attend_smem() {
-  return cudaFuncSetAttribute(sv::k_attend<D, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(sv::AttendGeo<D, NP>::kSmemBytes)) == cudaSuccess;
-}
-
-bool attend_prepare(int head_dim) {
-  if (head_dim == 64) return attend_smem<64, 16>() && attend_smem<64, 32>() && attend_smem<64, 48>() && attend_smem<64, 64>();
-  if (head_dim == 128)
-    return attend_smem<128, 16>() && attend_smem<128, 32>() && attend_smem<128, 48>() && attend_smem<128, 64>();
-  return attend_smem<256, 16>() && attend_smem<256, 32>();
+bool prepare_attend(int head_dim) {
+  return head_dim == 64    ? sv::attend_prepare<64>()
+         : head_dim == 128 ? sv::attend_prepare<128>()
+                           : sv::attend_prepare<256>();
 }
 
 }  // namespace
@@ -221,7 +185,7 @@ spec_status spec_cache_init(spec_cache_ctx** out, int device, int max_batch, int
   c->part_l = reinterpret_cast<float2*>(b + o_l);
   c->cuts = reinterpret_cast<sv::AttendCut*>(b + o_cuts);
   c->error = reinterpret_cast<unsigned*>(b + o_err);
-  if (cudaMemset(c->error, 0, 256) != cudaSuccess || !attend_prepare(head_dim)) {
+  if (cudaMemset(c->error, 0, 256) != cudaSuccess || !prepare_attend(head_dim)) {
     cudaFree(c->ws);
     delete c;
     return SPEC_ERR_CUDA;
@@ -297,9 +261,10 @@ spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
   DeviceGuard g(c->device);
   if (!g.ok) return SPEC_ERR_CUDA;
   cudaGetLastError();
-  if (c->head_dim == 64) return launch_attend<64>(c, p, stream);
-  if (c->head_dim == 128) return launch_attend<128>(c, p, stream);
-  return launch_attend<256>(c, p, stream);
+  const bool done = c->head_dim == 64    ? sv::attend_launch<64>(p, c->num_sms, stream)
+                    : c->head_dim == 128 ? sv::attend_launch<128>(p, c->num_sms, stream)
+                                         : sv::attend_launch<256>(p, c->num_sms, stream);
+  return done && cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status spec_cache_errors(spec_cache_ctx* c, uint32_t* out) {
