@@ -50,6 +50,7 @@ struct AttendParams {
   const int32_t* block_len;  // nullptr: T
   int B, T, heads_q, group;  // group: query heads per key/value head
   int rp;                    // query rows of a row tile
+  int seg_units;             // what a segment costs beside its tiles, in tiles
   int bf16;                  // q and out are bf16 (else fp16)
   float scale;
   float one;  // 1.0f (mul_add_2)
@@ -375,9 +376,10 @@ __device__ __forceinline__ void group_sync(int id) {
 
 // ------------------------------------------------------------- work shares --
 // A request's units, in order: head, row tile, token tile.  A segment (one row
-// tile of one head) counts kSegUnits more than its tiles: that is what its first
-// references, its Q and its output cost beside them.
-constexpr int kSegUnits = 6;
+// tile of one head) counts p.seg_units more than its tiles: what its first
+// references, its Q and its output cost beside them.  Equal shares of bare tiles
+// left the CTAs with many short segments 29% behind the mean (256 requests of
+// 64..4096 positions).
 __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t& n, int& L) {
   n = __ldg(p.cache_len + i);
   L = p.block_len ? min(max(__ldg(p.block_len + i), 0), p.T) : p.T;
@@ -412,7 +414,7 @@ static __device__ __noinline__ long long attend_units(const AttendParams& p, int
 #pragma unroll 1
   for (int rt = 0; rt < nrt; ++rt) {
     attend_rows(p, n, L, rt, s);
-    u += s.tiles + kSegUnits;
+    u += s.tiles + p.seg_units;
   }
   return u;
 }
@@ -464,7 +466,7 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
       open = true;
     }
     attend_rows(p, n, L, rt, s);
-    const int all = s.tiles + kSegUnits;
+    const int all = s.tiles + p.seg_units;
     if (off >= all) {  // only where the share starts behind a row tile
       off -= all;
       ++rt;
@@ -472,8 +474,8 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
     }
     s.i = i;
     s.h = h;
-    s.t0 = static_cast<int>(max(off - kSegUnits, 0ll));
-    s.t1 = static_cast<int>(max(min(static_cast<long long>(all), off + left) - kSegUnits, 0ll));
+    s.t0 = static_cast<int>(max(off - p.seg_units, 0ll));
+    s.t1 = static_cast<int>(max(min(static_cast<long long>(all), off + left) - p.seg_units, 0ll));
     if (ns == 0 && s.t0 > 0) {
       const long long first = u0 - s.t0;  // the segment's first tile
       if (share_of(total, first, n_ctas) == static_cast<int>(blockIdx.x) - 1) {
