@@ -12,13 +12,19 @@ per second (sum of L_i over the batch / step time), plus the HBM bandwidth
 the step sustains.
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--impl ours|reference]
-                  [--workload headline|stochastic|greedy|conf|conf_budget|sweep:B|lmhead]
+                  [--workload headline|stochastic|greedy|conf|conf_budget|sweep:B|lmhead|attend]
 
 ``--workload lmhead`` times verification fused into the shared LM head
 instead: the inputs are the two models' last hidden states (B=256, k=5,
 H=2560, bf16) and the output head W [151936, 2560] bf16; one step is the
 tcgen05 GEMM with the statistics epilogue, the accept chains, the GEMM of the
 sampled rows and the sample.  Its roofline is the tensor-core one.
+
+``--workload attend`` times the part of a step that comes before the head: the
+blocks' keys and values written into the 4-bit block cache and the blocks'
+attention over it (B=256, 6 tokens each, contexts of 64..4096 positions, 32 query
+and 8 key/value heads of 128).  Its roofline is the HBM one, its reference arm the
+same attention in fp64 torch on the host cores.
 
 With N > 1 (launched by torch.distributed.run) every rank verifies its own
 batch of the same shape (weak scaling, no collective on the data path); the
@@ -58,7 +64,7 @@ def parse_args():
                     help="ours: the CUDA library; reference: the fp64 CPU oracle on the host "
                          "cores, on a bounded sample of the same workload")
     ap.add_argument("--workload", default="headline",
-                    help="headline | stochastic | greedy | conf | conf_budget | sweep:B | lmhead")
+                    help="headline | stochastic | greedy | conf | conf_budget | sweep:B | lmhead | attend")
     ap.add_argument("--timed-seconds", type=float, default=1.0,
                     help="repeat the timed block of --steps steps until this much time has "
                          "elapsed (0: one block, e.g. under a profiler)")
@@ -266,7 +272,8 @@ def measured_peaks():
 KERNEL_SOURCES = {
     "k_engine": ["common.cuh", "conf.cuh", "engine.cuh", "fp64.cuh", "philox.cuh", "refine.cuh",
                  "sample.cuh", "stage.cuh", "stats.cuh"],
-    "k_lmhead": ["common.cuh", "philox.cuh", "stage.cuh", "stats.cuh", "lmhead.cuh"],
+    "k_lmhead": ["common.cuh", "philox.cuh", "ptx.cuh", "stage.cuh", "stats.cuh", "lmhead.cuh"],
+    "k_attend": ["ptx.cuh", "cache.cuh", "attend.cuh"],
 }
 
 
@@ -894,9 +901,155 @@ def run_lmhead_reference(args):
     print(json.dumps(line), flush=True)
 
 
+# ----------------------------------------------------- block attention ----
+ATTEND_METRIC = "query positions/s of the 4-bit block cache's write + attention, B=256 T=6 32/8 heads of 128"
+
+
+def attend_config(w, n):
+    return {"model": "attention of a verification step: %s" % w["name"], "global_batch": w["B"] * n,
+            "seq_len": w["T"], "positions_max": int(max(w["lens"])), "parallelism": "dp%d" % n,
+            "inputs": "larger than L2 (the pages)"}
+
+
+def attend_oracle_sample(w):
+    """Request 0's attention in fp64 torch on the host: (seconds, positions)."""
+    import torch
+    n, T, G = w["lens"][0], w["T"], w["heads_q"] // w["heads_kv"]
+    g = torch.Generator().manual_seed(0)
+    k = torch.randn((w["heads_kv"], n + T, w["d"]), generator=g, dtype=torch.float64)
+    v = torch.randn((w["heads_kv"], n + T, w["d"]), generator=g, dtype=torch.float64)
+    q = torch.randn((w["heads_kv"], T, G, w["d"]), generator=g, dtype=torch.float64)
+    t0 = time.perf_counter()
+    s = torch.einsum("htgd,hnd->htgn", q, k) * w["d"] ** -0.5
+    see = torch.arange(n + T) <= n + torch.arange(T)[:, None]
+    s = s.masked_fill(~see[None, :, None, :], -math.inf)
+    torch.einsum("htgn,hnd->htgd", torch.softmax(s, -1), v)
+    return time.perf_counter() - t0, T
+
+
+def run_attend(args):
+    import torch
+    import torch.distributed as dist
+    from speculative_decoding_verification_86_b200 import binding, build, ranks, workloads as W
+
+    world = int(os.environ.get("WORLD_SIZE", "1"))
+    rank = int(os.environ.get("RANK", "0"))
+    local = int(os.environ.get("LOCAL_RANK", "0"))
+    if args.impl == "reference":
+        if rank == 0:
+            w = W.block_cache("cpu", seed=6, data=False)
+            runs = [attend_oracle_sample(w) for _ in range(max(1, args.steps))]
+            value = sum(p for _, p in runs) / sum(t for t, _ in runs)
+            print(json.dumps({
+                "impl": "reference", "metric": ATTEND_METRIC, "value": value, "unit": UNIT, "n_gpus": args.gpus,
+                "steps": args.steps, "warmup": 0, "ms_per_step": 1e3 * sum(t for t, _ in runs) / len(runs),
+                "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "f64",
+                "data": "synthetic", "config": attend_config(w, 1),
+                "e2e": {"value": value, "unit": UNIT, "h2d_bytes_per_step": 0, "d2h_bytes_per_step": 0}}),
+                flush=True)
+        return
+    if world != args.gpus:
+        raise SystemExit("--gpus %d but WORLD_SIZE=%d" % (args.gpus, world))
+    torch.cuda.set_device(local)
+    dev = torch.device("cuda", local)
+    if world > 1:
+        from datetime import timedelta
+        dist.init_process_group("nccl", timeout=timedelta(seconds=120), device_id=dev)
+    build.build()
+    w = W.block_cache(dev, seed=6 + rank)
+    B, T, hq, hkv, d = w["B"], w["T"], w["heads_q"], w["heads_kv"], w["d"]
+    cache = binding.BlockCache(dev, hq, hkv, d, w["page"], max_batch=B)
+    pages = cache.alloc(w["num_pages"])
+    scales = dict(k_scale=w["k_scale"], v_scale=w["v_scale"])
+    zero = torch.zeros(B, dtype=torch.int32, device=dev)
+    for k, v, i in w["context"]():  # contexts, one request at a time
+        cache.write(k, v, pages, w["table"][i:i + 1], zero[:1], **scales)
+    k, v, q = w["k"], w["v"], w["q"]
+    out = torch.zeros_like(q)
+    lse = torch.zeros((B, T, hq), device=dev)
+    where = dict(table=w["table"], cache_len=w["cache_len"], **scales)
+
+    def step():
+        cache.write(k, v, pages, **where)
+        cache.attend(q, pages, out=out, lse=lse, **where)
+
+    stream = torch.cuda.current_stream(dev)
+    for _ in range(max(args.warmup, 3)):
+        step()
+    visible = os.environ.get("CUDA_VISIBLE_DEVICES")
+    clocks = ClockSampler(int(visible.split(",")[local]) if visible else local)
+    clocks.start()
+    time.sleep(0.2)
+    if world > 1:
+        dist.barrier()
+    torch.cuda.synchronize(dev)
+    clocks.mark()
+    block_ms = timed_blocks(step, args.steps, stream, dev, world, args.timed_seconds)
+    clocks.mark()
+    clk = clocks.stop()
+    ms = statistics.median(block_ms) / args.steps
+    positions = B * T
+
+    e2e = None
+    if args.e2e_steps > 0:  # the block's rows from pinned host memory, the output back
+        host = [t.cpu().pin_memory() for t in (k, v, q)]
+        back = torch.empty(out.shape, dtype=out.dtype).pin_memory()
+        a0, a1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+
+        def hstep():
+            for t, h in zip((k, v, q), host):
+                t.copy_(h, non_blocking=True)
+            step()
+            back.copy_(out, non_blocking=True)
+
+        hstep()
+        torch.cuda.synchronize(dev)
+        a0.record(stream)
+        for _ in range(args.e2e_steps):
+            hstep()
+        a1.record(stream)
+        torch.cuda.synchronize(dev)
+        e_ms = ranks.max_over_ranks(a0.elapsed_time(a1), dev) / args.e2e_steps
+        e2e = {"value": positions * world / (e_ms / 1e3), "unit": UNIT, "ms_per_step": e_ms,
+               "h2d_bytes_per_step": int(sum(h.numel() * h.element_size() for h in host)),
+               "d2h_bytes_per_step": int(back.numel() * back.element_size())}
+
+    cpu = None
+    if world == 1 and not args.no_cpu_baseline:
+        dt, pos = attend_oracle_sample(w)
+        cpu = {"value": pos / dt, "unit": UNIT, "cores": torch.get_num_threads(), "kind": "fp64 torch",
+               "sample": "request 0 of %d, %d positions" % (B, w["lens"][0])}
+    peaks = measured_peaks()
+    peak = float(peaks["hbm_gbs"]) if peaks and peaks.get("hbm_gbs") else FALLBACK_HBM_GBS
+    # the packed context and block once, the block's rows in, the output out
+    nbytes = (sum(w["lens"]) + B * T) * hkv * 2 * d * 9 // 16 + B * T * d * 2 * (2 * hkv + 2 * hq)
+    achieved = nbytes / (ms * 1e-3) / 1e9
+    line = {
+        "metric": ATTEND_METRIC, "value": positions * world / (ms / 1e3), "unit": UNIT, "n_gpus": world,
+        "steps": args.steps, "warmup": max(args.warmup, 3), "ms_per_step": ms, "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "config": attend_config(w, world),
+        "roofline": {"bound": "memory", "kernel": "k_attend (with k_cache_write, k_attend_join)",
+                     "achieved": achieved, "peak": peak, "unit": "GB/s", "frac": achieved / peak,
+                     "bytes_per_step": nbytes, "traffic": profiled_traffic("k_attend", "attend")},
+        "timed_blocks": {"blocks": len(block_ms), "steps_per_block": args.steps,
+                         "ms_per_block_min": min(block_ms), "ms_per_block_median": statistics.median(block_ms),
+                         "ms_per_block_max": max(block_ms)},
+        "kernel_errors": cache.errors(), "clocks": clk, "e2e": e2e, "cpu_baseline": cpu,
+        "gpu_launches": 3 * args.steps * len(block_ms),
+    }
+    if rank == 0:
+        print(json.dumps(line), flush=True)
+    cache.close()
+    if world > 1:
+        dist.destroy_process_group()
+
+
 def main():
     args = parse_args()
-    if args.workload == "lmhead":
+    if args.workload == "attend":
+        run_attend(args)
+    elif args.workload == "lmhead":
         if args.impl == "reference":
             run_lmhead_reference(args)
         else:

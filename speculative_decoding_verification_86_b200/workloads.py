@@ -212,6 +212,53 @@ def lmhead(device="cpu", seed=5, B=256, k=5, V=VOCAB_QWEN, H=HIDDEN_QWEN3_4B, gr
                                                                         " (exact grid)" if grid else ""))
 
 
+def block_cache(device="cpu", seed=6, B=256, k=5, heads_q=32, heads_kv=8, head_dim=128, page_size=64,
+                lo=64, hi=4096, data=True):
+    """Inputs of the 4-bit block cache: B requests with contexts of U{lo..hi}
+    positions, each in its own pages (handed out in random order), and a block of
+    k + 1 tokens to write and attend.
+
+    q, k, v ~ N(0, 1) bf16, key channels scaled by exp(0.7 N(0, 1)) (rotary keys
+    have channels of very unlike sizes); calibration scales near the largest
+    magnitude / (6 * 448).  ``context()`` yields (k, v, request) of one context
+    after the other, so that they need not be held at once.  ``data=False`` draws
+    the lengths only."""
+    import random
+    r = random.Random(seed)
+    T = k + 1
+    lens = [r.randint(lo, hi) for _ in range(B)]
+    out = dict(B=B, T=T, heads_q=heads_q, heads_kv=heads_kv, d=head_dim, page=page_size, lens=lens,
+               name="4-bit block cache B=%d T=%d positions %d..%d heads %d/%d x %d pages of %d" % (
+                   B, T, lo, hi, heads_q, heads_kv, head_dim, page_size))
+    if not data:
+        return out
+    g = _gen(device, seed)
+    per = [(n + T + page_size - 1) // page_size for n in lens]
+    ids = torch.randperm(sum(per), generator=g, device=device).to(torch.int32).cpu()
+    table = torch.full((B, max(per)), -1, dtype=torch.int32)
+    at = 0
+    for i, m in enumerate(per):
+        table[i, :m] = ids[at:at + m]
+        at += m
+    size = torch.exp(_normal((heads_kv, head_dim), 0.7, g, device))
+
+    def rows(n, heads, scale=None):
+        x = _normal((n[0], n[1], heads, head_dim), 1.0, g, device)
+        return (x if scale is None else x * scale).to(torch.bfloat16)
+
+    def context():
+        for i, n in enumerate(lens):
+            yield rows((1, n), heads_kv, size), rows((1, n), heads_kv), i
+
+    out.update(num_pages=sum(per), table=table.to(device),
+               cache_len=torch.tensor(lens, dtype=torch.int32, device=device),
+               k_scale=0.004 * (0.5 + torch.rand(heads_kv, generator=g, device=device)),
+               v_scale=0.002 * (0.5 + torch.rand(heads_kv, generator=g, device=device)),
+               q=rows((B, T), heads_q), k=rows((B, T), heads_kv, size), v=rows((B, T), heads_kv),
+               context=context)
+    return out
+
+
 def to_numpy_inputs(w):
     """Host copies in the oracle's formats (bf16 as raw uint16 bits)."""
     import numpy as np

@@ -472,6 +472,96 @@ def test_two_streams_with_a_context_each(dev):
     assert s["cache"].errors() == 0 and other.errors() == 0
 
 
+def test_batches_larger_than_a_block_of_threads(dev):
+    """1500 requests: the shares come from a scan in several rounds; many requests have nothing to do."""
+    B, T = 1500, 2
+    rng = np.random.RandomState(5)
+    lens = [int(x) for x in rng.randint(0, 40, size=B)]
+    block = [int(x) for x in rng.randint(-1, 4, size=B)]  # clamped to 0..2
+    lens[700] = -1
+    per = [max(1, (max(n, 0) + T + 15) // 16) for n in lens]
+    table = np.full((B, 3), -1, dtype=np.int32)
+    ids, at = rng.permutation(sum(per)), 0
+    for i, m in enumerate(per):
+        table[i, :m] = ids[at:at + m]
+        at += m
+    cache = binding.BlockCache(dev, 2, 1, 64, 16, max_batch=B)
+    pages = cache.alloc(sum(per))
+    g = torch.Generator(device=dev).manual_seed(9)
+    k = torch.randn((B, 42, 1, 64), generator=g, device=dev)
+    v = torch.randn((B, 42, 1, 64), generator=g, device=dev)
+    t = on(dev, table)
+    cache.write(k, v, pages, t, torch.zeros(B, dtype=torch.int32, device=dev),
+                block_len=on(dev, [max(n, 0) + min(max(b, 0), T) for n, b in zip(lens, block)]))
+    q = torch.randn((B, T, 2, 64), generator=g, device=dev).half()
+    out = torch.full_like(q, 7.0)
+    lse = torch.full((B, T, 2), 7.0, device=dev)
+    status = torch.zeros(B, dtype=torch.int32, device=dev)
+    cache.attend(q, pages, t, on(dev, lens), block_len=on(dev, block), out=out, lse=lse, status=status)
+    assert status.nonzero().flatten().tolist() == [700] and int(status[700]) == binding.DEV_BAD_LENGTH
+    kk, vv = cache.read(pages, t, rows=42, dtype=torch.float32)
+    ok = torch.zeros((B, T), dtype=torch.bool)
+    for i in range(B):
+        for j in range(min(max(block[i], 0), T) if i != 700 else 0):
+            ok[i, j] = True
+            n = lens[i] + j + 1
+            x = q[i, j].double() @ kk[i, :n, 0].double().T / 8
+            p = torch.softmax(x, -1)
+            want, a = p @ vv[i, :n, 0].double(), p @ vv[i, :n, 0].double().abs()
+            size = (q[i, j].double().abs() @ kk[i, :n, 0].double().abs().T).amax(-1) / 8
+            z = torch.logsumexp(x, -1)
+            tol, tol_lse = ref.attend_bounds(want.cpu().numpy(), z.cpu().numpy(), a.cpu().numpy(), size.cpu().numpy(), 42,
+                                             64, q.dtype)
+            assert np.all(np.abs(ref.to_np(out[i, j]) - want.cpu().numpy()) <= tol)
+            assert np.all(np.abs(ref.to_np(lse[i, j]) - z.cpu().numpy()) <= tol_lse)
+    left = ~ok.to(dev)
+    assert bool((out[left] == 7).all()) and bool((lse[left] == 7).all())
+    assert cache.errors() == 0
+
+
+@pytest.mark.parametrize("d,hq,hkv,T", [(128, 32, 1, 5), (64, 1, 1, 150), (256, 8, 2, 21), (128, 3, 3, 65)])
+def test_blocks_of_several_row_tiles(dev, d, hq, hkv, T):
+    """More query rows than a tile holds: every row tile reads its own span of positions."""
+    s = make(dev, B=2, T=T, heads_q=hq, heads_kv=hkv, d=d, page=32, lens=[45, 210], block=[T, T - 2], seed=T)
+    check_attend(s)
+    check_attend(s, window=50)
+
+
+def test_a_score_that_leaps_far_past_all_before_it(dev):
+    """A key whose score passes the running maximum by thousands of powers of two: the sums so far overflow
+    or vanish, and the row is that key's value."""
+    d, n = 64, 700
+    s = make(dev, B=1, T=1, heads_q=3, heads_kv=1, d=d, page=16, lens=[n], seed=77, scales=False)
+    g = torch.Generator().manual_seed(3)
+    k = torch.randn((1, n, 1, d), generator=g) * 0.01
+    q = torch.randn((1, 1, 3, d), generator=g)
+    k[0, 300, 0] = q[0, 0, 0] * 40.0
+    k[0, 650, 0] = q[0, 0, 0] * 300.0
+    k[0, 450, 0] = q[0, 0, 1] * 8.0
+    v = torch.randn((1, n, 1, d), generator=g)
+    s["raw"] = ref.write(s["raw"], 16, s["table"], [0], k, v)
+    for scale in (0.05, 1.0, 30.0):
+        check_attend(s, q=q.to(torch.bfloat16), scale=scale)
+
+
+def test_outputs_on_the_callers_stream(dev):
+    """Outputs that the call makes are filled on the stream that it runs on."""
+    s = make(dev, B=2, T=3, heads_q=2, heads_kv=1, d=64, page=16, lens=[50, 3], block=[3, 1], seed=13)
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    k, v, q = s["k"].to(dev), s["v"].to(dev), s["q"].to(dev)
+    st = torch.cuda.Stream(dev)
+    st.wait_stream(torch.cuda.current_stream(dev))
+    s["cache"].write(k, v, pages, stream=st, **a)
+    out, lse = s["cache"].attend(q, pages, stream=st, **a)
+    kk, _ = s["cache"].read(pages, a["table"], rows=4, stream=st)
+    st.synchronize()
+    raw = ref.write(s["raw"], 16, s["table"], s["lens"], s["k"], s["v"], s["block"], s["ks"], s["vs"])
+    compare(s, raw, s["q"], out, lse)
+    assert bool((out[1, 1:] == 0).all()) and bool(torch.isneginf(lse[1, 1:]).all())
+    assert kk.shape == (2, 4, 1, 64)
+
+
 def test_gpu_refusals(dev):
     c = binding.BlockCache(dev, 4, 2, 64, 16, max_batch=2)
     pages = c.alloc(4)
