@@ -381,8 +381,8 @@ __device__ __forceinline__ void group_sync(int id) {
 // left the CTAs with many short segments 29% behind the mean (256 requests of
 // 64..4096 positions).
 __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t& n, int& L) {
-  n = __ldg(p.cache_len + i);
-  L = p.block_len ? min(max(__ldg(p.block_len + i), 0), p.T) : p.T;
+  n = p.cache_len[i];
+  L = p.block_len ? min(max(p.block_len[i], 0), p.T) : p.T;
   return n >= 0 && n + L <= p.c.capacity;
 }
 
@@ -1072,7 +1072,7 @@ __device__ __forceinline__ void attend_load_q(const AttendParams& p, AttendShare
   const int ch = lane * E;
   const uint16_t* q = static_cast<const uint16_t*>(p.q.data) + s.i * p.q.sb +
                       static_cast<int64_t>(s.h * p.group) * p.q.sh;
-  const float gk = p.c.k_scale ? __ldg(p.c.k_scale + s.h) : 1.0f;
+  const float gk = p.c.k_scale ? p.c.k_scale[s.h] : 1.0f;
   const float unit = p.scale * 1.4426950408889634f * gk;
   struct alignas(E * 2) Raw {
     uint32_t w[E / 2];
@@ -1171,7 +1171,7 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
     const bool cut = s.t0 > 0 || s.t1 < s.tiles;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 > 0 ? 0 : 1);
     const uint32_t* row = sh.row[ns % kSegs];
-    const float gv = p.c.v_scale ? __ldg(p.c.v_scale + s.h) : 1.0f;
+    const float gv = p.c.v_scale ? p.c.v_scale[s.h] : 1.0f;
     for (int r = lane; r < s.rows; r += 32) {
       // join the sets: a set that saw nothing of the row (or had no tile) has l = 0
       float l[G::kSets], mr = -INFINITY, sum = 0.0f;
@@ -1331,6 +1331,8 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  // what came before in the stream is complete: from here on memory is read
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // this CTA's share of the units
   long long mine = 0, total = 0, before = 0;
 #pragma unroll 1
@@ -1418,6 +1420,7 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
   __shared__ float inv[kJoinRows];
   __shared__ float sum[kJoinRows][kThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const AttendCut& cut = p.cuts[blockIdx.x + 1];
   const int last = __ldcg(&cut.last);
   if (last < 0) return;
@@ -1429,7 +1432,7 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto slot = [&](int e) { return 2 * (first + e) + (e == 0 ? 1 : 0); };
   const int nr = min(kJoinRows, rows - r0);
-  const float gv = p.c.v_scale ? __ldg(p.c.v_scale + h) : 1.0f;
+  const float gv = p.c.v_scale ? p.c.v_scale[h] : 1.0f;
   if (warp < nr) {
     const int r = r0 + warp;
     constexpr int kPer = kJoinMaxParts / 32;

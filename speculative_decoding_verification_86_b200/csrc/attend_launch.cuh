@@ -1,6 +1,7 @@
 // The attention's launches, one unit per head width (attend64.cu and so on).
 #pragma once
 #include "attend.cuh"
+#include "host.cuh"
 
 namespace sv {
 
@@ -39,19 +40,10 @@ struct AttendRun {
     if (*started || p.rp > NP) return true;
     *started = true;
     using G = AttendGeo<SV_ATTEND_WIDTH, NP>;
-    k_attend<SV_ATTEND_WIDTH, NP><<<num_sms, G::kThreads, G::kSmemBytes, stream>>>(p);
-    if (num_sms == 1) return true;
-    // the join starts while the attention drains, and waits for its end by itself
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(num_sms - 1, (p.rp + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(join_threads(SV_ATTEND_WIDTH));
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attend_join<SV_ATTEND_WIDTH, NP>, p) == cudaSuccess;
+    return launch_waiting(k_attend<SV_ATTEND_WIDTH, NP>, dim3(num_sms), G::kThreads, G::kSmemBytes, stream, p) &&
+           (num_sms == 1 || launch_waiting(k_attend_join<SV_ATTEND_WIDTH, NP>,
+                                           dim3(num_sms - 1, (p.rp + kJoinRows - 1) / kJoinRows),
+                                           join_threads(SV_ATTEND_WIDTH), 0, stream, p));
   }
 };
 }  // namespace

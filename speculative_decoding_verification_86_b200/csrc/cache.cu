@@ -67,7 +67,9 @@ spec_status check_rows(const spec_cache_rows* r, spec_dtype dtype, sv::CacheRows
   const int64_t unit = static_cast<int64_t>(16 / dtype_bytes(dtype));
   if (!aligned(r->data, 16) || r->stride_b % unit || r->stride_t % unit || r->stride_h % unit)
     return SPEC_ERR_UNSUPPORTED;
-  *out = sv::CacheRows{r->data, r->stride_b, r->stride_t, r->stride_h};
+  const bool wide = aligned(r->data, 32) && r->stride_b % (2 * unit) == 0 && r->stride_t % (2 * unit) == 0 &&
+                    r->stride_h % (2 * unit) == 0;
+  *out = sv::CacheRows{r->data, r->stride_b, r->stride_t, r->stride_h, wide};
   return SPEC_OK;
 }
 
@@ -78,17 +80,19 @@ spec_status launch_move(const sv::CacheMove& p, spec_dtype dtype, cudaStream_t s
   const int64_t warps = static_cast<int64_t>(p.B) * p.runs * p.c.heads * 2 * (WRITE ? D / 64 : 1);
   const int64_t blocks = (warps * 32 + sv::kMoveThreads - 1) / sv::kMoveThreads;
   if (blocks > 0x7fffffff) return SPEC_ERR_INVALID_ARG;
-  const dim3 g(static_cast<unsigned>(blocks)), b(sv::kMoveThreads);
-  if constexpr (WRITE) {
-    if (dtype == SPEC_F32) sv::k_cache_write<D, float><<<g, b, 0, stream>>>(p);
-    else if (dtype == SPEC_BF16) sv::k_cache_write<D, __nv_bfloat16><<<g, b, 0, stream>>>(p);
-    else sv::k_cache_write<D, __half><<<g, b, 0, stream>>>(p);
-  } else {
-    if (dtype == SPEC_F32) sv::k_cache_read<D, float><<<g, b, 0, stream>>>(p);
-    else if (dtype == SPEC_BF16) sv::k_cache_read<D, __nv_bfloat16><<<g, b, 0, stream>>>(p);
-    else sv::k_cache_read<D, __half><<<g, b, 0, stream>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  auto launch = [&](auto kernel) {
+    return launch_waiting(kernel, dim3(static_cast<unsigned>(blocks)), sv::kMoveThreads, 0, stream, p);
+  };
+  bool ok;
+  if constexpr (WRITE)
+    ok = dtype == SPEC_F32    ? launch(sv::k_cache_write<D, float>)
+         : dtype == SPEC_BF16 ? launch(sv::k_cache_write<D, __nv_bfloat16>)
+                              : launch(sv::k_cache_write<D, __half>);
+  else
+    ok = dtype == SPEC_F32    ? launch(sv::k_cache_read<D, float>)
+         : dtype == SPEC_BF16 ? launch(sv::k_cache_read<D, __nv_bfloat16>)
+                              : launch(sv::k_cache_read<D, __half>);
+  return ok ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 template <bool WRITE>

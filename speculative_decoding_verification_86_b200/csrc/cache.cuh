@@ -43,6 +43,7 @@ struct CacheView {
 struct CacheRows {
   void* data;
   int64_t sb, st, sh;  // elements
+  bool wide;           // rows start on 32 bytes
 };
 
 // The run `run` (position / 16) of request i, head h; nullptr where the table
@@ -50,7 +51,7 @@ struct CacheRows {
 template <int D>
 __device__ __forceinline__ uint8_t* cache_run(const CacheView& c, int i, int h, int64_t run) {
   const int per_page = c.page_shift - 4;  // log2(runs of a page)
-  const int64_t page = __ldg(c.table + i * c.table_stride + (run >> per_page));
+  const int64_t page = c.table[i * c.table_stride + (run >> per_page)];
   if (page < 0 || page >= c.num_pages) return nullptr;
   const int64_t r = ((page * c.heads + h) << per_page) + (run & ((1 << per_page) - 1));
   return c.pages + r * run_bytes(D);
@@ -119,25 +120,49 @@ __device__ __forceinline__ float2 h2_to_f2(uint32_t a) {
   return __half22float2(*reinterpret_cast<const __half2*>(&a));
 }
 
-// 16 neighbouring channels of a row, as fp32 (32 or 64 aligned bytes); returns the
-// largest magnitude, NaN where there is a NaN.
+// 32 bytes at once where the rows allow it (`wide`: 32-byte aligned), else in two
+// halves: a sector that two instructions write by halves costs twice the requests.
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&v)[8]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+        : "l"(p)
+        : "memory");
+  } else {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&v)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+
+// 16 neighbouring channels of a row, as fp32 (32 or 64 bytes); returns the largest
+// magnitude, NaN where there is a NaN.
 template <typename T>
-__device__ __forceinline__ float load_group(const T* p, float (&x)[16]) {
+__device__ __forceinline__ float load_group(const T* p, bool wide, float (&x)[16]) {
   if constexpr (sizeof(T) == 4) {
     uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(p) + u);
-      x[4 * u] = f.x, x[4 * u + 1] = f.y, x[4 * u + 2] = f.z, x[4 * u + 3] = f.w;
+    for (int u = 0; u < 2; ++u) {
+      uint32_t v[8];
+      load32(p + 8 * u, wide, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[8 * u + e] = __uint_as_float(v[e]);
     }
 #pragma unroll
     for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);  // NaN above all
     return __uint_as_float(top);
   } else {
-    uint4 w[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) w[u] = __ldg(reinterpret_cast<const uint4*>(p) + u);
-    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    uint32_t v[8];
+    load32(p, wide, v);
     uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -160,28 +185,28 @@ __device__ __forceinline__ float load_group(const T* p, float (&x)[16]) {
   }
 }
 template <typename T>
-__device__ __forceinline__ void store_group(T* p, const float (&x)[16]) {
+__device__ __forceinline__ void store_group(T* p, bool wide, const float (&x)[16]) {
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      reinterpret_cast<float4*>(p)[u] = make_float4(x[4 * u], x[4 * u + 1], x[4 * u + 2], x[4 * u + 3]);
-  } else {
-#pragma unroll
     for (int u = 0; u < 2; ++u) {
-      uint32_t v[4];
+      uint32_t v[8];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float a = x[8 * u + 2 * e], b = x[8 * u + 2 * e + 1];
-        if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-          v[e] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-          const __half2 h = __floats2half2_rn(a, b);
-          v[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      }
-      reinterpret_cast<uint4*>(p)[u] = make_uint4(v[0], v[1], v[2], v[3]);
+      for (int e = 0; e < 8; ++e) v[e] = __float_as_uint(x[8 * u + e]);
+      store32(p + 8 * u, wide, v);
     }
+  } else {
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+        v[e] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __half2 h = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+        v[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    store32(p, wide, v);
   }
 }
 
@@ -256,8 +281,8 @@ struct CacheMove {
 
 // The request's span of positions, or false where it is skipped.
 __device__ __forceinline__ bool cache_span(const CacheMove& p, int i, int64_t& n, int& L) {
-  n = p.start ? __ldg(p.start + i) : 0;
-  L = p.count ? min(max(__ldg(p.count + i), 0), p.T) : p.T;
+  n = p.start ? p.start[i] : 0;
+  L = p.count ? min(max(p.count[i], 0), p.T) : p.T;
   return n >= 0 && n + L <= p.c.capacity;
 }
 
@@ -286,8 +311,18 @@ __device__ __forceinline__ bool cache_task(const CacheMove& p, CacheTask& t) {
 
 constexpr int kMoveThreads = 128;
 
+// These kernels and the attention start while what is before them in the stream
+// drains, let what is behind them do the same, and touch memory only after this.
+// So their inputs may change within their lifetime: none is read by a
+// non-coherent load.
+__device__ __forceinline__ void wait_for_stream() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
+  wait_for_stream();
   CacheTask t;
   if (!cache_task<D / 64>(p, t)) return;
   const int lane = threadIdx.x & 31;
@@ -308,7 +343,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   const int b = lane & 7, g = t.chunk * 4 + (lane >> 3);
   const CacheRows& rows = t.is_v ? p.v : p.k;
   const float* gs = t.is_v ? p.c.v_scale : p.c.k_scale;
-  const float rg = gs ? __frcp_rn(__ldg(gs + t.h)) : 1.0f;
+  const float rg = gs ? __frcp_rn(gs[t.h]) : 1.0f;
   const T* src = static_cast<const T*>(rows.data) + t.i * rows.sb + t.h * rows.sh + g * kGroup;
   float x[2][16], top[2] = {0.0f, 0.0f};
   bool in[2];
@@ -317,7 +352,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
     const int tok = 2 * b + u;
     in[u] = tok >= lo && tok < hi;
     if (in[u]) {
-      top[u] = load_group(src + (run * kRun + tok - n) * rows.st, x[u]);
+      top[u] = load_group(src + (run * kRun + tok - n) * rows.st, rows.wide, x[u]);
     } else {
 #pragma unroll
       for (int e = 0; e < 16; ++e) x[u][e] = 0.0f;
@@ -333,13 +368,26 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) sc[u] = quantise_group(x[u], top[u], rg, code[u]);
   if (!t.is_v) {
+    // The lanes of neighbouring groups (lane ^ 8) trade halves, so that each stores
+    // the 16 bytes of one token's chunk: the even group token 2b, the odd one 2b + 1;
+    // and four lanes' scale bytes come together in the first two (lane ^ 8, ^ 16).
+    const int u = g & 1;
+    const uint64_t got = __shfl_xor_sync(0xffffffffu, code[u ^ 1], 8);
+    const uint64_t first = u ? got : code[0], second = u ? code[1] : got;
+    uint32_t four[2];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (!in[u]) continue;
-      const int tok = 2 * b + u;
-      *reinterpret_cast<uint64_t*>(dst + (g >> 1) * 256 + tok * 16 + (g & 1) * 8) = code[u];
-      dst[run_k_scales(D) + tok * (D / kGroup) + g] = static_cast<uint8_t>(sc[u]);
+    for (int v = 0; v < 2; ++v) {
+      uint32_t x = sc[v] << (8 * (g & 3));
+      x |= __shfl_xor_sync(0xffffffffu, x, 8);
+      four[v] = x | __shfl_xor_sync(0xffffffffu, x, 16);
     }
+    const int tok = 2 * b + u;
+    if (!(u ? in[1] : in[0])) return;
+    *reinterpret_cast<uint4*>(dst + (g >> 1) * 256 + tok * 16) =
+        make_uint4(static_cast<uint32_t>(first), static_cast<uint32_t>(first >> 32), static_cast<uint32_t>(second),
+                   static_cast<uint32_t>(second >> 32));
+    if ((g & 2) == 0)
+      *reinterpret_cast<uint32_t*>(dst + run_k_scales(D) + tok * (D / kGroup) + (g & ~3)) = u ? four[1] : four[0];
     return;
   }
   // bytes of channel pairs: channel c of tokens (2b, 2b+1) in byte c
@@ -383,6 +431,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
+  wait_for_stream();
   CacheTask t;
   if (!cache_task<1>(p, t)) return;  // the whole run: all its bytes in flight
   const int lane = threadIdx.x & 31;
@@ -405,7 +454,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
   }
   const int b = lane & 7;
   const float* gs = t.is_v ? p.c.v_scale : p.c.k_scale;
-  const float gv = gs ? __ldg(gs + t.h) : 1.0f;
+  const float gv = gs ? gs[t.h] : 1.0f;
   constexpr int C = D / 64;
   uint4 raw[C];  // keys: token 2b's codes, token 2b + 1's; values: channel 2b's, channel 2b + 1's
   uint32_t sc[C];
@@ -461,7 +510,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
           x[8 * q + 2 * e + 1] = f.y;
         }
       }
-      store_group(out + (run * kRun + tok - n) * rows.st + g * kGroup, x);
+      store_group(out + (run * kRun + tok - n) * rows.st + g * kGroup, rows.wide, x);
     }
   }
 }
