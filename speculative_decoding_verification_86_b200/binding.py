@@ -859,7 +859,8 @@ class BlockCache:
         self.device = dev
         self.heads_q, self.heads_kv, self.head_dim = int(heads_q), int(heads_kv), int(head_dim)
         self.page_size, self.max_batch = int(page_size), int(max_batch)
-        self._page_shape = torch.Size((self.heads_kv, self.page_size // 16, 18 * self.head_dim))
+        self._index = dev.index
+        self._page_shape = (self.heads_kv, self.page_size // 16, 18 * self.head_dim)
         h = _vp()
         _check(lib().spec_cache_init(ctypes.byref(h), dev.index, self.max_batch, self.heads_q,
                                      self.heads_kv, self.head_dim, self.page_size), "spec_cache_init")
@@ -902,75 +903,81 @@ class BlockCache:
         return int(out.value)
 
     # -- helpers --------------------------------------------------------------
-    # A call is a few microseconds on the GPU, so the checks are plain ones: one
-    # look at a tensor's shape, strides, device number and type each.
-    def _dev(self, t, dtype, name):
+    # A small call takes a few microseconds on the GPU, so the checks are plain ones:
+    # one look at a tensor's device number, type, shape and strides each.
+    def _wrong(self, t, dtype, name):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s must be a torch.Tensor" % name)
-        if t.get_device() != self.device.index:
+        if t.get_device() != self._index:
             raise ValueError("%s is on %s, expected %s" % (name, t.device, self.device))
-        if t.dtype is not dtype:
-            raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
 
     def _pages(self, pages, table, B, k_scale, v_scale):
-        self._dev(pages, torch.uint8, "pages")
+        if not isinstance(pages, torch.Tensor) or pages.get_device() != self._index or pages.dtype is not torch.uint8:
+            self._wrong(pages, torch.uint8, "pages")
         n = pages.shape
-        if len(n) != 4 or n[1:] != self._page_shape:
-            raise ValueError("pages must be [num_pages, %d, %d, %d]" % tuple(self._page_shape))
+        if len(n) != 4 or (n[1], n[2], n[3]) != self._page_shape:
+            raise ValueError("pages must be [num_pages, %d, %d, %d]" % self._page_shape)
         if not pages.is_contiguous():
             raise ValueError("pages must be contiguous")
-        self._dev(table, torch.int32, "table")
+        if not isinstance(table, torch.Tensor) or table.get_device() != self._index or table.dtype is not torch.int32:
+            self._wrong(table, torch.int32, "table")
         w = table.shape
         if len(w) != 2 or w[0] != B:
             raise ValueError("table must be [B, width] with B = %d" % B)
-        stride = table.stride()
-        if w[1] > 1 and stride[1] != 1:
+        w = w[1]
+        row, one = table.stride()
+        if one != 1 and w > 1:
             raise ValueError("a row of the table must be contiguous")
-        return CachePages(pages.data_ptr(), n[0], table.data_ptr(), stride[0] if B > 1 else w[1], w[1],
-                          self._vector(k_scale, torch.float32, self.heads_kv, "k_scale"),
-                          self._vector(v_scale, torch.float32, self.heads_kv, "v_scale"))
+        return CachePages(pages.data_ptr(), n[0], table.data_ptr(), row if B > 1 else w, w,
+                          None if k_scale is None else self._vector(k_scale, torch.float32, self.heads_kv, "k_scale"),
+                          None if v_scale is None else self._vector(v_scale, torch.float32, self.heads_kv, "v_scale"))
 
-    def _rows(self, t, heads, name, shape=None, dtype=None):
+    def _rows(self, t, heads, name, shape=None, dtype=None, written=False):
         if not isinstance(t, torch.Tensor):
             raise TypeError("%s must be a torch.Tensor" % name)
-        if t.get_device() != self.device.index:
+        if t.get_device() != self._index:
             raise ValueError("%s must be on %s" % (name, self.device))
         dt = t.dtype
         if dt not in _CACHE_DTYPES or (dtype is not None and dt is not dtype):
             raise TypeError("%s has dtype %s" % (name, dt))
         n = t.shape
-        if len(n) != 4 or n[2] != heads or n[3] != self.head_dim or (shape is not None and n[:2] != shape):
+        if len(n) != 4 or n[2] != heads or n[3] != self.head_dim or (shape is not None and (n[0], n[1]) != shape):
             raise ValueError("%s must be [B, T, %d, %d], got %s" % (name, heads, self.head_dim, tuple(n)))
         b, r, h, c = t.stride()
         if c != 1:
             raise ValueError("the channels of %s must be contiguous" % name)
         # the stride of a dimension of one element says nothing
-        return CacheRows(t.data_ptr(), b if n[0] > 1 else 0, r if n[1] > 1 else 0, h if heads > 1 else 0)
+        if n[0] <= 1:
+            b = 0
+        elif written and b == 0:
+            raise ValueError("%s must not be an expanded tensor" % name)
+        if n[1] <= 1:
+            r = 0
+        elif written and r == 0:
+            raise ValueError("%s must not be an expanded tensor" % name)
+        if heads <= 1:
+            h = 0
+        elif written and h == 0:
+            raise ValueError("%s must not be an expanded tensor" % name)
+        return CacheRows(t.data_ptr(), b, r, h)
 
     def _vector(self, t, dtype, n, name):
-        if t is None:
-            return None
-        self._dev(t, dtype, name)
-        if t.shape != (n,):
+        if not isinstance(t, torch.Tensor) or t.get_device() != self._index or t.dtype is not dtype:
+            self._wrong(t, dtype, name)
+        if t.dim() != 1 or t.numel() != n:
             raise ValueError("%s must be [%d]" % (name, n))
-        if n > 1 and t.stride()[0] != 1:
+        if not t.is_contiguous():
             raise ValueError("%s must be contiguous" % name)
         return t.data_ptr()
 
     def _ints(self, t, B, name):
-        return self._vector(t, torch.int32, B, name)
+        return None if t is None else self._vector(t, torch.int32, B, name)
 
     @staticmethod
     def _on(stream):
         """Outputs that a call makes are filled on the stream that it runs on."""
         return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-    @staticmethod
-    def _one_place(rows, shape, name):
-        """Rows that are written must not share memory (an expanded dimension)."""
-        if (shape[0] > 1 and rows.stride_b == 0) or (shape[1] > 1 and rows.stride_t == 0) or \
-                (shape[2] > 1 and rows.stride_h == 0):
-            raise ValueError("%s must not be an expanded tensor" % name)
 
     # -- entry points ---------------------------------------------------------
     def write(self, k, v, pages, table, cache_len, block_len=None, k_scale=None, v_scale=None,
@@ -980,7 +987,7 @@ class BlockCache:
         tokens of each request."""
         if not isinstance(k, torch.Tensor) or k.dim() != 4:
             raise ValueError("k must be [B, T, %d, %d]" % (self.heads_kv, self.head_dim))
-        B, T = k.shape[:2]
+        B, T, _, _ = k.shape
         kr = self._rows(k, self.heads_kv, "k")
         vr = self._rows(v, self.heads_kv, "v", (B, T), k.dtype)
         if cache_len is None:
@@ -1006,13 +1013,11 @@ class BlockCache:
                 out = (torch.zeros(shape, dtype=dtype, device=self.device),
                        torch.zeros(shape, dtype=dtype, device=self.device))
         k, v = out
-        if k.dim() != 4 or (rows is not None and k.shape[1] != rows):
+        if not isinstance(k, torch.Tensor) or k.dim() != 4 or (rows is not None and k.shape[1] != rows):
             raise ValueError("out must be two [B, rows, %d, %d] tensors" % (self.heads_kv, self.head_dim))
         T = k.shape[1]
-        kr = self._rows(k, self.heads_kv, "out[0]", (B, T))
-        vr = self._rows(v, self.heads_kv, "out[1]", (B, T), k.dtype)
-        self._one_place(kr, k.shape, "out[0]")
-        self._one_place(vr, v.shape, "out[1]")
+        kr = self._rows(k, self.heads_kv, "out[0]", (B, T), written=True)
+        vr = self._rows(v, self.heads_kv, "out[1]", (B, T), k.dtype, written=True)
         pg = self._pages(pages, table, B, k_scale, v_scale)
         st = lib().spec_cache_read(
             self._h, ctypes.byref(pg), self._ints(start, B, "start"), self._ints(count, B, "count"), B, T,
@@ -1033,15 +1038,14 @@ class BlockCache:
             raise ValueError("q must be [B, T, %d, %d]" % (self.heads_q, self.head_dim))
         if q.dtype == torch.float32:
             raise TypeError("q must be bfloat16 or float16")
-        B, T = q.shape[:2]
+        B, T, _, _ = q.shape
         qr = self._rows(q, self.heads_q, "q")
         if cache_len is None:
             raise ValueError("cache_len is needed")
         if out is None:
             with self._on(stream):
                 out = torch.zeros((B, T, self.heads_q, self.head_dim), dtype=q.dtype, device=self.device)
-        outr = self._rows(out, self.heads_q, "out", (B, T), q.dtype)
-        self._one_place(outr, out.shape, "out")
+        outr = self._rows(out, self.heads_q, "out", (B, T), q.dtype, written=True)
         if lse is None or lse is True:
             with self._on(stream):
                 lse = torch.full((B, T, self.heads_q), float("-inf"), device=self.device)
@@ -1049,7 +1053,8 @@ class BlockCache:
             lse = None
         lse_ptr = None
         if lse is not None:
-            self._dev(lse, torch.float32, "lse")
+            if not isinstance(lse, torch.Tensor) or lse.get_device() != self._index or lse.dtype is not torch.float32:
+                self._wrong(lse, torch.float32, "lse")
             if lse.shape != (B, T, self.heads_q) or not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous [B, T, %d]" % self.heads_q)
             lse_ptr = lse.data_ptr()

@@ -50,6 +50,8 @@ struct AttendParams {
   const int32_t* block_len;  // nullptr: T
   int B, T, heads_q, group;  // group: query heads per key/value head
   int rp;                    // query rows of a row tile
+  uint32_t group_mul;        // of_group
+  int group_shift;
   int seg_units;             // what a segment costs beside its tiles, in tiles
   int bf16;                  // q and out are bf16 (else fp16)
   float scale;
@@ -166,7 +168,7 @@ struct alignas(16) AttendShared {
   long long scan[32];
   long long units;      // this CTA's share: number of units, and where it starts
   int start_i;
-  long long start_off;
+  long long start_off, start_units;
   uint32_t tmem;
 };
 
@@ -386,10 +388,23 @@ __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t
   return n >= 0 && n + L <= p.c.capacity;
 }
 
-static __device__ __noinline__ void attend_rows(const AttendParams& p, int64_t n, int L, int rt, AttendSeg& s) {
+// row / group for 0 <= row < 2^31, by a multiplication: with 2^shift >= group and
+// mul = floor(2^32 (2^shift - group) / group) + 1 the error of (2^32 + mul) row / 2^32
+// stays below 2^shift / group for such rows.  (The plan is on every call's way; a
+// division by a number that is not known here is some 100 cycles each time.)
+__device__ __forceinline__ int of_group(const AttendParams& p, int row) {
+  return static_cast<int>((__umulhi(static_cast<uint32_t>(row), p.group_mul) + static_cast<uint32_t>(row)) >>
+                          p.group_shift);
+}
+__device__ __forceinline__ int row_tiles(const AttendParams& p, int L) {
+  const int rows = L * p.group;
+  return rows <= p.rp ? (rows > 0) : (rows + p.rp - 1) / p.rp;
+}
+
+__device__ __forceinline__ void attend_rows(const AttendParams& p, int64_t n, int L, int rt, AttendSeg& s) {
   s.row0 = rt * p.rp;
   s.rows = min(p.rp, L * p.group - s.row0);
-  const int j0 = s.row0 / p.group, j1 = (s.row0 + s.rows - 1) / p.group;
+  const int j0 = of_group(p, s.row0), j1 = of_group(p, s.row0 + s.rows - 1);
   const int64_t hi = p.causal ? n + j1 + 1 : n + L;
   const int64_t lo = p.window ? max(n + j0 + 1 - p.window, int64_t(0)) : 0;
   s.run0 = lo >> 4;
@@ -404,11 +419,11 @@ static __device__ __noinline__ void attend_rows(const AttendParams& p, int64_t n
 }
 
 // Units of one head of request i; -1 where the request is skipped.
-static __device__ __noinline__ long long attend_units(const AttendParams& p, int i) {
+__device__ __forceinline__ long long attend_units(const AttendParams& p, int i) {
   int64_t n;
   int L;
   if (!attend_len(p, i, n, L)) return -1;
-  const int nrt = (L * p.group + p.rp - 1) / p.rp;
+  const int nrt = row_tiles(p, L);
   long long u = 0;
   AttendSeg s;
 #pragma unroll 1
@@ -420,11 +435,23 @@ static __device__ __noinline__ long long attend_units(const AttendParams& p, int
 }
 
 static __device__ __noinline__ long long div64(long long a, long long b) { return a / b; }
-// CTA c of n takes the units [total c / n, total (c + 1) / n); the CTA of a unit.
-__device__ __forceinline__ long long share_start(long long total, int c, int n) { return div64(total * c, n); }
-__device__ __forceinline__ int share_of(long long total, long long unit, int n) {
-  return static_cast<int>(div64((unit + 1) * n - 1, total));
+// a / b for a >= 0, b > 0; small numbers in a few instructions
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 31) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : div64(a, b);
 }
+// Of n CTAs each takes `base` units, the first `more` of them one more.
+struct AttendShares {
+  long long base;
+  int more;
+  __device__ __forceinline__ AttendShares(long long total, int n) : base(quotient(total, n)) {
+    more = static_cast<int>(total - base * n);
+  }
+  __device__ __forceinline__ long long start(int c) const { return base * c + min(c, more); }
+  __device__ __forceinline__ int of(long long unit) const {
+    const long long t = (base + 1) * more;
+    return static_cast<int>(unit < t ? quotient(unit, base + 1) : more + quotient(unit - t, base));
+  }
+};
 
 // All lanes of a warp leave a wait together; false where the phase did not complete
 // within kWaitTries tries.  A try sleeps for up to 2700 cycles (measured), so that
@@ -443,7 +470,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 // One warp.  Also leaves the cut at the start of the share for k_attend_join.
 template <int D, int NP>
 __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<D, NP>& sh, long long u0,
-                                            long long total, int n_ctas) {
+                                            const AttendShares& shares) {
   const int lane = threadIdx.x & 31;
   long long left = sh.units, off = sh.start_off;
   int i = sh.start_i, h = 0, rt = 0;
@@ -451,16 +478,20 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
   uint32_t ns = 0;
   int64_t n = 0;
   int L = 0, nrt = 0;
+  long long per_head = sh.start_units;
+  bool known = true;  // per_head is request i's
   bool open = false;  // request i is under way at (h, rt, off tiles into it)
   AttendCut cut;
   cut.last = -1;
   while (left > 0) {
     if (!open) {
-      long long per_head = 0;
-      while ((per_head = attend_units(p, i)) <= 0) ++i;  // requests without units
+      if (!known) {
+        while ((per_head = attend_units(p, i)) <= 0) ++i;  // requests without units
+      }
+      known = false;
       attend_len(p, i, n, L);
-      nrt = (L * p.group + p.rp - 1) / p.rp;
-      h = static_cast<int>(div64(off, per_head));
+      nrt = row_tiles(p, L);
+      h = off ? static_cast<int>(quotient(off, per_head)) : 0;
       off -= h * per_head;
       rt = 0;
       open = true;
@@ -478,13 +509,13 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
     s.t1 = static_cast<int>(max(min(static_cast<long long>(all), off + left) - p.seg_units, 0ll));
     if (ns == 0 && s.t0 > 0) {
       const long long first = u0 - s.t0;  // the segment's first tile
-      if (share_of(total, first, n_ctas) == static_cast<int>(blockIdx.x) - 1) {
+      if (shares.of(first) == static_cast<int>(blockIdx.x) - 1) {
         cut.i = s.i;
         cut.h = s.h;
         cut.row0 = s.row0;
         cut.rows = s.rows;
         cut.first = static_cast<int>(blockIdx.x) - 1;
-        cut.last = share_of(total, first + s.tiles - 1, n_ctas);
+        cut.last = shares.of(first + s.tiles - 1);
       }
     }
     const long long here = min(static_cast<long long>(all) - off, left);
@@ -493,7 +524,7 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
       const int slot = static_cast<int>(ns % kSegs);
       if (!warp_wait(&sh.segfree[slot], ((ns / kSegs) & 1u) ^ 1u)) break;
       for (int r = lane; r < NP; r += 32) {
-        const int row = s.row0 + r, j = row / p.group;
+        const int row = s.row0 + r, j = of_group(p, row);
         sh.row[slot][r] = static_cast<uint32_t>(j) << 16 | static_cast<uint32_t>(row - j * p.group);
         int2 v = make_int2(0, INT_MAX);
         if (r < s.rows) {
@@ -671,7 +702,7 @@ static __device__ __noinline__ unsigned long long attend_nan_rows(const AttendPa
     const uint8_t* run = cache_run<D>(p.c, s.i, s.h, s.run0 + (t >> 4));
     if (!run || (run[run_v_scales(D) + group * 16 + (t & 15)] & 0x7fu) != kScaleNaN) continue;
     for (int r = 0; r < s.rows; ++r) {
-      const int64_t q = s.n + (s.row0 + r) / p.group, pos = base + t;
+      const int64_t q = s.n + of_group(p, s.row0 + r), pos = base + t;
       if ((p.causal ? pos <= q : pos < s.n + s.L) && (!p.window || pos > q - p.window)) m |= 1ull << r;
     }
   }
@@ -1262,25 +1293,28 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
   return true;
 }
 
-// Exclusive prefix of v over the CTA, and the total.
+// Exclusive prefix of v over the first `warps` warps of the CTA, and the total; the
+// value of the others' threads is not looked at.
 template <class SH>
-__device__ __forceinline__ long long block_scan(SH& sh, long long v, long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+__device__ __forceinline__ long long block_scan(SH& sh, long long v, int warps, long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
+  if (warp < warps) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sh.scan[warp] = x;
   }
-  __syncthreads();
-  if (lane == 31) sh.scan[warp] = x;
   __syncthreads();
   long long before = 0;
   total = 0;
-#pragma unroll 1
+#pragma unroll 4
   for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += sh.scan[w];
-    total += sh.scan[w];
+    const long long y = sh.scan[w];
+    if (w < warp) before += y;
+    total += y;
   }
   return before + x - v;
 }
@@ -1322,6 +1356,7 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
     mbar_init(&sh.drain, 1);
     sh.start_i = 0;
     sh.start_off = 0;
+    sh.start_units = 0;
     mbar_init_fence();
   }
   if (threadIdx.x < kSegs) sh.nan_seen[threadIdx.x] = 0;
@@ -1334,40 +1369,42 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   // what came before in the stream is complete: from here on memory is read
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // this CTA's share of the units
-  long long mine = 0, total = 0, before = 0;
+  long long per_head = 0, mine = 0, total = 0, before = 0;
+  auto scan = [&](int i0, bool tell) {
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    per_head = i < p.B ? attend_units(p, i) : 0;
+    if (per_head < 0) {
+      per_head = 0;
+      if (tell && p.status && blockIdx.x == 0) atomicOr(p.status + i, kDevBadLength);
+    }
+    mine = per_head * p.c.heads;
+    long long sum;
+    before = total + block_scan(sh, mine, (min(p.B - i0, G::kThreads) + 31) >> 5, sum);
+    total += sum;
+  };
 #pragma unroll 1
   for (int i0 = 0; i0 < p.B; i0 += G::kThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x);
-    mine = 0;
-    if (i < p.B) {
-      mine = attend_units(p, i) * p.c.heads;
-      if (mine < 0) {
-        mine = 0;
-        if (p.status && blockIdx.x == 0) atomicOr(p.status + i, kDevBadLength);
-      }
-    }
-    long long sum;
-    before = total + block_scan(sh, mine, sum);
-    total += sum;
+    if (i0) __syncthreads();
+    scan(i0, true);
   }
   const int n = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
   const int c = static_cast<int>(blockIdx.x);
-  const long long u0 = c < n ? share_start(total, c, n) : 0, u1 = c < n ? share_start(total, c + 1, n) : 0;
+  const AttendShares shares(total, max(n, 1));
+  const long long u0 = c < n ? shares.start(c) : 0, u1 = c < n ? shares.start(c + 1) : 0;
   // whose request holds unit u0: known from the scan, or from a second one where
   // the batch is larger than the CTA
+  const bool once = p.B <= G::kThreads;
+  if (!once) total = 0;
 #pragma unroll 1
-  for (int i0 = 0, once = p.B <= G::kThreads; i0 < p.B; i0 += G::kThreads) {
-    const int i = i0 + static_cast<int>(threadIdx.x);
+  for (int i0 = 0; i0 < p.B; i0 += G::kThreads) {
     if (!once) {
-      if (i0 == 0) total = 0;
-      mine = i < p.B ? max(attend_units(p, i), 0ll) * p.c.heads : 0;
-      long long sum;
-      before = total + block_scan(sh, mine, sum);
-      total += sum;
+      __syncthreads();
+      scan(i0, false);
     }
     if (u0 >= before && u0 < before + mine) {
-      sh.start_i = i;
+      sh.start_i = i0 + static_cast<int>(threadIdx.x);
       sh.start_off = u0 - before;
+      sh.start_units = per_head;
     }
   }
   if (threadIdx.x == 0) sh.units = u1 - u0;
@@ -1381,7 +1418,7 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   } else if (warp == G::kWarpMma) {
     ok = attend_mma<D, NP>(p, sh, q_smem, p_smem);
   } else if (warp == G::kWarpPlan) {
-    ok = attend_plan<D, NP>(p, sh, u0, total, n);
+    ok = attend_plan<D, NP>(p, sh, u0, shares);
   } else if (warp < 4) {
     ok = attend_keys<D, NP>(p, sh, stages);
   } else if (warp < 8) {
@@ -1461,7 +1498,7 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
     if (lane == 0) {
       inv[warp] = l == 0.0f ? 0.0f : __frcp_rn(l);
       if (p.lse) {
-        const int row = row0 + r, j = row / p.group, hq = h * p.group + row % p.group;
+        const int row = row0 + r, j = of_group(p, row), hq = h * p.group + row - j * p.group;
         p.lse[(static_cast<int64_t>(i) * p.T + j) * p.heads_q + hq] =
             l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       }
@@ -1486,7 +1523,7 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
 #pragma unroll
     for (int u = 0; u < S; ++u) o += sum[r][u * D + cc];
     o = o * inv[r] * gv;
-    const int row = row0 + r0 + r, j = row / p.group, hq = h * p.group + row % p.group;
+    const int row = row0 + r0 + r, j = of_group(p, row), hq = h * p.group + row - j * p.group;
     const int64_t to = i * p.out.sb + j * p.out.st + hq * p.out.sh + cc;
     if (p.bf16) static_cast<__nv_bfloat16*>(p.out.data)[to] = __float2bfloat16_rn(o);
     else static_cast<__half*>(p.out.data)[to] = __float2half_rn(o);

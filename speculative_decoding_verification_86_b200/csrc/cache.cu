@@ -253,11 +253,14 @@ spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
   p.lse = out_lse;
   p.status = out_status;
   p.bf16 = dtype == SPEC_BF16;
+  while ((1u << p.group_shift) < static_cast<uint32_t>(p.group)) ++p.group_shift;
+  p.group_mul = static_cast<uint32_t>(
+      (((uint64_t{1} << p.group_shift) - static_cast<uint64_t>(p.group)) << 32) / static_cast<uint64_t>(p.group) + 1);
   // row tiles of equal size
   const int64_t rows = static_cast<int64_t>(T) * p.group;
   const int64_t tiles = (rows + max_rows(c->head_dim) - 1) / max_rows(c->head_dim);
   p.rp = static_cast<int>((rows + tiles - 1) / tiles);
-  if (rows > INT_MAX) return SPEC_ERR_INVALID_ARG;
+  if (rows > INT_MAX - 64) return SPEC_ERR_INVALID_ARG;
   // 3 against 6: decoding 64 requests (8 rows) 97 and 100 us, verifying 256 (24
   // rows) 283 and 268 us
   p.seg_units = p.rp <= 16 ? 3 : 6;
