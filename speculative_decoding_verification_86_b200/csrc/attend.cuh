@@ -507,17 +507,6 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
     s.h = h;
     s.t0 = static_cast<int>(max(off - p.seg_units, 0ll));
     s.t1 = static_cast<int>(max(min(static_cast<long long>(all), off + left) - p.seg_units, 0ll));
-    if (ns == 0 && s.t0 > 0) {
-      const long long first = u0 - s.t0;  // the segment's first tile
-      if (shares.of(first) == static_cast<int>(blockIdx.x) - 1) {
-        cut.i = s.i;
-        cut.h = s.h;
-        cut.row0 = s.row0;
-        cut.rows = s.rows;
-        cut.first = static_cast<int>(blockIdx.x) - 1;
-        cut.last = shares.of(first + s.tiles - 1);
-      }
-    }
     const long long here = min(static_cast<long long>(all) - off, left);
     off = 0;
     if (s.t1 > s.t0) {
@@ -540,7 +529,18 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.segfull[slot]);
-  ++ns;
+      if (ns == 0 && s.t0 > 0) {  // behind the first segment, which the roles wait for
+        const long long first = u0 - s.t0;  // the segment's first tile
+        if (shares.of(first) == static_cast<int>(blockIdx.x) - 1) {
+          cut.i = s.i;
+          cut.h = s.h;
+          cut.row0 = s.row0;
+          cut.rows = s.rows;
+          cut.first = static_cast<int>(blockIdx.x) - 1;
+          cut.last = shares.of(first + s.tiles - 1);
+        }
+      }
+      ++ns;
     }
     left -= here;
     if (++rt == nrt) {
@@ -1000,10 +1000,12 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
             attend_columns<0, 8>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
           } else {
             attend_columns<0, 16>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
-            if constexpr (CW == 24)
-              attend_columns<16, 8>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
-            if constexpr (CW == 32)
-              attend_columns<16, 16>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
+            // columns behind the segment's rows: whatever their P holds stays in
+            // columns of O that nobody reads
+            if constexpr (CW > 16) {
+              if (rows > c0 + 16)
+                attend_columns<16, CW - 16>(s_tmem, cs, nm, p.one, whole, see, pt, c0, pflip, again, redo, l, top);
+            }
           }
           fence_async_shared();
         }
@@ -1196,13 +1198,13 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
       continue;
     }
     const uint32_t ns = na - 1, ob = ns % G::kOB, par = (ns / G::kOB) & 1u;
+    const float gv = p.c.v_scale ? p.c.v_scale[s.h] : 1.0f;
     if (!warp_wait(&sh.lready[ob], par)) return false;
     if (!warp_wait(&sh.oready[ob], par)) return false;
     tc_fence_after();
     const bool cut = s.t0 > 0 || s.t1 < s.tiles;
     const int slot = 2 * static_cast<int>(blockIdx.x) + (s.t0 > 0 ? 0 : 1);
     const uint32_t* row = sh.row[ns % kSegs];
-    const float gv = p.c.v_scale ? p.c.v_scale[s.h] : 1.0f;
     for (int r = lane; r < s.rows; r += 32) {
       // join the sets: a set that saw nothing of the row (or had no tile) has l = 0
       float l[G::kSets], mr = -INFINITY, sum = 0.0f;
