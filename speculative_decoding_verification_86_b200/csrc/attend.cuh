@@ -50,8 +50,7 @@ struct AttendParams {
   const int32_t* block_len;  // nullptr: T
   int B, T, heads_q, group;  // group: query heads per key/value head
   int rp;                    // query rows of a row tile
-  uint32_t group_mul;        // of_group
-  int group_shift;
+  Quotient by_group;
   int seg_units;             // what a segment costs beside its tiles, in tiles
   int bf16;                  // q and out are bf16 (else fp16)
   float scale;
@@ -388,13 +387,8 @@ __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t
   return n >= 0 && n + L <= p.c.capacity;
 }
 
-// row / group for 0 <= row < 2^31, by a multiplication: with 2^shift >= group and
-// mul = floor(2^32 (2^shift - group) / group) + 1 the error of (2^32 + mul) row / 2^32
-// stays below 2^shift / group for such rows.  (The plan is on every call's way; a
-// division by a number that is not known here is some 100 cycles each time.)
 __device__ __forceinline__ int of_group(const AttendParams& p, int row) {
-  return static_cast<int>((__umulhi(static_cast<uint32_t>(row), p.group_mul) + static_cast<uint32_t>(row)) >>
-                          p.group_shift);
+  return static_cast<int>(p.by_group(static_cast<uint32_t>(row)));
 }
 __device__ __forceinline__ int row_tiles(const AttendParams& p, int L) {
   const int rows = L * p.group;

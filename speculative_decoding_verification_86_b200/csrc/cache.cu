@@ -76,12 +76,14 @@ spec_status check_rows(const spec_cache_rows* r, spec_dtype dtype, sv::CacheRows
 // Launch the write (a warp per 64 channels of a run, keys or values) or the read
 // (a warp per run).
 template <bool WRITE, int D>
-spec_status launch_move(const sv::CacheMove& p, spec_dtype dtype, cudaStream_t stream) {
-  const int64_t warps = static_cast<int64_t>(p.B) * p.runs * p.c.heads * 2 * (WRITE ? D / 64 : 1);
-  const int64_t blocks = (warps * 32 + sv::kMoveThreads - 1) / sv::kMoveThreads;
-  if (blocks > 0x7fffffff) return SPEC_ERR_INVALID_ARG;
+spec_status launch_move(sv::CacheMove& p, int64_t runs, spec_dtype dtype, cudaStream_t stream) {
+  const int64_t warps = runs * p.c.heads * 2 * (WRITE ? D / 64 : 1);
+  if (warps >= (int64_t{1} << 27)) return SPEC_ERR_INVALID_ARG;  // threads in 32 bits
+  p.warps = static_cast<uint32_t>(warps);
+  p.by_heads = sv::Quotient(static_cast<uint32_t>(p.c.heads));
+  const dim3 grid(static_cast<unsigned>((warps * 32 + sv::kMoveThreads - 1) / sv::kMoveThreads), p.B);
   auto launch = [&](auto kernel) {
-    return launch_waiting(kernel, dim3(static_cast<unsigned>(blocks)), sv::kMoveThreads, 0, stream, p);
+    return launch_waiting(kernel, grid, sv::kMoveThreads, 0, stream, p);
   };
   bool ok;
   if constexpr (WRITE)
@@ -114,14 +116,14 @@ spec_status move(spec_cache_ctx* c, const spec_cache_pages* cache, const spec_ca
   p.count = count;
   p.B = B;
   p.T = T;
-  p.runs = (static_cast<int64_t>(T) + 2 * (sv::kRun - 1)) / sv::kRun;  // a span may start anywhere in a run
+  const int64_t runs = (static_cast<int64_t>(T) + 2 * (sv::kRun - 1)) / sv::kRun;  // a span may start anywhere in a run
   p.status = out_status;
   DeviceGuard g(c->device);
   if (!g.ok) return SPEC_ERR_CUDA;
   cudaGetLastError();
-  if (c->head_dim == 64) return launch_move<WRITE, 64>(p, dtype, stream);
-  if (c->head_dim == 128) return launch_move<WRITE, 128>(p, dtype, stream);
-  return launch_move<WRITE, 256>(p, dtype, stream);
+  if (c->head_dim == 64) return launch_move<WRITE, 64>(p, runs, dtype, stream);
+  if (c->head_dim == 128) return launch_move<WRITE, 128>(p, runs, dtype, stream);
+  return launch_move<WRITE, 256>(p, runs, dtype, stream);
 }
 
 // Query rows of a row tile at most: the accumulators of 128 (256) channels
@@ -253,9 +255,7 @@ spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
   p.lse = out_lse;
   p.status = out_status;
   p.bf16 = dtype == SPEC_BF16;
-  while ((1u << p.group_shift) < static_cast<uint32_t>(p.group)) ++p.group_shift;
-  p.group_mul = static_cast<uint32_t>(
-      (((uint64_t{1} << p.group_shift) - static_cast<uint64_t>(p.group)) << 32) / static_cast<uint64_t>(p.group) + 1);
+  p.by_group = sv::Quotient(static_cast<uint32_t>(p.group));
   // row tiles of equal size
   const int64_t rows = static_cast<int64_t>(T) * p.group;
   const int64_t tiles = (rows + max_rows(c->head_dim) - 1) / max_rows(c->head_dim);

@@ -28,6 +28,23 @@ __host__ __device__ constexpr int run_k_scales(int D) { return 8 * D; }
 __host__ __device__ constexpr int run_v_codes(int D) { return 9 * D; }
 __host__ __device__ constexpr int run_v_scales(int D) { return 17 * D; }
 
+// n / d for 0 <= n < 2^31 by a multiplication: with 2^shift >= d and
+// mul = floor(2^32 (2^shift - d) / d) + 1 the error of (2^32 + mul) n / 2^32 stays
+// below 2^shift / d for such n.  A division by a number that the compiler does not
+// know is some 100 cycles.
+struct Quotient {
+  uint32_t mul = 0;
+  int shift = 0;
+  Quotient() = default;
+  explicit Quotient(uint32_t d) {
+    while ((1u << shift) < d) ++shift;
+    mul = static_cast<uint32_t>((((uint64_t{1} << shift) - d) << 32) / d + 1);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(n, mul) + n) >> shift; }
+#endif
+};
+
 struct CacheView {
   uint8_t* pages;
   int64_t num_pages;
@@ -144,46 +161,49 @@ __device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&v)[
   }
 }
 
-// 16 neighbouring channels of a row, as fp32 (32 or 64 bytes); returns the largest
-// magnitude, NaN where there is a NaN.
+// 16 neighbouring channels of a row, as they are (half the registers of fp32, so
+// more warps are resident), and as fp32.
 template <typename T>
-__device__ __forceinline__ float load_group(const T* p, bool wide, float (&x)[16]) {
-  if constexpr (sizeof(T) == 4) {
-    uint32_t top = 0;
+struct Group {
+  static constexpr int kWords = 4 * sizeof(T);
+  uint32_t v[kWords];
+
+  __device__ __forceinline__ void load(const T* p, bool wide) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      uint32_t v[8];
-      load32(p + 8 * u, wide, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[8 * u + e] = __uint_as_float(v[e]);
-    }
-#pragma unroll
-    for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);  // NaN above all
-    return __uint_as_float(top);
-  } else {
-    uint32_t v[8];
-    load32(p, wide, v);
-    uint32_t top = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float2 f;
-      if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-        f = make_float2(__uint_as_float(v[e] << 16), __uint_as_float(v[e] & 0xffff0000u));
-        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(top) : "r"(v[e] & 0x7fff7fffu));
-      } else {
-        f = h2_to_f2(v[e]);
-        asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(top) : "r"(v[e] & 0x7fff7fffu));
-      }
-      x[2 * e] = f.x;
-      x[2 * e + 1] = f.y;
-    }
-    float2 t;
-    if constexpr (std::is_same<T, __nv_bfloat16>::value)
-      t = make_float2(__uint_as_float(top << 16), __uint_as_float(top & 0xffff0000u));
-    else t = h2_to_f2(top);
-    return t.x != t.x || t.x > t.y ? t.x : t.y;
+    for (int u = 0; u < kWords / 8; ++u) load32(p + 8 * u, wide, *reinterpret_cast<uint32_t(*)[8]>(v + 8 * u));
   }
-}
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int e = 0; e < kWords; ++e) v[e] = 0;
+  }
+  __device__ __forceinline__ float2 pair(uint32_t w) const {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return h2_to_f2(w);
+  }
+  // elements 2 e and 2 e + 1
+  __device__ __forceinline__ float2 at(int e) const {
+    if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+    else return pair(v[e]);
+  }
+  // the largest magnitude, NaN where there is a NaN
+  __device__ __forceinline__ float top() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int e = 0; e < kWords; ++e) {
+      if constexpr (sizeof(T) == 4) m = max(m, v[e] & 0x7fffffffu);  // NaN above all
+      else if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v[e] & 0x7fff7fffu));
+      else asm("max.NaN.f16x2 %0, %0, %1;" : "+r"(m) : "r"(v[e] & 0x7fff7fffu));
+    }
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(m);
+    } else {
+      const float2 t = pair(m);
+      return t.x != t.x || t.x > t.y ? t.x : t.y;
+    }
+  }
+};
 template <typename T>
 __device__ __forceinline__ void store_group(T* p, bool wide, const float (&x)[16]) {
   if constexpr (sizeof(T) == 4) {
@@ -211,15 +231,16 @@ __device__ __forceinline__ void store_group(T* p, bool wide, const float (&x)[16
 }
 
 // Quantise one group.  `code` gets the sixteen codes, channel c in bits 4c;
-// returns the scale's byte.  rg = RN(1/g); `top` is max |x|, NaN or infinite where
-// an element is: |y| <= RN(top rg), since rounding is monotone.
+// returns the scale's byte.  rg = RN(1/g); the largest |x| bounds y, |y| <= RN(top rg),
+// since rounding is monotone.
 // The quotient y / s is formed as q0 = y r, q = q0 - (q0 s - y) r with r = RN(1/s):
 // the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990), and -0
 // for y = -0.  A correctly rounded quotient lies on a midpoint of two codes only if
 // the exact one does (the midpoints have three significant bits), so the
 // conversion's ties-to-even decides exactly the ties of y / s.
-__device__ __forceinline__ uint32_t quantise_group(const float (&x)[16], float top, float rg, uint64_t& code) {
-  top = __fmul_rn(top, rg);
+template <typename T>
+__device__ __forceinline__ uint32_t quantise_group(const Group<T>& x, float rg, uint64_t& code) {
+  const float top = __fmul_rn(x.top(), rg);
   const bool bad = !(top < INFINITY);
   uint32_t sb = f32_to_e4m3(fminf(__fdiv_rn(top, 6.0f), 448.0f));
   sb = sb ? sb : 1u;  // 2^-9, the smallest scale
@@ -231,7 +252,7 @@ __device__ __forceinline__ uint32_t quantise_group(const float (&x)[16], float t
     float q[8];
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-      const float2 yn = mul_pair(make_float2(x[8 * u + e], x[8 * u + e + 1]), -rg);  // -y
+      const float2 yn = mul_pair(x.at(4 * u + e / 2), -rg);  // -y
       const float2 q0 = mul_pair(yn, -r);
       const float2 v = fma_pair(fma_pair(q0, s, yn), -r, q0);
       q[e] = v.x;
@@ -275,7 +296,8 @@ struct CacheMove {
   const int32_t* start;  // first position per request (nullptr: 0)
   const int32_t* count;  // tokens per request, clamped to [0, T] (nullptr: T)
   int B, T;
-  int64_t runs;          // runs a request's tokens can touch
+  uint32_t warps;        // of one request: runs its tokens can touch x heads x 2 (x chunks)
+  Quotient by_heads;
   uint32_t* status;
 };
 
@@ -289,24 +311,22 @@ __device__ __forceinline__ bool cache_span(const CacheMove& p, int i, int64_t& n
 // One warp moves a run of one (request, head), keys or values (the write: 64
 // channels of it): lane = token pair b (tokens 2b, 2b+1) + 8 * scale group.  A pair
 // of tokens fills one byte of a value's row, so a warp holds whole rows of codes, and
-// no two warps touch the same bytes.
+// no two warps touch the same bytes.  Blocks (x, request); neighbouring warps have
+// the chunks, keys and values, and heads of one run.
 struct CacheTask {
   int i, h, chunk, is_v;
   int64_t run;
 };
 template <int C>
 __device__ __forceinline__ bool cache_task(const CacheMove& p, CacheTask& t) {
-  int64_t w = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5;
+  const uint32_t w = (blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  t.i = static_cast<int>(blockIdx.y);
   t.chunk = static_cast<int>(w % C);
-  w /= C;
-  t.is_v = static_cast<int>(w & 1);
-  w >>= 1;
-  t.h = static_cast<int>(w % p.c.heads);
-  w /= p.c.heads;
-  t.run = w % p.runs;
-  w /= p.runs;
-  t.i = static_cast<int>(w);
-  return w < p.B;
+  t.is_v = static_cast<int>(w / C & 1);
+  const uint32_t run = p.by_heads(w / (2 * C));
+  t.run = run;
+  t.h = static_cast<int>(w / (2 * C) - run * static_cast<uint32_t>(p.c.heads));
+  return w < p.warps;
 }
 
 constexpr int kMoveThreads = 128;
@@ -345,18 +365,14 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   const float* gs = t.is_v ? p.c.v_scale : p.c.k_scale;
   const float rg = gs ? __frcp_rn(gs[t.h]) : 1.0f;
   const T* src = static_cast<const T*>(rows.data) + t.i * rows.sb + t.h * rows.sh + g * kGroup;
-  float x[2][16], top[2] = {0.0f, 0.0f};
+  Group<T> x[2];
   bool in[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int tok = 2 * b + u;
     in[u] = tok >= lo && tok < hi;
-    if (in[u]) {
-      top[u] = load_group(src + (run * kRun + tok - n) * rows.st, rows.wide, x[u]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) x[u][e] = 0.0f;
-    }
+    if (in[u]) x[u].load(src + (run * kRun + tok - n) * rows.st, rows.wide);
+    else x[u].clear();
   }
   if (!dst) {
     if (p.status && t.h == 0 && t.chunk == 0 && !t.is_v && lane == 0)
@@ -366,7 +382,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   uint64_t code[2];
   uint32_t sc[2];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) sc[u] = quantise_group(x[u], top[u], rg, code[u]);
+  for (int u = 0; u < 2; ++u) sc[u] = quantise_group(x[u], rg, code[u]);
   if (!t.is_v) {
     // The lanes of neighbouring groups (lane ^ 8) trade halves, so that each stores
     // the 16 bytes of one token's chunk: the even group token 2b, the odd one 2b + 1;
