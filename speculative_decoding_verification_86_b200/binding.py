@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import os
 import re
+import struct
 
 import torch
 
@@ -58,15 +59,10 @@ class ConfArgs(ctypes.Structure):
                 ("total_budget", ctypes.c_int64)]
 
 
-class CachePages(ctypes.Structure):
-    _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
-                ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int),
-                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
-
-
-class CacheRows(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
-                ("stride_h", ctypes.c_int64)]
+# spec_cache_pages and spec_cache_rows, packed as the C compiler lays them out: a
+# third of the time of a ctypes.Structure, and passed as they are.
+_pack_pages = struct.Struct("PqPqiPP").pack  # pages, num_pages, table, table_stride, table_width, k_scale, v_scale
+_pack_rows = struct.Struct("Pqqq").pack  # data, stride_b, stride_t, stride_h
 
 
 _lib = None
@@ -128,7 +124,7 @@ def lib():
                                             ctypes.POINTER(ctypes.c_double)]
     L.spec_verify_ex2_error_bound.argtypes = []
     L.spec_verify_ex2_error_bound.restype = ctypes.c_double
-    pages_t, rows_t = ctypes.POINTER(CachePages), ctypes.POINTER(CacheRows)
+    pages_t = rows_t = ctypes.c_char_p
     L.spec_cache_page_bytes.argtypes = [_i32, _i32, _i32, ctypes.POINTER(ctypes.c_size_t)]
     L.spec_cache_init.argtypes = [ctypes.POINTER(_vp), _i32, _i32, _i32, _i32, _i32, _i32]
     L.spec_cache_destroy.argtypes = [_vp]
@@ -862,6 +858,7 @@ class BlockCache:
         self._index = dev.index
         self._page_shape = (self.heads_kv, self.page_size // 16, 18 * self.head_dim)
         h = _vp()
+        self._lib = lib()
         _check(lib().spec_cache_init(ctypes.byref(h), dev.index, self.max_batch, self.heads_q,
                                      self.heads_kv, self.head_dim, self.page_size), "spec_cache_init")
         self._h = h
@@ -929,9 +926,9 @@ class BlockCache:
         row, one = table.stride()
         if one != 1 and w > 1:
             raise ValueError("a row of the table must be contiguous")
-        return CachePages(pages.data_ptr(), n[0], table.data_ptr(), row if B > 1 else w, w,
-                          None if k_scale is None else self._vector(k_scale, torch.float32, self.heads_kv, "k_scale"),
-                          None if v_scale is None else self._vector(v_scale, torch.float32, self.heads_kv, "v_scale"))
+        return _pack_pages(pages.data_ptr(), n[0], table.data_ptr(), row if B > 1 else w, w,
+                           0 if k_scale is None else self._vector(k_scale, torch.float32, self.heads_kv, "k_scale"),
+                           0 if v_scale is None else self._vector(v_scale, torch.float32, self.heads_kv, "v_scale"))
 
     def _rows(self, t, heads, name, shape=None, dtype=None, written=False):
         if not isinstance(t, torch.Tensor):
@@ -960,7 +957,7 @@ class BlockCache:
             h = 0
         elif written and h == 0:
             raise ValueError("%s must not be an expanded tensor" % name)
-        return CacheRows(t.data_ptr(), b, r, h)
+        return _pack_rows(t.data_ptr(), b, r, h)
 
     def _vector(self, t, dtype, n, name):
         if not isinstance(t, torch.Tensor) or t.get_device() != self._index or t.dtype is not dtype:
@@ -993,8 +990,8 @@ class BlockCache:
         if cache_len is None:
             raise ValueError("cache_len is needed")
         pg = self._pages(pages, table, B, k_scale, v_scale)
-        st = lib().spec_cache_write(
-            self._h, ctypes.byref(pg), ctypes.byref(kr), ctypes.byref(vr), _CACHE_DTYPES[k.dtype],
+        st = self._lib.spec_cache_write(
+            self._h, pg, kr, vr, _CACHE_DTYPES[k.dtype],
             self._ints(cache_len, B, "cache_len"), self._ints(block_len, B, "block_len"), B, T,
             self._ints(status, B, "status"), _stream_number(stream, self.device))
         _check(st, "spec_cache_write")
@@ -1019,9 +1016,9 @@ class BlockCache:
         kr = self._rows(k, self.heads_kv, "out[0]", (B, T), written=True)
         vr = self._rows(v, self.heads_kv, "out[1]", (B, T), k.dtype, written=True)
         pg = self._pages(pages, table, B, k_scale, v_scale)
-        st = lib().spec_cache_read(
-            self._h, ctypes.byref(pg), self._ints(start, B, "start"), self._ints(count, B, "count"), B, T,
-            _CACHE_DTYPES[k.dtype], ctypes.byref(kr), ctypes.byref(vr), self._ints(status, B, "status"),
+        st = self._lib.spec_cache_read(
+            self._h, pg, self._ints(start, B, "start"), self._ints(count, B, "count"), B, T,
+            _CACHE_DTYPES[k.dtype], kr, vr, self._ints(status, B, "status"),
             _stream_number(stream, self.device))
         _check(st, "spec_cache_read")
         return out
@@ -1059,11 +1056,11 @@ class BlockCache:
                 raise ValueError("lse must be a contiguous [B, T, %d]" % self.heads_q)
             lse_ptr = lse.data_ptr()
         pg = self._pages(pages, table, B, k_scale, v_scale)
-        st = lib().spec_cache_attend(
-            self._h, ctypes.byref(pg), ctypes.byref(qr), _CACHE_DTYPES[q.dtype],
+        st = self._lib.spec_cache_attend(
+            self._h, pg, qr, _CACHE_DTYPES[q.dtype],
             self._ints(cache_len, B, "cache_len"), self._ints(block_len, B, "block_len"), B, T,
             float(self.head_dim ** -0.5 if scale is None else scale), int(bool(causal)), int(window),
-            ctypes.byref(outr), lse_ptr,
+            outr, lse_ptr,
             self._ints(status, B, "status"), _stream_number(stream, self.device))
         _check(st, "spec_cache_attend")
         return out, lse

@@ -562,6 +562,62 @@ def test_outputs_on_the_callers_stream(dev):
     assert kk.shape == (2, 4, 1, 64)
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_in_a_row_do_not_overtake_one_another(dev, captured):
+    """Kernels start while the ones before them drain: inputs that the call before has just written, pages that
+    the next call overwrites, a fork and a join of streams, memsets and copies between, all without a wait of
+    the host, give the bits of the same calls made one by one."""
+    s = make(dev, B=5, T=4, heads_q=8, heads_kv=2, d=64, page=16, lens=[900, 0, 250, 17, 1500], seed=57)
+    a = device_args(s)
+    start = a["cache_len"].clone()
+    raw = torch.from_numpy(s["raw"]).to(dev)
+    pages = raw.clone()
+    k, v, q = s["k"].to(dev), s["v"].to(dev), s["q"].to(dev)
+    kk, qq = torch.empty_like(k), torch.empty_like(q)
+    side = torch.cuda.Stream(dev)
+
+    def run(wait):
+        main = torch.cuda.current_stream(dev)
+        pages.copy_(raw)
+        a["cache_len"].copy_(start)
+        res = []
+        for n in range(4):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                torch.mul(q, 1.0 + n, out=qq)
+            torch.mul(k, 2.0 - n, out=kk)
+            s["cache"].write(kk, v, pages, **a)
+            wait()
+            main.wait_stream(side)
+            out, lse = s["cache"].attend(qq, pages, **a)
+            wait()
+            back = s["cache"].read(pages, a["table"], a["cache_len"], rows=4, k_scale=a["k_scale"], v_scale=a["v_scale"])
+            wait()
+            twice = s["cache"].attend(qq, pages, window=100, **a)
+            wait()
+            res += [out, lse, back[0], back[1], twice[0], twice[1], out.clone()]
+            a["cache_len"].add_(n % 2)  # the next block is written over this one, or one further
+        return res + [pages.clone()]
+
+    with torch.cuda.stream(torch.cuda.Stream(dev)):
+        want = run(lambda: torch.cuda.synchronize(dev))
+        torch.cuda.synchronize(dev)
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got = run(lambda: None)
+            for _ in range(3):
+                graph.replay()
+        else:
+            for _ in range(3):
+                got = run(lambda: None)
+        torch.cuda.synchronize(dev)
+    for n, (x, y) in enumerate(zip(got, want)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), n
+    if captured:
+        del graph
+
+
 def test_gpu_refusals(dev):
     c = binding.BlockCache(dev, 4, 2, 64, 16, max_batch=2)
     pages = c.alloc(4)
