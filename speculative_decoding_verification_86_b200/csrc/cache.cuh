@@ -340,6 +340,11 @@ __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Bytes in flight and issue bound it about equally: 400 instructions for a warp's
+// 2 KB.  4 x 8191 tokens, 8 heads of 128, fp16: 45 us, 3.8 TB/s (0.58 of the copy
+// bandwidth); a block of 6 tokens 8.5 us from cold memory, four dependent reads.
+// A warp has 64 channels of the run, not all 128: twice the warps while the
+// registers of one task are all it needs (48).
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   wait_for_stream();
@@ -445,6 +450,8 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   }
 }
 
+// Bound by the memory it writes: 12 requests of 1000..16384 positions, 8 heads of 128,
+// to fp16: 110 us, 5.4 TB/s (0.82 of the copy bandwidth).
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
   wait_for_stream();
