@@ -242,7 +242,10 @@ template <typename T>
 __device__ __forceinline__ uint32_t quantise_group(const Group<T>& x, float rg, uint64_t& code) {
   const float top = __fmul_rn(x.top(), rg);
   const bool bad = !(top < INFINITY);
-  uint32_t sb = f32_to_e4m3(fminf(__fdiv_rn(top, 6.0f), 448.0f));
+  // top / 6 in the same way (where it is not a normal number, or overflows on its
+  // way, the scale is the smallest, or the largest or NaN, all the same)
+  const float sixth = 1.0f / 6.0f, t0 = __fmul_rn(top, sixth);
+  uint32_t sb = f32_to_e4m3(fminf(__fmaf_rn(__fmaf_rn(-6.0f, t0, top), sixth, t0), 448.0f));
   sb = sb ? sb : 1u;  // 2^-9, the smallest scale
   const float s = h2_to_f2(e4m3x2_to_f16x2(sb)).x;
   const float r = __frcp_rn(s);
@@ -340,11 +343,10 @@ __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Bytes in flight and issue bound it about equally: 400 instructions for a warp's
-// 2 KB.  4 x 8191 tokens, 8 heads of 128, fp16: 45 us, 3.8 TB/s (0.58 of the copy
-// bandwidth); a block of 6 tokens 8.5 us from cold memory, four dependent reads.
-// A warp has 64 channels of the run, not all 128: twice the warps while the
-// registers of one task are all it needs (48).
+// Issue bounds it: 70 % of the slots, the ALU pipe 55 %, some 400 instructions for a
+// warp's 2 KB (12 or 14 blocks a SM instead of 10 change nothing).  4 x 8191 tokens,
+// 8 heads of 128, fp16: 43 us, 4.0 TB/s (0.61 of the copy bandwidth); a block of 6
+// tokens 8 us from cold memory, four dependent reads.
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   wait_for_stream();
@@ -392,8 +394,8 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
     // The lanes of neighbouring groups (lane ^ 8) trade halves, so that each stores
     // the 16 bytes of one token's chunk: the even group token 2b, the odd one 2b + 1;
     // and four lanes' scale bytes come together in the first two (lane ^ 8, ^ 16).
-    const int u = g & 1;
-    const uint64_t got = __shfl_xor_sync(0xffffffffu, code[u ^ 1], 8);
+    const bool u = g & 1;
+    const uint64_t got = __shfl_xor_sync(0xffffffffu, u ? code[0] : code[1], 8);
     const uint64_t first = u ? got : code[0], second = u ? code[1] : got;
     uint32_t four[2];
 #pragma unroll
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
 }
 
 // Bound by the memory it writes: 12 requests of 1000..16384 positions, 8 heads of 128,
-// to fp16: 110 us, 5.4 TB/s (0.82 of the copy bandwidth).
+// to fp16: 107 us, 5.5 TB/s (0.85 of the copy bandwidth).
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
   wait_for_stream();
