@@ -548,7 +548,8 @@ spec_status spec_cache_read(spec_cache_ctx* ctx, const spec_cache_pages* cache,
  * For each query head, with k~, v~ the stored values:
  *   out = sum_t softmax_t(scale * q . k~_t) v~_t,   lse = ln sum_t exp(scale * q . k~_t).
  * q and out: [B, T, heads_q, head_dim] rows of `dtype` (SPEC_BF16 or SPEC_F16);
- * out_lse [B, T, heads_q] fp32 or NULL.  Rows from L_i on stay as they were.  A
+ * out_lse [B, T, heads_q] fp32 or NULL.  out may be q (the same rows); other
+ * overlaps are not allowed.  Rows from L_i on stay as they were.  A
  * row that sees nothing (its pages are missing) gives 0 and lse = -inf.  NaN
  * and infinities: a row of q that holds one gives NaN; a NaN key gives NaN to
  * the rows that see it, a NaN value group to those rows' channels of the group;

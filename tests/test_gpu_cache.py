@@ -618,6 +618,57 @@ def test_calls_in_a_row_do_not_overtake_one_another(dev, captured):
         del graph
 
 
+@pytest.mark.parametrize("d,hq,hkv,dtype", [(64, 6, 2, torch.bfloat16), (128, 3, 3, torch.float16),
+                                            (256, 4, 1, torch.bfloat16)])
+def test_a_prompt_as_one_block(dev, d, hq, hkv, dtype):
+    """A block of many hundred tokens: dozens of row tiles, most of them cut into several CTAs' shares."""
+    s = make(dev, B=2, T=1300, heads_q=hq, heads_kv=hkv, d=d, page=64, lens=[0, 70], block=[1300, 701], dtype=dtype,
+             seed=d)
+    check_attend(s)
+    check_attend(s, window=300)
+
+
+def test_out_may_be_the_queries(dev):
+    """The outputs over the queries: whole segments, cut ones, rows that stay as they were."""
+    s = make(dev, B=3, T=6, heads_q=8, heads_kv=2, d=128, page=32, lens=[9000, 40, 0], block=[6, 3, 6], seed=23)
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    q = s["q"].to(dev)
+    s["cache"].write(s["k"].to(dev), s["v"].to(dev), pages, **a)
+    want, wl = s["cache"].attend(q, pages, **a)
+    want[1, 3:] = q[1, 3:]
+    out, lse = s["cache"].attend(q, pages, out=q, **a)
+    assert out is q and torch.equal(q, want) and torch.equal(lse, wl)
+
+
+def test_two_graphs_of_one_context_in_turn(dev):
+    """Graphs share the context's workspace; replayed one behind the other they do not disturb one another."""
+    s = make(dev, B=1, T=2, heads_q=8, heads_kv=1, d=128, page=64, lens=[20000], seed=29)
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    s["cache"].write(s["k"].to(dev), s["v"].to(dev), pages, **a)
+    qs = [s["q"].to(dev), torch.flip(s["q"], (1,)).contiguous().to(dev)]
+    want = [s["cache"].attend(q, pages, window=w, **a) for q, w in zip(qs, (0, 5000))]
+    outs = [(torch.zeros_like(qs[0]), torch.zeros_like(want[0][1])) for _ in qs]
+    torch.cuda.synchronize(dev)
+    graphs = []
+    for q, w, (out, lse) in zip(qs, (0, 5000), outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s["cache"].attend(q, pages, window=w, out=out, lse=lse, **a)
+        graphs.append(g)
+    for _ in range(10):
+        for out, lse in outs:
+            out.zero_()
+            lse.zero_()
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize(dev)
+    for (out, lse), (wo, wl) in zip(outs, want):
+        assert torch.equal(out, wo) and torch.equal(lse, wl)
+    del graphs
+
+
 def test_gpu_refusals(dev):
     c = binding.BlockCache(dev, 4, 2, 64, 16, max_batch=2)
     pages = c.alloc(4)
