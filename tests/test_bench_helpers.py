@@ -37,3 +37,21 @@ def test_profiled_traffic_reads_a_matching_summary(tmp_path, monkeypatch):
     assert bench.profiled_traffic("k_engine", "x_y") == 123.0
     assert bench.profiled_traffic("k_engine", "x_z") is None   # another kernel's code
     assert bench.profiled_traffic("k_engine", "missing") is None
+
+
+def test_superseded_summaries_are_not_read_as_the_present_kernels():
+    """A committed summary of an earlier kernel, kept for comparison, says so in its title; its traffic must
+    not be reported for the sources of today."""
+    import glob
+    kept = 0
+    for path in glob.glob(os.path.join(ROOT, "profiles", "*.md")):
+        with open(path) as f:
+            title = f.readline()
+        if "superseded" not in title:
+            continue
+        name = os.path.basename(path)[:-len(".md")]
+        for kernel in bench.KERNEL_SOURCES:
+            if name.startswith(kernel + "_"):
+                kept += 1
+                assert bench.profiled_traffic(kernel, name[len(kernel) + 1:]) is None, name
+    assert kept > 0
