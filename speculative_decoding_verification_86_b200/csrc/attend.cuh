@@ -1221,7 +1221,8 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
       if (mr == -INFINITY) mr = 0.0f;
 #pragma unroll
       for (int u = 0; u < G::kSets; ++u) {
-        const float w = l[u] != 0.0f ? ex2(sh.mout[ob][u][r] - mr) : 0.0f;
+        float w = l[u] != 0.0f ? ex2(sh.mout[ob][u][r] - mr) : 0.0f;
+        if (l[u] != l[u]) w = l[u];  // NaN counts, however far below the other set's maximum
         sh.weight[warp][u][r] = w;
         if (w != 0.0f) sum += w * l[u];
       }

@@ -726,3 +726,29 @@ def test_gpu_refusals(dev):
     with pytest.raises(binding.SpecVerifyError) as e:
         binding.BlockCache(dev, heads_q=5, heads_kv=2, head_dim=64, page_size=16)
     assert e.value.status == binding.SPEC_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bad,high", [(5, 200), (200, 5), (130, 260), (260, 130)])
+def test_a_nan_key_far_below_the_maximum_is_not_lost(dev, d, bad, high):
+    """A NaN key in one tile, and a score hundreds of powers of two above all others in the next: the first
+    tile's sums weigh nothing beside the second's, and are NaN all the same.  Enough requests that a CTA takes
+    whole segments (and some that are cut)."""
+    B, T, h, n, page = 40, 2, 8, 300, 64
+    cache = binding.BlockCache(dev, h, h, d, page, max_batch=B)
+    width = (n + T + page - 1) // page
+    pages = cache.alloc(B * width)
+    table = torch.randperm(B * width, generator=torch.Generator().manual_seed(d)).to(torch.int32).view(B, width).to(dev)
+    g = torch.Generator(device=dev).manual_seed(7)
+    k = torch.randn((B, n + T, h, d), generator=g, device=dev)
+    v = torch.randn((B, n + T, h, d), generator=g, device=dev)
+    q = torch.randn((B, T, h, d), generator=g, device=dev).bfloat16()
+    k[:, high] = 100.0 * q[:, 0].float().sign()
+    k[::2, bad, :, 3] = float("nan")  # every other request
+    zero = torch.zeros(B, dtype=torch.int32, device=dev)
+    cache.write(k, v, pages, table, zero)
+    q[:, 1] = q[:, 0]  # both rows meet the large key
+    out, lse = cache.attend(q, pages, table, zero + n, scale=1.0)
+    assert bool(out[::2].isnan().all()) and bool(lse[::2].isnan().all())
+    assert bool(out[1::2].isfinite().all()) and bool(lse[1::2].isfinite().all())
+    assert cache.errors() == 0
