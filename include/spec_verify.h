@@ -95,7 +95,8 @@ typedef enum { SPEC_MODE_DENSE = 0, SPEC_MODE_PREFIX = 1, SPEC_MODE_AUTO = 2 } s
 #define SPEC_DEV_BAD_TEMPERATURE 4u /* temperature negative, NaN, inf, in (0, 2^-100), or
                                        T > 0 with L_i > 0 but no draft logits */
 #define SPEC_DEV_BAD_PAGE 8u        /* (spec_cache_*) a page the call needs is outside [0, num_pages) */
-#define SPEC_DEV_INTERNAL 16u       /* internal consistency check failed (should not occur) */
+#define SPEC_DEV_INTERNAL 16u       /* internal consistency check failed, or a bounded wait ran
+                                       out (should not occur) */
 #define SPEC_DEV_BAD_LENGTH 32u     /* (spec_cache_*) the request's positions do not fit its table */
 
 typedef struct spec_verify_ctx spec_verify_ctx;
@@ -568,8 +569,10 @@ spec_status spec_cache_attend(spec_cache_ctx* ctx, const spec_cache_pages* cache
                               float* out_lse, uint32_t* out_status, cudaStream_t stream);
 
 /* Error word of the attention kernel since the context was created
- * (synchronises the device): non-zero = a wait inside the kernel timed out and
- * that launch's outputs are not to be used. */
+ * (synchronises the device): non-zero = a wait inside the kernel ran out (60 ms at
+ * least, 6 s at most; a healthy launch waits for microseconds).  Such a launch ends by
+ * itself, its outputs are not to be used, and out_status says SPEC_DEV_INTERNAL for
+ * every request of its batch; the context stays usable. */
 spec_status spec_cache_errors(spec_cache_ctx* ctx, uint32_t* out);
 
 const char* spec_status_string(spec_status s);

@@ -842,7 +842,8 @@ class BlockCache:
     rest (a failed request's -1 leaves it as it was).
 
     ``status`` [B] int32, where given, gets DEV_BAD_LENGTH and DEV_BAD_PAGE
-    OR-ed in; the caller zeroes it."""
+    OR-ed in (and DEV_INTERNAL for the whole batch where an attention gave up);
+    the caller zeroes it."""
 
     def __init__(self, device=None, heads_q=32, heads_kv=8, head_dim=128, page_size=64, max_batch=1024):
         dev = torch.device("cuda") if device is None else torch.device(device)

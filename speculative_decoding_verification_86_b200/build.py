@@ -33,11 +33,13 @@ def sources():
                   + [os.path.join(INCLUDE, "spec_verify.h")])
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+def build(force: bool = False, verbose: bool = False, extra_flags=(), out: str = LIB) -> str:
+    """Build the library unless it is newer than its sources; ``out`` names another file, for a build with
+    other ``extra_flags``."""
     newest = max(os.path.getmtime(s) for s in sources())
-    if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest and not extra_flags:
-        return LIB
-    tmp = LIB + ".tmp.%d" % os.getpid()
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= newest and not extra_flags:
+        return out
+    tmp = out + ".tmp.%d" % os.getpid()
     units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     objects = ["%s.%s.o" % (tmp, os.path.basename(u)) for u in units]
     cmds = [[_nvcc(), *NVCC_FLAGS, *extra_flags, "-I", INCLUDE, "-I", CSRC, "-c", u, "-o", o]
@@ -57,8 +59,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         for o in objects:
             if os.path.exists(o):
                 os.remove(o)
-    os.replace(tmp, LIB)
-    return LIB
+    os.replace(tmp, out)
+    return out
 
 
 if __name__ == "__main__":

@@ -29,8 +29,9 @@
 //                 unnormalised fp32 partials, which k_attend_join adds in the
 //                 order of the CTAs.
 // Every wait is bounded (warp_wait): a role whose wait runs out leaves, those that
-// wait for it follow, the error word is raised, copies and products in flight are
-// awaited and tensor memory is freed.
+// wait for it follow, copies and products in flight are awaited and tensor memory is
+// freed.  The error word and SPEC_DEV_INTERNAL of the batch's requests are raised,
+// and rows that such a CTA has a part of are not joined.
 //
 // What bounds it: instruction issue.  A tile of 128 tokens (18 KB at D = 128) costs
 // its SM 3000 (8 query rows) to 4000 (24) warp instructions, about half of them to
@@ -73,6 +74,7 @@ struct AttendParams {
   float2* part_l;  // [2 grid][NP]: (reference exponent, sum)
   struct AttendCut* cuts;  // [grid]
   unsigned* error;
+  int* lost;  // [grid]: this CTA gave up
 };
 
 // A segment that is cut at the start of a CTA's share: which rows, and which
@@ -458,14 +460,22 @@ struct AttendShares {
 };
 
 // All lanes of a warp leave a wait together; false where the phase did not complete
-// within kWaitTries tries.  A try sleeps for up to 2700 cycles (measured), so that
-// is 1.5 s at most.  Nothing more happens here, since this stands at some thirty
-// places: a role that gives up returns false, which raises the error word, and
-// the roles that wait for it give up in their turn.
-constexpr uint32_t kWaitTries = 1u << 20;
+// within kWaitTries tries.  A try sleeps for up to 2700 cycles (measured) but may
+// return at once, some 30 cycles with the loop, so this is 60 ms at least and 6 s at
+// most; a healthy launch waits 40 ms at most, for a share of all the tokens that fit
+// 180 GB.  Looking at the clock here, or a limit that the compiler does not know, cost
+// a sixth to a third of the kernel's time (256 requests 215 -> 250..290 us): this
+// stands at some thirty places.  A role that gives up returns false, and the roles
+// that wait for it give up in their turn.
+#ifndef SV_WAIT_TRIES
+#define SV_WAIT_TRIES (1u << 22)
+#endif
+constexpr uint32_t kWaitTries = SV_WAIT_TRIES;
+constexpr uint32_t kDrainTries = 1u << 22;  // what is in flight lands whatever the roles do
+template <uint32_t TRIES = kWaitTries>
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (uint32_t left = kWaitTries; left; --left)
+  for (uint32_t left = TRIES; left; --left)
     if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
   return false;
 }
@@ -567,13 +577,18 @@ __device__ __forceinline__ bool attend_plan(const AttendParams& p, AttendShared<
   return ok;
 }
 
-// The roles' view of the ring: the segment, or nullptr at the share's end (or
-// where the wait for it ran out; the plan's own wait tells).
+// The roles' view of the ring: the segment, or nullptr at the share's end and where
+// the wait for it ran out (seg_ended tells which).
 template <class SH>
 __device__ __forceinline__ const AttendSeg* seg_wait(SH& sh, uint32_t ns) {
   const int slot = static_cast<int>(ns % kSegs);
   if (!warp_wait(&sh.segfull[slot], (ns / kSegs) & 1u)) return nullptr;
   return sh.seg[slot].rows > 0 ? &sh.seg[slot] : nullptr;
+}
+template <class SH>
+__device__ __forceinline__ bool seg_ended(SH& sh, uint32_t ns) {
+  const int slot = static_cast<int>(ns % kSegs);
+  return __all_sync(0xffffffffu, mbar_test(&sh.segfull[slot], (ns / kSegs) & 1u)) && sh.seg[slot].rows == 0;
 }
 template <class SH>
 __device__ __forceinline__ void seg_done(SH& sh, uint32_t ns) {
@@ -588,7 +603,8 @@ __device__ __forceinline__ bool attend_producer(const AttendParams& p, AttendSha
   uint32_t g = 0;
   bool ok = true;
   const AttendSeg* sp;
-  for (uint32_t ns = 0; ok && (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+  uint32_t ns = 0;
+  for (; ok && (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
     const int i = sp->i, h = sp->h, t1 = sp->t1, hi = sp->hi;
     const int64_t run0 = sp->run0;
     // a lane looks up one run; 32 runs are four tiles
@@ -624,10 +640,11 @@ __device__ __forceinline__ bool attend_producer(const AttendParams& p, AttendSha
     }
     seg_done(sh, ns);
   }
+  ok = ok && seg_ended(sh, ns);
   // the copies this warp issued land before the CTA's memory goes away
 #pragma unroll 1
   for (uint32_t e = g > G::kStages ? g - G::kStages : 0; e < g; ++e)
-    ok = warp_wait(&sh.full[e % G::kStages], (e / G::kStages) & 1u) && ok;
+    ok = warp_wait<kDrainTries>(&sh.full[e % G::kStages], (e / G::kStages) & 1u) && ok;
   return ok;
 }
 
@@ -641,7 +658,8 @@ __device__ __forceinline__ bool attend_keys(const AttendParams& p, AttendShared<
   const uint32_t tmem = sh.tmem + (static_cast<uint32_t>(warp * 32) << 16) + G::kTmemK;
   uint32_t g = 0;
   const AttendSeg* sp;
-  for (uint32_t ns = 0; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+  uint32_t ns = 0;
+  for (; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
     const uint32_t end = g + static_cast<uint32_t>(sp->t1 - sp->t0);
 #pragma unroll 1
     for (; g != end; ++g) {
@@ -688,7 +706,7 @@ __device__ __forceinline__ bool attend_keys(const AttendParams& p, AttendShared<
     }
     seg_done(sh, ns);
   }
-  return true;
+  return seg_ended(sh, ns);
 }
 
 // 0xff in the bytes that are NaN as e4m3.
@@ -724,7 +742,8 @@ __device__ __forceinline__ bool attend_values(const AttendParams& p, AttendShare
   scratch += warp * 512 * G::kMT;
   uint32_t g = 0;
   const AttendSeg* sp;
-  for (uint32_t ns = 0; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+  uint32_t ns = 0;
+  for (; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
     const int t1 = sp->t1, lo = sp->lo, hi = sp->hi;
 #pragma unroll 1
     for (int t = sp->t0; t < t1; ++t, ++g) {
@@ -811,7 +830,7 @@ __device__ __forceinline__ bool attend_values(const AttendParams& p, AttendShare
     }
     seg_done(sh, ns);
   }
-  return true;
+  return seg_ended(sh, ns);
 }
 
 // One lane issues; the warp stays together.  S of tile g goes before O of tile
@@ -881,9 +900,10 @@ __device__ __forceinline__ bool attend_mma(const AttendParams& p, AttendShared<D
       idx = 0;
     }
   }
+  ok = ok && seg_ended(sh, ns);
   // what was issued completes before tensor memory is released
   umma_commit_if(&sh.drain, el);
-  return warp_wait(&sh.drain, 0) && ok;
+  return warp_wait<kDrainTries>(&sh.drain, 0) && ok;
 }
 
 // Which of a thread's N rows see the token `at` (counted from the segment's first run).
@@ -967,8 +987,10 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
   const uint32_t prow = p_smem + tok * 32, pflip = (tok & 4) << 2;
   uint32_t g = 0;
   bool ok = true;
-  const AttendSeg* sp;
-  for (uint32_t ns = 0; (sp = seg_wait(sh, ns)) != nullptr; ++ns) {
+  for (uint32_t ns = 0;; ++ns) {
+    const AttendSeg* sp = seg_wait(sh, ns);
+    // together: the group's barriers wait for all of it
+    if (group_any(id, sp == nullptr)) return ok && seg_ended(sh, ns);
     const int rows = sp->rows, t1 = sp->t1, full_lo = sp->full_lo, full_hi = sp->full_hi;
     const uint32_t qb = ns & 1u, ob = ns % G::kOB;
     const int slot = static_cast<int>(ns % kSegs);
@@ -1093,7 +1115,6 @@ __device__ __forceinline__ bool attend_softmax(const AttendParams& p, AttendShar
     }
     seg_done(sh, ns);
   }
-  return ok;
 }
 
 // Q of a segment: rows to fp16 times a power of two that brings the row's
@@ -1193,6 +1214,7 @@ __device__ __forceinline__ bool attend_epilogue(const AttendParams& p, AttendSha
   for (uint32_t na = 0; more; ++na) {
     const AttendSeg* sp = seg_wait(sh, na);
     more = sp != nullptr;
+    if (!more && !seg_ended(sh, na)) return false;
     if (more) {
       ahead = *sp;
       attend_load_q<D, NP>(p, sh, ahead, na, q_smem);
@@ -1375,6 +1397,7 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   }
   // what came before in the stream is complete: from here on memory is read
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x == 0) p.lost[blockIdx.x] = 0;
   // this CTA's share of the units
   long long per_head = 0, mine = 0, total = 0, before = 0;
   auto scan = [&](int i0, bool tell) {
@@ -1435,7 +1458,10 @@ __global__ void __launch_bounds__(AttendGeo<D, NP>::kThreads, 1) k_attend(const 
   } else {
     ok = attend_softmax<D, NP>(p, sh, p_smem);
   }
-  if (!ok) atomicOr(p.error, 1u);
+  if (!ok) {
+    atomicOr(p.error, 1u);
+    p.lost[blockIdx.x] = 1;
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == G::kWarpMma) {
@@ -1455,11 +1481,11 @@ constexpr int kJoinMaxParts = 256;
 // attention.  Joining in the CTA that finishes last would save a launch, but one
 // CTA would then read all the parts of a long context (19 x 24 rows x 128 channels
 // for one of 100,003 positions).
-// Join the parts of the segments that were cut: block (x, y) takes the rows
-// [2 y, 2 y + 2) of the segment that CTA x + 1's share starts inside of, where
-// that is the segment's first cut.  Parts are added in the order of the CTAs (at
-// D = 64 in two interleaved halves, then their sum), so the result does not depend
-// on timing.
+// Join the parts of the segments that were cut: block (x, y), x > 0, takes the rows
+// [2 y, 2 y + 2) of the segment that CTA x's share starts inside of, where
+// that is the segment's first cut; block (0, 0) looks for CTAs that gave up.  Parts
+// are added in the order of the CTAs (at D = 64 in two interleaved halves, then their
+// sum), so the result does not depend on timing.
 template <int D, int NP>
 __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_constant__ AttendParams p) {
   constexpr int kThreads = join_threads(D);
@@ -1469,7 +1495,15 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
   __shared__ float sum[kJoinRows][kThreads];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const AttendCut& cut = p.cuts[blockIdx.x + 1];
+  if (blockIdx.x == 0) {
+    if (blockIdx.y > 0 || !p.status) return;
+    bool gone = false;
+    for (int c = threadIdx.x; c < static_cast<int>(gridDim.x); c += kThreads) gone |= __ldcg(p.lost + c) != 0;
+    if (__syncthreads_or(gone))
+      for (int i = threadIdx.x; i < p.B; i += kThreads) atomicOr(p.status + i, kDevInternal);
+    return;
+  }
+  const AttendCut& cut = p.cuts[blockIdx.x];
   const int last = __ldcg(&cut.last);
   if (last < 0) return;
   const int i = __ldcg(&cut.i), h = __ldcg(&cut.h), row0 = __ldcg(&cut.row0), rows = __ldcg(&cut.rows),
@@ -1481,6 +1515,7 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
   auto slot = [&](int e) { return 2 * (first + e) + (e == 0 ? 1 : 0); };
   const int nr = min(kJoinRows, rows - r0);
   const float gv = p.c.v_scale ? p.c.v_scale[h] : 1.0f;
+  int gone = 0;  // a part's CTA gave up
   if (warp < nr) {
     const int r = r0 + warp;
     constexpr int kPer = kJoinMaxParts / 32;
@@ -1490,7 +1525,9 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
     for (int u = 0; u < kPer; ++u) {
       const int e = lane + 32 * u;
       v[u] = e < parts ? __ldcg(p.part_l + slot(e) * NP + r) : make_float2(0.0f, 0.0f);
+      gone |= e < parts ? __ldcg(p.lost + first + e) : 0;
     }
+    gone = __any_sync(0xffffffffu, gone);
 #pragma unroll
     for (int u = 0; u < kPer; ++u)
       if (v[u].y != 0.0f) m = fmaxf(m, v[u].x);
@@ -1508,14 +1545,14 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
       inv[warp] = l == 0.0f ? 0.0f : __frcp_rn(l);
-      if (p.lse) {
+      if (p.lse && !gone) {
         const int row = row0 + r, j = of_group(p, row), hq = h * p.group + row - j * p.group;
         p.lse[(static_cast<int64_t>(i) * p.T + j) * p.heads_q + hq] =
             l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       }
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(gone)) return;
   const int ch = threadIdx.x % D, part = threadIdx.x / D;
   float acc[kJoinRows] = {};
 #pragma unroll 8

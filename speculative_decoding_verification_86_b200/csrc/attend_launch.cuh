@@ -41,9 +41,8 @@ struct AttendRun {
     *started = true;
     using G = AttendGeo<SV_ATTEND_WIDTH, NP>;
     return launch_waiting(k_attend<SV_ATTEND_WIDTH, NP>, dim3(num_sms), G::kThreads, G::kSmemBytes, stream, p) &&
-           (num_sms == 1 || launch_waiting(k_attend_join<SV_ATTEND_WIDTH, NP>,
-                                           dim3(num_sms - 1, (p.rp + kJoinRows - 1) / kJoinRows),
-                                           join_threads(SV_ATTEND_WIDTH), 0, stream, p));
+           launch_waiting(k_attend_join<SV_ATTEND_WIDTH, NP>, dim3(num_sms, (p.rp + kJoinRows - 1) / kJoinRows),
+                          join_threads(SV_ATTEND_WIDTH), 0, stream, p);
   }
 };
 }  // namespace

@@ -21,6 +21,7 @@ struct spec_cache_ctx {
   float2* part_l = nullptr;
   sv::AttendCut* cuts = nullptr;
   unsigned* error = nullptr;
+  int* lost = nullptr;
 };
 
 namespace {
@@ -180,7 +181,8 @@ spec_status spec_cache_init(spec_cache_ctx** out, int device, int max_batch, int
   const size_t rows = 2 * static_cast<size_t>(c->num_sms) * max_rows(head_dim);
   const size_t o_l = align_up(rows * head_dim * sizeof(float), 256);
   const size_t o_cuts = align_up(o_l + rows * sizeof(float2), 256);
-  const size_t o_err = align_up(o_cuts + c->num_sms * sizeof(sv::AttendCut), 256);
+  const size_t o_lost = align_up(o_cuts + c->num_sms * sizeof(sv::AttendCut), 256);
+  const size_t o_err = align_up(o_lost + c->num_sms * sizeof(int), 256);
   if (c->num_sms > sv::kJoinMaxParts || cudaMalloc(&c->ws, o_err + 256) != cudaSuccess) {
     cudaGetLastError();
     delete c;
@@ -190,6 +192,7 @@ spec_status spec_cache_init(spec_cache_ctx** out, int device, int max_batch, int
   c->part_o = reinterpret_cast<float*>(b);
   c->part_l = reinterpret_cast<float2*>(b + o_l);
   c->cuts = reinterpret_cast<sv::AttendCut*>(b + o_cuts);
+  c->lost = reinterpret_cast<int*>(b + o_lost);
   c->error = reinterpret_cast<unsigned*>(b + o_err);
   if (cudaMemset(c->error, 0, 256) != cudaSuccess || !prepare_attend(head_dim)) {
     cudaFree(c->ws);
@@ -268,6 +271,7 @@ spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
   p.part_l = c->part_l;
   p.cuts = c->cuts;
   p.error = c->error;
+  p.lost = c->lost;
   DeviceGuard g(c->device);
   if (!g.ok) return SPEC_ERR_CUDA;
   cudaGetLastError();

@@ -18,6 +18,7 @@
 namespace sv {
 
 constexpr uint32_t kDevBadPage = 8u;
+constexpr uint32_t kDevInternal = 16u;
 constexpr uint32_t kDevBadLength = 32u;
 constexpr int kRun = 16;    // tokens of a run
 constexpr int kGroup = 16;  // channels that share a scale

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import cache_reference as ref
-from speculative_decoding_verification_86_b200 import binding
+from speculative_decoding_verification_86_b200 import binding, build
 
 pytestmark = pytest.mark.gpu
 
@@ -752,3 +752,48 @@ def test_a_nan_key_far_below_the_maximum_is_not_lost(dev, d, bad, high):
     assert bool(out[::2].isnan().all()) and bool(lse[::2].isnan().all())
     assert bool(out[1::2].isfinite().all()) and bool(lse[1::2].isfinite().all())
     assert cache.errors() == 0
+
+
+@pytest.fixture(scope="module")
+def hasty(tmp_path_factory):
+    """The library with waits of one try (1.4 us at most) instead of 2^22."""
+    return build.build(extra_flags=["-DSV_WAIT_TRIES=1"], out=str(tmp_path_factory.mktemp("hasty") / "libhasty.so"))
+
+
+@pytest.mark.parametrize("d,hq,hkv,T,lens", [
+    (128, 32, 8, 6, [30000, 70, 0, 3000]),  # two softmax sets, cut segments and whole ones
+    (64, 32, 8, 12, [30000, 400]),          # one set of two warpgroups
+    (256, 48, 8, 4, [20000, 100, 2000]),    # one set of one
+    (256, 8, 4, 3, [700] * 40),             # two sets, one K and one O buffer
+    (64, 32, 8, 1, [300] * 400),            # more segments a CTA than the ring of plans holds
+])
+def test_a_wait_that_runs_out_ends_the_launch_and_says_so(dev, hasty, monkeypatch, d, hq, hkv, T, lens):
+    """With less patience than the memory's latency, or a segment, needs, the roles leave one after another:
+    the call returns, the requests' status and the error word say it, and what runs next is as ever."""
+    B, page = len(lens), 64
+    width = (max(lens) + T + page - 1) // page
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    table = torch.randperm(B * width, generator=torch.Generator().manual_seed(d)).to(torch.int32).view(B, width).to(dev)
+    g = torch.Generator(device=dev).manual_seed(5)
+    k = torch.randn((B, max(lens) + T, hkv, d), generator=g, device=dev, dtype=torch.bfloat16)
+    q = torch.randn((B, T, hq, d), generator=g, device=dev, dtype=torch.bfloat16)
+    with binding.BlockCache(dev, hq, hkv, d, page, max_batch=B) as cache:
+        pages = cache.alloc(B * width)
+        status = torch.zeros(B, dtype=torch.int32, device=dev)
+        cache.write(k, k.flip(1), pages, table, torch.zeros_like(n), block_len=n + T)
+        want, wl = cache.attend(q, pages, table, n, status=status)
+        assert cache.errors() == 0 and not bool(status.any())
+        with monkeypatch.context() as m:
+            m.setattr(binding, "LIB_PATH", hasty)
+            m.setattr(binding, "_lib", None)
+            with binding.BlockCache(dev, hq, hkv, d, page, max_batch=B) as other:
+                for _ in range(20):
+                    status.zero_()
+                    other.attend(q, pages, table, n, status=status)
+                    other.attend(q, pages, table, n)
+                    torch.cuda.synchronize(dev)
+                    assert status.tolist() == [binding.DEV_INTERNAL] * B and other.errors() != 0
+        status.zero_()
+        out, lse = cache.attend(q, pages, table, n, status=status)
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        assert cache.errors() == 0 and not bool(status.any())
