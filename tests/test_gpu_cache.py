@@ -797,3 +797,62 @@ def test_a_wait_that_runs_out_ends_the_launch_and_says_so(dev, hasty, monkeypatc
         out, lse = cache.attend(q, pages, table, n, status=status)
         assert torch.equal(out, want) and torch.equal(lse, wl)
         assert cache.errors() == 0 and not bool(status.any())
+
+
+@pytest.mark.parametrize("group,T", [(1, 1), (8, 1), (3, 3), (8, 2), (17, 1), (8, 3), (5, 5), (8, 4), (11, 3), (8, 6),
+                                     (7, 7), (8, 8)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_every_count_of_rows_that_changes_the_kernel(dev, d, group, T):
+    """1, 8, 9, 16, 17, 24, 25, 32, 33, 48, 49 and 64 rows at every width: the first and the last count of rows
+    of each instance of the attention (width 256 splits what is above 32)."""
+    s = make(dev, B=2, T=T, heads_q=group, heads_kv=1, d=d, page=32, lens=[290, 17], block=[T, (T + 1) // 2],
+             seed=group * T + d)
+    check_attend(s)
+    check_attend(s, window=70)
+
+
+def crowd(s, copies, **how):
+    """The requests of s among `copies` more that read the first one's pages: enough work that a CTA takes
+    whole segments, where the few of s alone would be cut into the CTAs' shares."""
+    dev, a = s["dev"], device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    s["cache"].write(s["k"].to(dev), s["v"].to(dev), pages, **a)
+    raw = ref.write(s["raw"], s["page"], s["table"], s["lens"], s["k"], s["v"], s["block"], s["ks"], s["vs"])
+    B, T, hq, d = s["q"].shape
+    first = torch.zeros(B + copies, dtype=torch.long)
+    first[copies // 2:copies // 2 + B] = torch.arange(B)  # not at an end
+    q = s["q"][first].contiguous()
+    hkv = s["k"].shape[2]
+    a["table"], a["cache_len"] = a["table"][first.to(dev)].contiguous(), a["cache_len"][first.to(dev)].contiguous()
+    if a["block_len"] is not None:
+        a["block_len"] = a["block_len"][first.to(dev)].contiguous()
+    with binding.BlockCache(dev, hq, hkv, d, s["page"], max_batch=B + copies) as cache:
+        out, lse = cache.attend(q.to(dev), pages, **a, **how)
+        assert cache.errors() == 0
+    mine = slice(copies // 2, copies // 2 + B)
+    compare(s, raw, s["q"], out[mine], lse[mine], how.get("causal", True), how.get("window", 0))
+
+
+@pytest.mark.parametrize("d,hq,hkv,T", [(64, 4, 2, 6), (64, 16, 2, 5), (128, 8, 2, 6), (128, 12, 2, 10),
+                                        (256, 4, 2, 4), (256, 12, 2, 4), (256, 8, 2, 8)])
+@pytest.mark.parametrize("copies", [0, 120])
+def test_nan_tokens_in_every_form_of_the_kernel(dev, d, hq, hkv, T, copies):
+    """NaN keys, value groups and queries at every width, with one and two softmax sets, in segments that are
+    cut between CTAs (few requests) and in whole ones (many)."""
+    s = make(dev, B=2, T=T, heads_q=hq, heads_kv=hkv, d=d, page=16, lens=[300, 9], seed=d + T)
+    s["k"][0, 3, 0, 17] = float("nan")
+    s["v"][0, 2, 1, 40] = float("inf")
+    s["v"][0, 1, 0, d - 1] = float("nan")
+    s["v"][1, 2, 0, 3] = float("nan")
+    s["v"][1, 3, 1, d // 2] = float("-inf")
+    # and one in the context, which whole rows of tiles before and behind it do not see with a window
+    ctx_k = torch.randn((1, 1, hkv, d), generator=torch.Generator().manual_seed(1))
+    ctx_v = ctx_k.clone()
+    ctx_v[0, 0, 1, d - 20] = float("nan")
+    s["raw"] = ref.write(s["raw"], 16, s["table"][:1], [150], ctx_k, ctx_v, None, s["ks"], s["vs"])
+    q = s["q"]
+    q[0, 1, 1, 5] = float("inf")
+    q[1, 0, 0, 5] = float("nan")
+    crowd(s, copies)
+    crowd(s, copies, window=2)
+    crowd(s, copies, causal=False, window=152)
