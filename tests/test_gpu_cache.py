@@ -856,3 +856,77 @@ def test_nan_tokens_in_every_form_of_the_kernel(dev, d, hq, hkv, T, copies):
     crowd(s, copies)
     crowd(s, copies, window=2)
     crowd(s, copies, causal=False, window=152)
+
+
+@pytest.mark.parametrize("d,hq,hkv,T,lens", [
+    (64, 4, 1, 2, [100003]),
+    (64, 12, 1, 3, [40007, 0, 25003]),
+    (128, 8, 2, 6, [30011]),
+    (128, 8, 4, 1, [20000, 129, 20001]),
+    (128, 40, 2, 2, [9999, 30000]),
+    (256, 4, 2, 2, [12345, 4000]),
+    (256, 12, 1, 2, [30011]),
+])
+@pytest.mark.parametrize("window", [0, 5000])
+def test_every_token_counts_once_wherever_a_context_is_cut(dev, d, hq, hkv, T, lens, window):
+    """Equal scores and a value of one channel for each token: a row's output is a count of its tokens by
+    channel, its lse the logarithm of their number.  All sums are of integers below 2^24, so a token lost or
+    counted twice at the border of a tile, a page or a share changes a count of a few hundred by one, and lse
+    by 1 / N, far beyond the rounding of the results.  Two assignments of tokens to channels."""
+    B, page = len(lens), 64
+    width = (max(lens) + T + page - 1) // page
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    table = torch.randperm(B * width, generator=torch.Generator().manual_seed(d)).to(torch.int32).view(B, width).to(dev)
+    t = torch.arange(max(lens) + T, device=dev)
+    k = torch.randn((1, 1, hkv, d), device=dev, dtype=torch.bfloat16).expand(B, len(t), hkv, d)
+    q = torch.zeros((B, T, hq, d), dtype=torch.float16, device=dev)
+    with binding.BlockCache(dev, hq, hkv, d, page, max_batch=B) as cache:
+        pages = cache.alloc(B * width)
+        for channel in (t % d, t // d % d):
+            v = (6.0 * torch.nn.functional.one_hot(channel, d)).bfloat16()  # 6 is a code, its scale 1
+            cache.write(k, v[None, :, None].expand(B, len(t), hkv, d), pages, table, torch.zeros_like(n), block_len=n + T)
+            out, lse = cache.attend(q, pages, table, n, window=window)
+            assert cache.errors() == 0
+            for i in range(B):
+                for j in range(T):
+                    end = lens[i] + j + 1
+                    first = max(0, end - window) if window else 0
+                    want = 6.0 * torch.bincount(channel[first:end], minlength=d).double() / (end - first)
+                    # to fp16, and three roundings of the normalisation in fp32
+                    off = (out[i, j].double() - want).abs() - want * (2.0 ** -11 + 2.0 ** -20)
+                    assert float(off.max()) <= 0, (i, j)
+                    # lg2 to 2^-22 absolute, a sum of at most 25 and a product rounded
+                    assert float((lse[i, j].double() - math.log(end - first)).abs().max()) <= 2.0 ** -22 + 30 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("d,hq,T", [(64, 8, 1), (64, 32, 2), (128, 8, 3), (128, 32, 1), (128, 16, 4), (256, 8, 1),
+                                    (256, 32, 1)])
+def test_a_key_is_found_at_every_border(dev, d, hq, T):
+    """Keys with one channel each at the borders of tiles, runs and shares of a long context, and rows that ask
+    for one of them: each row's output is that token's value, its lse that score."""
+    n, page, block = 30011, 16, hq * T
+    rng = np.random.RandomState(d + hq)
+    ends = [0, 1, n - 1, n - 2]
+    spots = torch.tensor(ends + [128 * e + o for e in rng.permutation(np.arange(1, n // 128))[:2 * d] for o in (-1, 0)],
+                         device=dev)
+    width = (n + T + page - 1) // page
+    table = torch.randperm(width, generator=torch.Generator().manual_seed(d)).to(torch.int32).view(1, width).to(dev)
+    length = torch.tensor([n], dtype=torch.int32, device=dev)
+    v = torch.randn((1, n + T, 1, d), generator=torch.Generator(device=dev).manual_seed(2), device=dev)
+    with binding.BlockCache(dev, hq, 1, d, page, max_batch=1) as cache:
+        pages = cache.alloc(width)
+        for at in range(0, len(spots) // d * d, d):
+            mine = spots[at:at + d]  # one channel each
+            k = torch.zeros((1, n + T, 1, d), device=dev)
+            k[0, mine, 0, torch.arange(d, device=dev)] = 96.0
+            cache.write(k, v, pages, table, torch.zeros_like(length))
+            _, vv = cache.read(pages, table, rows=n + T, dtype=torch.float32)
+            for c in range(0, d, block):
+                ask = (c + torch.arange(block, device=dev)) % d
+                q = torch.nn.functional.one_hot(ask, d).view(1, T, hq, d).half().contiguous()
+                out, lse = cache.attend(q, pages, table, length, scale=1.0)
+                # 30,000 tokens of score 0 weigh exp(-96) each: nothing
+                want = vv[0, mine[ask], 0].view(T, hq, d).double()
+                assert float(((out[0].double() - want).abs() - want.abs() * (2.0 ** -11 + 2.0 ** -20)).max()) <= 2.0 ** -25
+                assert float((lse - 96.0).abs().max()) <= 96 * 2.0 ** -22
+        assert cache.errors() == 0
