@@ -447,13 +447,16 @@ spec_status spec_lmhead_errors(spec_lmhead_ctx* ctx, uint32_t* out);
  * The values.  An element is an e2m1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and their
  * negatives); 16 neighbouring channels of a token share one e4m3 scale s, and a
  * key/value head has one fp32 calibration scale g (k_scale, v_scale; 1 where
- * NULL; it must be positive and finite).  Storing x:
+ * NULL; it must be a positive normal number).  Storing x:
  *   y = x * (1/g) in fp32, 1/g rounded to fp32;
  *   s = max(e4m3(min(max|y| / 6, 448)), 2^-9), over the 16 channels, the
  *       quotient in fp32, to nearest, ties to even;
  *   c = the e2m1 value nearest to y / s, ties to the even code, at most 6 in
  *       magnitude, with y's sign.
- * A group that holds a NaN or an infinity stores s = NaN, and reads as NaN.
+ * A group in which some y is a NaN or an infinity stores s = NaN and codes 0, and
+ * reads as NaN: one that holds such an x, and one with an x so large that y
+ * overflows fp32 (|x| of about 2^128 g or more).  Below that, what passes 6 * 448 * g is
+ * stored as 6 * 448 * g.
  * The stored value is c * s * g; c * s is exact in fp16, and that is what the
  * attention multiplies with.
  *

@@ -233,7 +233,7 @@ __device__ __forceinline__ void store_group(T* p, bool wide, const float (&x)[16
 
 // Quantise one group.  `code` gets the sixteen codes, channel c in bits 4c;
 // returns the scale's byte.  rg = RN(1/g); the largest |x| bounds y, |y| <= RN(top rg),
-// since rounding is monotone.
+// since rounding is monotone; where that is not finite (some y is not), the group is NaN.
 // The quotient y / s is formed as q0 = y r, q = q0 - (q0 s - y) r with r = RN(1/s):
 // the correctly rounded quotient (Markstein, IBM J. Res. Dev. 34, 1990), and -0
 // for y = -0.  A correctly rounded quotient lies on a midpoint of two codes only if

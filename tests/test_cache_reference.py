@@ -109,3 +109,16 @@ def test_null_cache_context_and_bad_geometry_are_rejected(L):
 def test_cache_needs_a_cuda_device():
     with pytest.raises(ValueError):
         binding.BlockCache("cpu", 8, 8, 128, 64)
+
+
+def test_values_that_overflow_behind_the_calibration_scale_are_nan():
+    """y = x / g decides: the largest finite y saturates, one that overflows makes the group NaN."""
+    big = np.float32(3e38)
+    x = np.zeros(16, np.float32)
+    x[3], x[4] = -big, 1.0
+    c, s = ref.quantise(x, 1.0)
+    assert s.tolist() == [0x7e] and c[3] == 15 and c[4] == 0  # -6 * 448
+    c, s = ref.quantise(x, 0.5)
+    assert s.tolist() == [0x7f] and not c.any()
+    x[3] = np.inf
+    assert ref.quantise(x, 4.0)[1].tolist() == [0x7f]

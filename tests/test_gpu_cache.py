@@ -930,3 +930,31 @@ def test_a_key_is_found_at_every_border(dev, d, hq, T):
                 assert float(((out[0].double() - want).abs() - want.abs() * (2.0 ** -11 + 2.0 ** -20)).max()) <= 2.0 ** -25
                 assert float((lse - 96.0).abs().max()) <= 96 * 2.0 ** -22
         assert cache.errors() == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_write_saturates_up_to_the_largest_finite_quotient(dev, dtype):
+    """Around the x whose y = x / g is the largest finite number: below it +-6 * 448, above it a NaN group."""
+    d, page = 64, 16
+    g = np.array([0.25, 0.3], np.float32)
+    top = np.float32(np.finfo(np.float32).max)
+    x = torch.zeros((1, 16, 2, d), dtype=dtype)
+    for h in range(2):
+        edge = torch.tensor(float(top) * float(g[h])).to(dtype)
+        for j in range(16):  # eight steps of the type on either side
+            bits = edge.view(torch.int32 if dtype == torch.float32 else torch.int16) + (j - 8)
+            x[0, j, h, 7] = bits.view(dtype)
+            x[0, j, h, 8:12] = -bits.view(dtype)
+            x[0, j, h, 33] = bits.view(dtype) / 2
+            x[0, j, h, 34] = 1e-3
+    table = np.zeros((1, 1), np.int32)
+    raw = np.zeros((1, 2, 1, 18 * d), np.uint8)
+    with binding.BlockCache(dev, 2, 2, d, page, max_batch=1) as c:
+        pages = torch.from_numpy(raw).to(dev)
+        gd = on(dev, g, torch.float32)
+        c.write(x.to(dev), x.flip(1).to(dev), pages, on(dev, table), on(dev, [0]), k_scale=gd, v_scale=gd)
+        want = ref.write(raw, page, table, [0], x, x.flip(1), None, g, g)
+        assert np.array_equal(pages.cpu().numpy(), want)
+        k, _ = c.read(pages, on(dev, table), rows=16, dtype=torch.float32, k_scale=gd)
+    assert bool(k[0, 0, :, 7].isfinite().all()) and bool(k[0, 15, :, 7].isnan().all())
+    assert bool(k[0, :, :, 32:48].isfinite().all())
