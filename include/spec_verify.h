@@ -527,7 +527,10 @@ spec_status spec_cache_destroy(spec_cache_ctx* ctx);
 /* Quantise and store: token j < L_i of request i goes to position
  * cache_len_i + j, L_i = block_len_i clamped to [0, T] (block_len NULL => T).
  * k, v: [B, T, heads_kv, head_dim] rows of `dtype` (SPEC_F32, SPEC_BF16,
- * SPEC_F16).  cache_len [B] int32.  Every other position keeps its bits. */
+ * SPEC_F16).  cache_len [B] int32.  Every other position keeps its bits.
+ * ceil((T + 15) / 16) * heads_kv * head_dim / 32 has to be below 2^27 (8 heads of
+ * 128: 67 million tokens a request), and so the read's ceil((T + 15) / 16) *
+ * heads_kv * 2; else SPEC_ERR_INVALID_ARG and nothing is done. */
 spec_status spec_cache_write(spec_cache_ctx* ctx, const spec_cache_pages* cache,
                              const spec_cache_rows* k, const spec_cache_rows* v, spec_dtype dtype,
                              const int32_t* cache_len, const int32_t* block_len, int B, int T,

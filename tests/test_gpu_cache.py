@@ -958,3 +958,16 @@ def test_write_saturates_up_to_the_largest_finite_quotient(dev, dtype):
         k, _ = c.read(pages, on(dev, table), rows=16, dtype=torch.float32, k_scale=gd)
     assert bool(k[0, 0, :, 7].isfinite().all()) and bool(k[0, 15, :, 7].isnan().all())
     assert bool(k[0, :, :, 32:48].isfinite().all())
+
+
+def test_a_write_past_the_largest_grid_is_refused(dev):
+    c = binding.BlockCache(dev, 1024, 1024, 256, 16, max_batch=1)
+    k = torch.zeros((1, 1, 1024, 256), dtype=torch.bfloat16, device=dev).expand(1, 262144, 1024, 256)
+    pages = c.alloc(1)
+    with pytest.raises(binding.SpecVerifyError) as e:
+        c.write(k, k, pages, torch.full((1, 1), -1, dtype=torch.int32, device=dev), on(dev, [0]))
+    assert e.value.status == binding.SPEC_ERR_INVALID_ARG
+    status = torch.zeros(1, dtype=torch.int32, device=dev)
+    few = k[:, :262113]  # the largest that fits: skipped, since the table does not hold it
+    c.write(few, few, pages, torch.full((1, 1), -1, dtype=torch.int32, device=dev), on(dev, [0]), status=status)
+    assert status.tolist() == [binding.DEV_BAD_LENGTH]
