@@ -1544,11 +1544,12 @@ __global__ void __launch_bounds__(join_threads(D)) k_attend_join(const __grid_co
 #pragma unroll
     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
-      inv[warp] = l == 0.0f ? 0.0f : __frcp_rn(l);
+      // the functions of the rows that are not cut (attend_epilogue), to the bit
+      inv[warp] = l == 0.0f ? 0.0f : rcp(l);
       if (p.lse && !gone) {
         const int row = row0 + r, j = of_group(p, row), hq = h * p.group + row - j * p.group;
         p.lse[(static_cast<int64_t>(i) * p.T + j) * p.heads_q + hq] =
-            l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+            l == 0.0f ? -INFINITY : (m + lg2(l)) * 0.6931471805599453f;
       }
     }
   }

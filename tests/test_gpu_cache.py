@@ -971,3 +971,29 @@ def test_a_write_past_the_largest_grid_is_refused(dev):
     few = k[:, :262113]  # the largest that fits: skipped, since the table does not hold it
     c.write(few, few, pages, torch.full((1, 1), -1, dtype=torch.int32, device=dev), on(dev, [0]), status=status)
     assert status.tolist() == [binding.DEV_BAD_LENGTH]
+
+
+@pytest.mark.parametrize("d,hq,n", [(64, 4, 700), (128, 4, 1000), (128, 40, 650), (256, 4, 517), (256, 24, 900)])
+def test_a_cut_row_has_the_lse_of_a_whole_one_where_its_sums_are_exact(dev, d, hq, n):
+    """Equal scores and values of whole numbers: every sum is exact in any order, so a request alone (cut into
+    the CTAs' shares) and its copies in a crowd (some cut, most whole) give the same lse, bit for bit.  (Outputs
+    need not: a whole row's two sums are scaled by 1 / l before they are added, a cut one's behind it, which is
+    one rounding of fp32 apart, or a step of the result where that passes a border: 2^-7 of a bf16.)"""
+    copies, page, T = 300, 64, 1
+    width = (n + T + page - 1) // page
+    table = torch.randperm(width, generator=torch.Generator().manual_seed(d)).to(torch.int32).view(1, width).to(dev)
+    length = torch.tensor([n], dtype=torch.int32, device=dev)
+    g = torch.Generator(device=dev).manual_seed(3)
+    k = torch.randn((1, n + T, 1, d), generator=g, device=dev)
+    v = torch.randint(-2, 3, (1, n + T, 1, d), generator=g, device=dev) * 2.0
+    v[..., 0::16] = 6.0  # the scale of each group is 1
+    with binding.BlockCache(dev, hq, 1, d, page, max_batch=copies) as cache:
+        pages = cache.alloc(width)
+        cache.write(k, v, pages, table, torch.zeros_like(length))
+        q = torch.zeros((copies, T, hq, d), dtype=torch.bfloat16, device=dev)
+        one, one_lse = cache.attend(q[:1], pages, table, length)
+        out, lse = cache.attend(q, pages, table.repeat(copies, 1), length.repeat(copies))
+        assert torch.equal(lse, one_lse.expand_as(lse))
+        off = (out.float() - one.float()).abs() - one.float().abs() * 2.0 ** -7
+        assert float(off.max()) <= 6 * 2.0 ** -22  # of the largest value, where the sum is near 0
+        assert cache.errors() == 0
