@@ -390,7 +390,7 @@ __device__ __forceinline__ void group_sync(int id) {
 // ------------------------------------------------------------- work shares --
 // A request's units, in order: head, row tile, token tile.  A segment (one row
 // tile of one head) counts p.seg_units more than its tiles: what its first
-// references, its Q and its output cost beside them.  Equal shares of bare tiles
+// references, its Q and its output cost beside them (chosen in cache.cu).  Equal shares of bare tiles
 // left the CTAs with many short segments 29% behind the mean (256 requests of
 // 64..4096 positions).
 __device__ __forceinline__ bool attend_len(const AttendParams& p, int i, int64_t& n, int& L) {

@@ -264,9 +264,17 @@ spec_status spec_cache_attend(spec_cache_ctx* c, const spec_cache_pages* cache,
   const int64_t tiles = (rows + max_rows(c->head_dim) - 1) / max_rows(c->head_dim);
   p.rp = static_cast<int>((rows + tiles - 1) / tiles);
   if (rows > INT_MAX - 64) return SPEC_ERR_INVALID_ARG;
-  // 3 against 6: decoding 64 requests (8 rows) 97 and 100 us, verifying 256 (24
-  // rows) 283 and 268 us
-  p.seg_units = p.rp <= 16 ? 3 : 6;
+  // One softmax thread has 8 or at least 16 rows.  3 against 6 tiles, 96 requests of
+  // 64..4096 positions (width 256: ..2048), us, width 64 / 128 / 256:
+  //    8 rows   74.9 : 78.4   74.1 : 76.7   40.3 : 44.1
+  //   12 rows   91.7 : 84.5   89.3 : 82.9   51.6 : 48.7
+  //   16 rows   97.5 : 85.7   89.4 : 83.3   52.8 : 49.2
+  //   24 rows    115 : 93.1    106 : 91.3   62.3 : 53.4
+  //   32 rows    141 : 115     128 : 114    72.6 : 60.4
+  //   64 rows    205 : 168     191 : 167
+  // 2, 4 and 8 are no better, but for contexts of 16..1000: 6 gains 2 us at 8 rows
+  // too (37.8 : 35.3), and 8 some at 48 rows and more (width 128, 6 : 8, 72.7 : 65.4).
+  p.seg_units = p.rp <= 8 ? 3 : 6;
   p.part_o = c->part_o;
   p.part_l = c->part_l;
   p.cuts = c->cuts;
