@@ -267,13 +267,14 @@ def measured_peaks():
         return None
 
 
-# The device sources each profiled kernel is compiled from (host code, the C
-# header and the other kernels' files do not change its machine code).
+# The device sources each profiled kernel is compiled from (the C header and the
+# other kernels' files do not change its machine code), and the host code that
+# chooses the attention's instance, row tiles and shares: they decide what it reads.
 KERNEL_SOURCES = {
     "k_engine": ["common.cuh", "conf.cuh", "engine.cuh", "fp64.cuh", "philox.cuh", "refine.cuh",
                  "sample.cuh", "stage.cuh", "stats.cuh"],
     "k_lmhead": ["common.cuh", "philox.cuh", "ptx.cuh", "stage.cuh", "stats.cuh", "lmhead.cuh"],
-    "k_attend": ["ptx.cuh", "cache.cuh", "attend.cuh"],
+    "k_attend": ["ptx.cuh", "cache.cuh", "attend.cuh", "attend_launch.cuh", "cache.cu", "host.cuh"],
 }
 
 

@@ -55,3 +55,8 @@ def test_superseded_summaries_are_not_read_as_the_present_kernels():
                 kept += 1
                 assert bench.profiled_traffic(kernel, name[len(kernel) + 1:]) is None, name
     assert kept > 0
+
+
+def test_the_attention_hash_covers_the_code_that_chooses_its_tiles():
+    """Row tiles, shares and instances are chosen on the host; they decide how often a page is read."""
+    assert {"cache.cu", "attend_launch.cuh"} <= set(bench.KERNEL_SOURCES["k_attend"])
