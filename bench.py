@@ -23,8 +23,9 @@ sampled rows and the sample.  Its roofline is the tensor-core one.
 ``--workload attend`` times the part of a step that comes before the head: the
 blocks' keys and values written into the 4-bit block cache and the blocks'
 attention over it (B=256, 6 tokens each, contexts of 64..4096 positions, 32 query
-and 8 key/value heads of 128).  Its roofline is the HBM one, its reference arm the
-same attention in fp64 torch on the host cores.
+and 8 key/value heads of 128).  Its roofline is the HBM one.  Its reference arm is a
+dense attention of one request in fp64 torch on the host cores, without the 4-bit
+format: it tells what the definition costs there, and is no ratio to quote.
 
 With N > 1 (launched by torch.distributed.run) every rank verifies its own
 batch of the same shape (weak scaling, no collective on the data path); the
@@ -906,6 +907,10 @@ def run_lmhead_reference(args):
 ATTEND_METRIC = "query positions/s of the 4-bit block cache's write + attention, B=256 T=6 32/8 heads of 128"
 
 
+ATTEND_DTYPE = "bf16 rows; cache e2m1 with e4m3 scales"
+ATTEND_ORACLE = "dense fp64 torch attention of request 0 alone, without the 4-bit format and its write"
+
+
 def attend_config(w, n):
     return {"model": "attention of a verification step: %s" % w["name"], "global_batch": w["B"] * n,
             "seq_len": w["T"], "positions_max": int(max(w["lens"])), "parallelism": "dp%d" % n,
@@ -945,7 +950,7 @@ def run_attend(args):
                 "impl": "reference", "metric": ATTEND_METRIC, "value": value, "unit": UNIT, "n_gpus": args.gpus,
                 "steps": args.steps, "warmup": 0, "ms_per_step": 1e3 * sum(t for t, _ in runs) / len(runs),
                 "higher_is_better": True, "scaling": "weak", "vs_baseline": None, "dtype": "f64",
-                "data": "synthetic", "config": attend_config(w, 1),
+                "data": "synthetic", "config": dict(attend_config(w, 1), sample=ATTEND_ORACLE),
                 "e2e": {"value": value, "unit": UNIT, "h2d_bytes_per_step": 0, "d2h_bytes_per_step": 0}}),
                 flush=True)
         return
@@ -1018,7 +1023,7 @@ def run_attend(args):
     cpu = None
     if world == 1 and not args.no_cpu_baseline:
         dt, pos = attend_oracle_sample(w)
-        cpu = {"value": pos / dt, "unit": UNIT, "cores": torch.get_num_threads(), "kind": "fp64 torch",
+        cpu = {"value": pos / dt, "unit": UNIT, "cores": torch.get_num_threads(), "kind": ATTEND_ORACLE,
                "sample": "request 0 of %d, %d positions" % (B, w["lens"][0])}
     peaks = measured_peaks()
     peak = float(peaks["hbm_gbs"]) if peaks and peaks.get("hbm_gbs") else FALLBACK_HBM_GBS
@@ -1028,9 +1033,9 @@ def run_attend(args):
     line = {
         "metric": ATTEND_METRIC, "value": positions * world / (ms / 1e3), "unit": UNIT, "n_gpus": world,
         "steps": args.steps, "warmup": max(args.warmup, 3), "ms_per_step": ms, "higher_is_better": True,
-        "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+        "scaling": "weak", "vs_baseline": None, "dtype": ATTEND_DTYPE, "data": "synthetic",
         "config": attend_config(w, world),
-        "roofline": {"bound": "memory", "kernel": "k_attend (with k_cache_write, k_attend_join)",
+        "roofline": {"bound": "memory", "kernel": "k_cache_write, k_attend and k_attend_join",
                      "achieved": achieved, "peak": peak, "unit": "GB/s", "frac": achieved / peak,
                      "bytes_per_step": nbytes, "traffic": profiled_traffic("k_attend", "attend")},
         "timed_blocks": {"blocks": len(block_ms), "steps_per_block": args.steps,
