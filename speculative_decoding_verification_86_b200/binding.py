@@ -1060,7 +1060,8 @@ class BlockCache:
         st = self._lib.spec_cache_attend(
             self._h, pg, qr, _CACHE_DTYPES[q.dtype],
             self._ints(cache_len, B, "cache_len"), self._ints(block_len, B, "block_len"), B, T,
-            float(self.head_dim ** -0.5 if scale is None else scale), int(bool(causal)), int(window),
+            float(self.head_dim ** -0.5 if scale is None else scale), int(bool(causal)),
+            max(-1, min(int(window), 2 ** 31 - 1)),  # no position is that far away
             outr, lse_ptr,
             self._ints(status, B, "status"), _stream_number(stream, self.device))
         _check(st, "spec_cache_attend")

@@ -997,3 +997,50 @@ def test_a_cut_row_has_the_lse_of_a_whole_one_where_its_sums_are_exact(dev, d, h
         off = (out.float() - one.float()).abs() - one.float().abs() * 2.0 ** -7
         assert float(off.max()) <= 6 * 2.0 ** -22  # of the largest value, where the sum is near 0
         assert cache.errors() == 0
+
+
+def test_windows_wider_than_a_32_bit_number(dev):
+    """A window that no position leaves is no window, whatever its size."""
+    s = make(dev, B=2, T=3, heads_q=4, heads_kv=2, d=64, page=16, lens=[200, 7], seed=3)
+    a = device_args(s)
+    pages = torch.from_numpy(s["raw"]).to(dev)
+    s["cache"].write(s["k"].to(dev), s["v"].to(dev), pages, **a)
+    want, lse = s["cache"].attend(s["q"].to(dev), pages, **a)
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5, 2 ** 63 - 1):
+        out, l2 = s["cache"].attend(s["q"].to(dev), pages, window=window, **a)
+        assert torch.equal(out, want) and torch.equal(lse, l2), window
+    for window in (-1, -2 ** 32 + 5):
+        with pytest.raises(binding.SpecVerifyError):
+            s["cache"].attend(s["q"].to(dev), pages, window=window, **a)
+
+
+def test_the_longest_block(dev):
+    """65535 query tokens (a row's number and head share 32 bits); one more is refused."""
+    T, d, hq, page = 65535, 64, 2, 256
+    g = torch.Generator(device=dev).manual_seed(1)
+    width = (T + page) // page + 1
+    with binding.BlockCache(dev, hq, 1, d, page, max_batch=1) as cache:
+        pages = cache.alloc(width)
+        table = torch.arange(width, dtype=torch.int32, device=dev).view(1, width)
+        n = torch.full((1,), 3, dtype=torch.int32, device=dev)
+        k = torch.randn((1, T + 3, 1, d), generator=g, device=dev, dtype=torch.bfloat16)
+        v = torch.randn((1, T + 3, 1, d), generator=g, device=dev, dtype=torch.bfloat16)
+        q = torch.randn((1, T, hq, d), generator=g, device=dev, dtype=torch.bfloat16)
+        cache.write(k, v, pages, table, torch.zeros_like(n))
+        kk, vv = cache.read(pages, table, rows=T + 3, dtype=torch.float32)
+        out, lse = cache.attend(q, pages, table, n)
+        for j in (0, 1, 125, 4095, 32768, 40000, T - 2, T - 1):
+            x = q[0, j].double() @ kk[0, :j + 4, 0].double().T / 8
+            p = torch.softmax(x, -1)
+            want, a = p @ vv[0, :j + 4, 0].double(), p @ vv[0, :j + 4, 0].double().abs()
+            size = (q[0, j].double().abs() @ kk[0, :j + 4, 0].double().abs().T).amax(-1) / 8
+            z = torch.logsumexp(x, -1)
+            # sums are 128 tokens deep in a tile and 512 tiles deep
+            tol, tol_lse = ref.attend_bounds(want.cpu().numpy(), z.cpu().numpy(), a.cpu().numpy(), size.cpu().numpy(),
+                                             800, d, q.dtype)
+            assert np.all(np.abs(ref.to_np(out[0, j]) - want.cpu().numpy()) <= tol), j
+            assert np.all(np.abs(ref.to_np(lse[0, j]) - z.cpu().numpy()) <= tol_lse), j
+        assert cache.errors() == 0
+        with pytest.raises(binding.SpecVerifyError) as e:
+            cache.attend(torch.zeros((1, T + 1, hq, d), dtype=torch.bfloat16, device=dev), pages, table, n)
+        assert e.value.status == binding.SPEC_ERR_INVALID_ARG
