@@ -33,14 +33,21 @@
 // freed.  The error word and SPEC_DEV_INTERNAL of the batch's requests are raised,
 // and rows that such a CTA has a part of are not joined.
 //
-// What bounds it: instruction issue.  A tile of 128 tokens (18 KB at D = 128) costs
-// its SM 3000 (8 query rows) to 4000 (24) warp instructions, about half of them to
-// decode the codes, at 2.5 of 4 a cycle; the tensor pipe is busy 16 % of the time.
+// What bounds it: no unit (24 rows: 63 % of the issue slots, ALU 49 %, tensor 16 %,
+// half of the copy bandwidth) but the roles' own serial paths, which share the issue
+// slots.  A tile of 128 tokens takes 1270 cycles at 8 query rows, 1570 at 24, 2450 at
+// 48 (D = 128) and costs 3000 to 4000 warp instructions, about half of them to decode
+// the codes.  With clocks around one role's waits at a time: above 32 rows the softmax
+// works 2250 of the 2450 cycles and waits for nothing; up to 32 rows the warp that
+// issues the products sets the pace (clocks around its five waits a tile lengthen the
+// call by half, around the two of a decoder by a tenth), and K and V decoders, some
+// 1000 and 1100 cycles a tile, follow closely; at D = 256 and 8 rows the decoders do
+// (1700 and 1800 of 2300; one K buffer).
 // Measured: 256 requests of 64..4096 positions, 24 rows each (32 / 8 heads of 128):
-// 218 us, 2.9 TB/s, 0.45 of the copy bandwidth; 64 requests of 500..8192 positions,
-// 8 rows: 94 us, 3.2 TB/s; one of 100,003 positions: 46 us; one of 700: 12 us, of
-// which 3 us are the plan, 3 us the join and the rest the chain of memory round
-// trips and one cold pass through every role's code.
+// 216 us (225 on another B200), 2.9 TB/s, 0.45 of the copy bandwidth; 64 requests of
+// 500..8192 positions, 8 rows: 93 us, 3.3 TB/s; one of 100,003 positions: 46 us; one
+// of 700: 12.3 us, of which 3 us are the plan, 3 us the join and the rest the chain of
+// memory round trips and one cold pass through every role's code.
 #pragma once
 #include <climits>
 

@@ -344,10 +344,11 @@ __device__ __forceinline__ void wait_for_stream() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Issue bounds it: 70 % of the slots, the ALU pipe 55 %, some 400 instructions for a
-// warp's 2 KB (12 or 14 blocks a SM instead of 10 change nothing).  4 x 8191 tokens,
+// Nearest to a limit is issue: 70 % of the slots, the ALU pipe 55 %, some 400 instructions
+// for a warp's 2 KB (12 or 14 blocks a SM instead of 10 change nothing).  4 x 8191 tokens,
 // 8 heads of 128, fp16: 43 us, 4.0 TB/s (0.61 of the copy bandwidth); a block of 6
-// tokens 8 us from cold memory, four dependent reads.
+// tokens 8 us from cold memory, four dependent reads.  Back to back in a graph (part
+// of the rows in the L2) 36 us at any width, 46 us from fp32; 256 blocks of 6: 8.5 us.
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
   wait_for_stream();
@@ -454,7 +455,8 @@ __global__ void __launch_bounds__(kMoveThreads) k_cache_write(CacheMove p) {
 }
 
 // Bound by the memory it writes: 12 requests of 1000..16384 positions, 8 heads of 128,
-// to fp16: 107 us, 5.5 TB/s (0.85 of the copy bandwidth).
+// to fp16: 113 us, 5.2 TB/s (0.80 of the copy bandwidth), 101 us back to back in a
+// graph (0.90); to fp32 180 us (0.90).
 template <int D, typename T>
 __global__ void __launch_bounds__(kMoveThreads) k_cache_read(CacheMove p) {
   wait_for_stream();
