@@ -473,7 +473,7 @@ struct AttendShares {
 // 180 GB.  Looking at the clock here, or a limit that the compiler does not know, cost
 // a sixth to a third of the kernel's time (256 requests 215 -> 250..290 us): this
 // stands at some thirty places.  A role that gives up returns false, and the roles
-// that wait for it give up in their turn.
+// that wait for it give up in their turn.  The tests build with 1 and run that.
 #ifndef SV_WAIT_TRIES
 #define SV_WAIT_TRIES (1u << 22)
 #endif
